@@ -51,7 +51,7 @@
  * are stored XOR-swizzled: logical chunk c of slot s sits at chunk (c ^ (s & 7)).
  * This is the 128-byte-swizzled operand layout the tensor cores read, so a page
  * block is copied into shared memory as-is. Every slot of a held page is either a
- * valid token or zero.
+ * valid token or zero (in a token stream's last page: or a dropped token).
  */
 #ifndef PKV_H
 #define PKV_H
@@ -75,7 +75,7 @@ typedef enum {
   PKV_ERR_DEVICE = 6   /* a kernel recorded an inconsistency in the error word   */
 } pkv_status;
 
-enum { PKV_MODE_FRAME = 0, PKV_MODE_CHUNKED = 1 };
+enum { PKV_MODE_FRAME = 0, PKV_MODE_CHUNKED = 1 };   /* token streams: pkv_stream_open_tokens */
 
 /* Per-stream configuration. Fields of the other mode are ignored. */
 typedef struct {
@@ -434,6 +434,93 @@ pkv_status pkv_attend_batched(pkv_t h, const void* q, const int* q_off, const in
 pkv_status pkv_attend_noalloc(pkv_t h, const void* q, int n_q, int stream_id, int layer, void* out,
                               float sm_scale, void* cuda_stream);
 
+/* ------------------------------------------------------------- token streams
+ * A language model's decoder over the same pool: a token stream grows by any number
+ * of tokens at a time, and its queries see keys causally (the frame and chunk
+ * calls attend bidirectionally). Position j of the stream is stored in slot
+ * j % page_size of the stream's page j / page_size, in bf16 or E4M3 rows as the
+ * cache holds them, with as many page sets as the cache has layers. Several streams
+ * are served by one call: a batch names n streams (1 .. 256, each once), and the
+ * rows of all of them lie back to back in one tensor, rows row_off[i] ..
+ * row_off[i + 1] - 1 being stream stream_ids[i]'s (n + 1 host ints that start at 0
+ * and do not fall; a stream may have no row). Values must be finite.
+ * Rows may be strided: k_stride, v_stride and q_stride are the elements from one
+ * token's row to the next one's (0: contiguous), multiples of 8, so that q, k and v
+ * may be parts of one tensor. The other calls that take a stream (close, reset,
+ * rollback, evict, visible page table, export) work on token streams; the frame
+ * and chunk calls refuse them with STATE. Every call below refuses a current device
+ * other than the handle's with INVALID. */
+
+/* Open a token stream of at most max_tokens tokens (dropped tokens not counted).
+ * window > 0: pkv_evict_window frees the pages whose tokens no later query sees
+ * with that window, except those that hold the first `sinks` tokens; such streams
+ * are for attention with a window of at most that size on every layer. window = 0
+ * keeps every token. Allocates the page list (4 bytes per page of max_tokens) and,
+ * once per handle, 64 MiB of split-KV scratch, so that no token call allocates.
+ * Errors: INVALID (null argument, max_tokens outside 1 .. 2^28, negative window or
+ * sinks, sinks above max_tokens or without a window), OOM (max_streams already
+ * open), CUDA (the allocation failed). */
+pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks, int* stream_id);
+
+/* Append each stream's rows of k and v (device bf16 [row_off[n]][heads][64], rows
+ * strided) behind its tokens. layer 0 pops the pages that they need, in the order
+ * of the batch, and counts the tokens; layer > 0 writes the same slots of that
+ * layer's page set and must bring the rows of the stream's last append on layer 0.
+ * On an E4M3 cache rows are quantised as pkv_create_fp8 says. Slots behind the
+ * last token of a page that the call opens are zeroed; a dropped token's row stays
+ * until its slot is written again.
+ * Errors: INVALID (shape, stride, layer, a stream twice or past its max_tokens, a
+ * null or unaligned pointer), OOM (too few free pages), STATE (not a token stream;
+ * layer > 0 without an append on layer 0 since the last drop, rollback or evict). */
+pkv_status pkv_append_tokens(pkv_t h, int n, const int* stream_ids, const int* row_off, int layer,
+                             const void* k, const void* v, long long k_stride, long long v_stride,
+                             void* cuda_stream);
+
+/* Drop each stream's last counts[i] tokens (host ints; drafted tokens that were
+ * not accepted). Pages left empty go back on the free stack, the last stream's
+ * first, so that dropping a whole append restores the stack.
+ * pkv_rollback_last_frame on a token stream drops its last append.
+ * Errors: INVALID (a count outside 0 .. the stream's tokens, a stream twice), STATE
+ * (not a token stream; what the stream's window would see from before the dropped
+ * tokens is evicted). */
+pkv_status pkv_drop_tokens(pkv_t h, int n, const int* stream_ids, const int* counts, void* cuda_stream);
+
+/* Read rows back: stream i's positions pos0[i] .. (row_off[i + 1] - row_off[i] of
+ * them; pos0 NULL: its last ones) into k_out and v_out, device bf16
+ * [row_off[n]][heads][64], contiguous. bf16 pages return the appended bits, E4M3
+ * pages decode(code) * 2^e, which is exact in bf16.
+ * Errors: INVALID (shape, layer, positions that the stream does not have, a null
+ * or unaligned pointer), STATE (not a token stream; evicted positions). */
+pkv_status pkv_read_tokens(pkv_t h, int n, const int* stream_ids, const int* pos0, const int* row_off,
+                           int layer, void* k_out, void* v_out, void* cuda_stream);
+
+/* Causal attention of each stream's last tokens over its keys, themselves included.
+ * Stream i's rows are its positions p = len - rows .. len - 1, with q_heads query
+ * heads, a multiple (up to 128) of the cache's; query head g reads KV head
+ * g / (q_heads / heads):
+ *   out[p][g] = softmax over the visible j of (sm_scale * q[p][g] . k[j]) v[j],
+ *   visible: j <= p, and with window > 0 also (j > p - window or j < sinks),
+ * so a window holds the query's own token and the window - 1 before it, and the
+ * stream's first `sinks` tokens stay visible beside it.
+ * q: device bf16 [row_off[n]][q_heads][64], rows q_stride apart; out: the same,
+ * contiguous. fp32 accumulation and softmax; the probabilities are rounded to bf16
+ * (bf16 pages) or f16 (E4M3 pages, q rounded to f16 as well) for the second
+ * product. sm_scale <= 0 means 1 / sqrt(64). Results depend on the batch only by
+ * rounding (the split of the keys is chosen for the whole call) and are the same
+ * bits for the same call. The handle's scratch is shared by its calls: order them
+ * on one CUDA stream.
+ * Errors: INVALID (shape, stride, layer, q_heads, negative window or sinks, sinks
+ * without a window, a null or unaligned pointer), STATE (not a token stream; more
+ * rows than tokens; keys that the rows see are evicted). */
+pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
+                             const int* stream_ids, int n, int layer, void* out, int window, int sinks,
+                             float sm_scale, void* cuda_stream);
+
+/* A token stream's tokens, and its evicted positions evicted_from ..
+ * evicted_to - 1 (0, 0: none); each pointer may be NULL.
+ * Errors: INVALID (the stream is not open), STATE (not a token stream). */
+pkv_status pkv_token_info(pkv_t h, int stream_id, int* n_tokens, int* evicted_from, int* evicted_to);
+
 /* Wait for `cuda_stream` and report the device error word (PKV_ERR_DEVICE) or a
  * pending CUDA error (PKV_ERR_CUDA). */
 pkv_status pkv_sync(pkv_t h, void* cuda_stream);
@@ -449,7 +536,9 @@ pkv_status pkv_free_pages(pkv_t h, int* n_free);
  *   [0] free-stack depth F, [1..F] free stack bottom to top,
  *   then the stream's visible table: n, idx[0..n), len[0..n),
  *   then mode-specific counters: frame mode {n_scale, n_window, n_special, sp_len,
- *   kept, pending}; chunked mode {n_chunks, open, pending, tokens of each chunk}.
+ *   kept, pending}; chunked mode {n_chunks, open, pending, tokens of each chunk};
+ *   token streams {tokens, live pages before the evicted ones, live pages behind
+ *   them, list entry of the first of those, pending}.
  * cap_words is the capacity of host_buf; *used_words receives the count.
  * Errors: INVALID (stream not open, null pointer, cap_words too small), CUDA. */
 pkv_status pkv_export_state(pkv_t h, int stream_id, int32_t* host_buf, size_t cap_words,

@@ -62,6 +62,16 @@ SIGNATURES = {
                                         ctypes.POINTER(c_void_p), ctypes.POINTER(c_void_p),
                                         ctypes.POINTER(c_void_p), c_int, c_int, c_int, c_int,
                                         c_void_p, c_float, ctypes.POINTER(c_void_p), c_void_p]),
+    "pkv_stream_open_tokens": (c_int, [c_void_p, c_int, c_int, c_int, ctypes.POINTER(c_int)]),
+    "pkv_append_tokens": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                  ctypes.c_longlong, ctypes.c_longlong, c_void_p]),
+    "pkv_drop_tokens": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
+    "pkv_read_tokens": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p,
+                                c_void_p, c_void_p]),
+    "pkv_attend_tokens": (c_int, [c_void_p, c_void_p, c_int, ctypes.c_longlong, c_void_p, c_void_p,
+                                  c_int, c_int, c_void_p, c_int, c_int, c_float, c_void_p]),
+    "pkv_token_info": (c_int, [c_void_p, c_int, ctypes.POINTER(c_int), ctypes.POINTER(c_int),
+                               ctypes.POINTER(c_int)]),
     "pkv_sync": (c_int, [c_void_p, c_void_p]),
     "pkv_visible_count": (c_int, [c_void_p, c_int, ctypes.POINTER(c_int), ctypes.POINTER(c_int)]),
     "pkv_free_pages": (c_int, [c_void_p, ctypes.POINTER(c_int)]),

@@ -37,6 +37,29 @@ def chunked_stream_cfg(chunk_size, sliding_window_num, tokens_per_frame):
                      tokens_per_frame)
 
 
+class TokenBatch:
+    """The streams of a token call and how many rows each has, for every layer's calls
+    of a step (PagedKVCache.token_batch)."""
+
+    def __init__(self, sids, counts):
+        sids, counts = [int(s) for s in sids], [int(c) for c in counts]
+        if len(sids) != len(counts):
+            raise ValueError("one count per stream")
+        if any(c < 0 for c in counts):
+            raise ValueError("counts must not be negative")
+        n = len(sids)
+        off = [0]
+        for c in counts:
+            off.append(off[-1] + c)
+        if off[-1] >= 2 ** 31:
+            raise ValueError("too many rows")
+        self.n, self.rows = n, off[-1]
+        # host arrays that the calls read (kept alive with the batch), and their addresses
+        self._ids, self._counts, self._off = (ctypes.c_int * n)(*sids), (ctypes.c_int * n)(*counts), \
+            (ctypes.c_int * (n + 1))(*off)
+        self.sids, self.counts, self.row_off = map(ctypes.addressof, (self._ids, self._counts, self._off))
+
+
 class PagedKVCache:
     """A page pool (per layer) with its free list, shared by up to max_streams streams."""
 
@@ -50,6 +73,7 @@ class PagedKVCache:
         create = self.lib.pkv_create_fp8 if fp8 else self.lib.pkv_create_ex
         check(create(pool_pages, page_size, heads, head_dim, layers, max_streams, ctypes.byref(h)), None)
         self.h = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def close(self):
         if self.h is not None and self.h.value:
@@ -281,6 +305,91 @@ class PagedKVCache:
                                                 _stream_ptr(stream)))
         return out
 
+    # -------------------------------------------------------- token streams
+    def open_token_stream(self, max_tokens, window=0, sinks=0):
+        """pkv_stream_open_tokens: a causal stream of up to max_tokens tokens; with a
+        window, evict_window(sid) frees what no later query of such a window sees
+        (the first `sinks` tokens' pages stay)."""
+        sid = ctypes.c_int(-1)
+        self._check(self.lib.pkv_stream_open_tokens(self.h, max_tokens, window, sinks, ctypes.byref(sid)))
+        return sid.value
+
+    def token_batch(self, sids, counts):
+        """The streams of the following token calls, and each one's rows in them."""
+        return TokenBatch(sids, counts)
+
+    def _rows(self, t, name, batch, heads=None):
+        """(address, row stride) of a [rows][heads][64] bf16 tensor on the cache's
+        device whose rows are contiguous and any multiple of 8 elements apart."""
+        if t.dtype != torch.bfloat16 or t.device != self.device:
+            raise ValueError(f"{name} must be a bf16 tensor on {self.device}")
+        shape = t.shape
+        if len(shape) != 3 or shape[0] != batch.rows or shape[2] != self.head_dim or \
+                (heads is not None and shape[1] != heads):
+            raise ValueError(f"{name} must be [{batch.rows}][{heads or 'q_heads'}][{self.head_dim}], "
+                             f"got {list(shape)}")
+        a, b, c = t.stride()
+        row = shape[1] * self.head_dim
+        if (c != 1 or (b != self.head_dim and shape[1] > 1)) and batch.rows > 0:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        if batch.rows > 1 and a < row:
+            raise ValueError(f"the rows of {name} overlap")
+        return t.data_ptr(), a if batch.rows > 1 else row
+
+    def append_tokens(self, batch, k, v, layer=0, stream=None):
+        """pkv_append_tokens: k and v, [batch rows][heads][64], behind the batch's
+        streams' tokens."""
+        kp, ks = self._rows(k, "k", batch, self.heads)
+        vp, vs = self._rows(v, "v", batch, self.heads)
+        self._check(self.lib.pkv_append_tokens(self.h, batch.n, batch.sids, batch.row_off, layer, kp, vp,
+                                               ks, vs, _stream_ptr(stream)))
+
+    def drop_tokens(self, batch, stream=None):
+        """pkv_drop_tokens: the batch's rows, the last ones of its streams, go."""
+        self._check(self.lib.pkv_drop_tokens(self.h, batch.n, batch.sids, batch.counts, _stream_ptr(stream)))
+
+    def read_tokens(self, batch, pos0=None, layer=0, k_out=None, v_out=None, stream=None):
+        """pkv_read_tokens: (k, v) of each stream's positions pos0[i] .. (its rows of
+        the batch; pos0 None: its last ones), [batch rows][heads][64] bf16."""
+        shape = (batch.rows, self.heads, self.head_dim)
+        outs = []
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is None:
+                t = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            elif tuple(t.shape) != shape or t.dtype != torch.bfloat16 or t.device != self.device or \
+                    not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous bf16 tensor {list(shape)} on {self.device}")
+            outs.append(t)
+        first = None
+        if pos0 is not None:
+            if len(pos0) != batch.n:
+                raise ValueError("one first position per stream")
+            first = (ctypes.c_int * batch.n)(*pos0)
+        self._check(self.lib.pkv_read_tokens(self.h, batch.n, batch.sids, first, batch.row_off, layer,
+                                             outs[0].data_ptr(), outs[1].data_ptr(), _stream_ptr(stream)))
+        return outs[0], outs[1]
+
+    def attend_tokens(self, batch, q, layer=0, window=0, sinks=0, out=None, sm_scale=0.0, stream=None):
+        """pkv_attend_tokens: causal attention of the batch's rows (the last tokens of
+        its streams) with q, [batch rows][q_heads][64]; q_heads is a multiple of the
+        cache's heads. window, sinks: see pkv_attend_tokens."""
+        qp, qs = self._rows(q, "q", batch)
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+        elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != self.device or \
+                not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous bf16 tensor {list(q.shape)} on {self.device}")
+        self._check(self.lib.pkv_attend_tokens(self.h, qp, q.shape[1], qs, batch.row_off, batch.sids, batch.n,
+                                               layer, out.data_ptr(), window, sinks, sm_scale,
+                                               _stream_ptr(stream)))
+        return out
+
+    def token_info(self, sid):
+        """(tokens, first evicted position, first position behind them) of a token stream."""
+        n, a, b = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+        self._check(self.lib.pkv_token_info(self.h, sid, ctypes.byref(n), ctypes.byref(a), ctypes.byref(b)))
+        return n.value, a.value, b.value
+
     def sync(self, stream=None):
         self._check(self.lib.pkv_sync(self.h, _stream_ptr(stream)))
 
@@ -350,6 +459,6 @@ def synth_fill(out, seed, workload, stream_id, layer, frame0, tensor, token0=0, 
     return out
 
 
-__all__ = ["PagedKVCache", "PkvError", "frame_stream_cfg", "chunked_stream_cfg", "synth_fill",
+__all__ = ["PagedKVCache", "TokenBatch", "PkvError", "frame_stream_cfg", "chunked_stream_cfg", "synth_fill",
            "kernel_launches",
            "MODE_FRAME", "MODE_CHUNKED"]

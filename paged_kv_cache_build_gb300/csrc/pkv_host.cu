@@ -20,64 +20,9 @@
 #include <string>
 #include <vector>
 
-#include "../../include/pkv.h"
-#include "pkv_internal.cuh"
+#include "pkv_ctx.h"
 
 using namespace pkv;
-
-namespace {
-
-struct Stream {
-  bool open = false;
-  pkv_stream_cfg cfg{};
-  // device lists (one allocation)
-  int32_t* d_mem = nullptr;
-  int32_t* d_scale = nullptr;
-  int32_t* d_window = nullptr;
-  int32_t* d_special = nullptr;
-  int32_t* d_chunks = nullptr;   // [sliding_window_num][ppc]
-  int32_t* d_tbl_idx = nullptr;
-  int32_t* d_tbl_len = nullptr;
-  int tbl_cap = 0;
-  // frame-mode counters
-  int f_sp = 0;
-  int n_scale = 0, win_head = 0, win_count = 0, n_special = 0, sp_len = 0, kept = 0;
-  bool pending = false;
-  bool u_to_scale = false, u_new_sp = false;
-  int u_sp_before = 0, u_sp_off = 0, u_patch_pos = 0;
-  // chunked-mode counters (by ring slot)
-  int ppc = 0;
-  int c_head = 0, n_chunks = 0;
-  bool c_open = false;
-  int c_len[kMaxChunks] = {0}, c_pages[kMaxChunks] = {0}, c_frames[kMaxChunks] = {0};
-  int u_n_new = 0, u_old_pages = 0, u_pos0 = 0, u_slot = 0;
-  bool u_new_chunk = false;
-};
-
-}  // namespace
-
-struct pkv_ctx {
-  int P = 0, Ps = 0, H = 0, D = 0, L = 0, max_streams = 0;
-  long long page_elems = 0;      // bf16 elements per page (bf16 pools)
-  int fp8 = 0;                   // 1: E4M3 pages with row exponents
-  long long page_bytes = 0;      // bytes per page (either format)
-  uint16_t* d_pool = nullptr;
-  int32_t* d_free = nullptr;
-  int* d_err = nullptr;
-  int free_top = 0;
-  std::vector<Stream> streams;
-  float* d_scratch = nullptr;
-  size_t scratch_bytes = 0;
-  int scratch_allocs = 0;        // times the split-KV scratch was (re)allocated
-  int device = 0;                // the device current at pkv_create_ex
-  float* noalloc_scratch = nullptr;   // device address of the static scratch on `device`
-  void* d_select = nullptr;      // page skipping: query means, page estimates, kept list
-  float* d_km = nullptr;         // bf16 pages: mean key per (layer, page, head, d)
-  int* d_km_len = nullptr;       // its tags per (layer, page): valid length, or -1
-  int select_kept = -1;          // entries in that kept list (the last call's); -1: none yet
-  int num_sms = 0;
-  std::string last_error;
-};
 
 namespace {
 
@@ -88,6 +33,10 @@ constexpr size_t kStaticScratchBytes = size_t(16) << 20;   // 16 MiB
 // every handle. In host code this name is only a stand-in for the symbol: kernels
 // get the device address that pkv_create_ex resolves with cudaGetSymbolAddress.
 static __device__ __align__(256) float g_noalloc_scratch[kStaticScratchBytes / sizeof(float)];
+
+}  // namespace
+
+namespace pkv {
 
 pkv_status fail(pkv_t h, pkv_status st, const char* fmt, ...) {
   char buf[512];
@@ -104,21 +53,7 @@ pkv_status cuda_fail(pkv_t h, cudaError_t e, const char* what) {
   return fail(h, PKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-#define PKV_CUDA(h, call)                                  \
-  do {                                                     \
-    cudaError_t e_ = (call);                               \
-    if (e_ != cudaSuccess) return cuda_fail((h), e_, #call); \
-  } while (0)
-
-inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
-
-// Layer `layer`'s page set (a byte offset, so that it holds for either format).
-inline uint16_t* layer_base(pkv_t h, int layer) {
-  return reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(h->d_pool) +
-                                     (long long)layer * h->P * h->page_bytes);
-}
-
-inline PoolView pool_view(pkv_t h, int layer) {
+PoolView pool_view(pkv_t h, int layer) {
   PoolView pv;
   pv.base = layer_base(h, layer);
   pv.page_elems = h->page_elems;
@@ -139,7 +74,9 @@ pkv_status get_stream(pkv_t h, int sid, Stream** out) {
   return PKV_OK;
 }
 
-inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+}  // namespace pkv
+
+namespace {
 
 // Visible table size from the counters.
 void visible_counts(const pkv_ctx* h, const Stream& st, int* n_pages, int* n_tokens, int* last) {
@@ -150,6 +87,12 @@ void visible_counts(const pkv_ctx* h, const Stream& st, int* n_pages, int* n_tok
     *n_pages = np;
     *n_tokens = nt;
     *last = st.n_special > 0 ? st.sp_len : (np > 0 ? h->Ps : 0);
+  } else if (st.cfg.mode == kModeTokens) {
+    const TokenCounts& t = st.tok;
+    const int front = tok_live_front(t), back = tok_live_back(t);
+    *n_pages = front + back;
+    *last = t.n_pages > 0 ? t.len - (t.n_pages - 1) * h->Ps : 0;
+    *n_tokens = *n_pages > 0 ? (*n_pages - 1) * h->Ps + *last : 0;
   } else {
     int np = 0, nt = 0, lst = 0;
     for (int i = 0; i < st.n_chunks; ++i) {
@@ -185,6 +128,19 @@ TableArgs table_args(pkv_t h, Stream& st, int32_t* idx, int32_t* len, int32_t* o
     t.n_special = st.n_special;
     t.sp_full_len = st.f_sp * st.cfg.n_special;
     t.sp_last_len = st.sp_len;
+  } else if (st.cfg.mode == kModeTokens) {
+    // the sinks' pages and the live ones behind them, all full but the last
+    t.mode = PKV_MODE_FRAME;
+    t.special = st.d_pages;
+    t.n_special = tok_live_front(st.tok) + tok_live_back(st.tok);
+    t.sp_full_len = h->Ps;
+    t.sp_last_len = last;
+    if (st.tok.gap1 > st.tok.keep0 && tok_live_back(st.tok) > 0) {
+      t.scale = st.d_pages;
+      t.n_scale = tok_live_front(st.tok);
+      t.special = st.d_pages + st.tok.gap1;
+      t.n_special = tok_live_back(st.tok);
+    }
   } else {
     t.n_chunks = st.n_chunks;
     for (int i = 0; i < st.n_chunks; ++i) {
@@ -201,6 +157,10 @@ TableArgs table_args(pkv_t h, Stream& st, int32_t* idx, int32_t* len, int32_t* o
   t.err = h->d_err;
   return t;
 }
+
+}  // namespace
+
+namespace pkv {
 
 pkv_status push_pages(pkv_t h, const PushSegment* segs, int n_seg, cudaStream_t s) {
   int total = 0;
@@ -223,7 +183,7 @@ pkv_status push_pages(pkv_t h, const PushSegment* segs, int n_seg, cudaStream_t 
   return PKV_OK;
 }
 
-PushSegment seg(const int32_t* src, int start, int count, int step = 1, int ring = 0) {
+PushSegment seg(const int32_t* src, int start, int count, int step, int ring) {
   PushSegment g;
   g.src = src;
   g.start = start;
@@ -233,9 +193,7 @@ PushSegment seg(const int32_t* src, int start, int count, int step = 1, int ring
   return g;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-}  // namespace
+}  // namespace pkv
 
 extern "C" {
 
@@ -280,6 +238,7 @@ static pkv_status create_cache(int pool_pages, int page_size, int heads, int hea
   // FP8 pages: 64 code bytes and one exponent byte per row; bf16 pages: 128 bytes per row
   h->page_bytes = fp8 ? 2LL * heads * page_size * (head_dim + 1) : 2LL * h->page_elems;
   h->streams.resize(max_streams);
+  h->seen.assign(max_streams, 0u);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   h->device = dev;
@@ -357,7 +316,7 @@ pkv_status pkv_destroy(pkv_t h) {
 
 }  // extern "C"
 
-namespace {
+namespace pkv {
 
 pkv_status ensure_scratch(pkv_t h, size_t bytes) {
   if (bytes <= h->scratch_bytes) return PKV_OK;
@@ -370,6 +329,10 @@ pkv_status ensure_scratch(pkv_t h, size_t bytes) {
   h->scratch_allocs++;
   return PKV_OK;
 }
+
+}  // namespace pkv
+
+namespace {
 
 // Split-KV scratch that the attention calls of a stream with this configuration
 // need at their natural query count (a frame's n_patch + n_special rows, or a
@@ -473,6 +436,9 @@ static pkv_status free_stream_pages(pkv_t h, Stream* st, cudaStream_t s) {
     segs.push_back(seg(st->d_scale, 0, st->n_scale));
     segs.push_back(seg(st->d_window, st->win_head, st->win_count, 1, st->cfg.window));
     segs.push_back(seg(st->d_special, 0, st->n_special));
+  } else if (st->cfg.mode == kModeTokens) {
+    segs.push_back(seg(st->d_pages, 0, tok_live_front(st->tok)));
+    segs.push_back(seg(st->d_pages, st->tok.gap1, tok_live_back(st->tok)));
   } else {
     for (int i = 0; i < st->n_chunks; ++i) {
       const int slot = (st->c_head + i) % st->cfg.sliding_window_num;
@@ -496,6 +462,9 @@ static void clear_counters(Stream* st) {
   fresh.tbl_cap = st->tbl_cap;
   fresh.f_sp = st->f_sp;
   fresh.ppc = st->ppc;
+  fresh.d_pages = st->d_pages;
+  if (st->cfg.mode == kModeTokens)
+    tok_open(&fresh.tok, st->tok.page_size, st->tok.max_tokens, st->tok.window, st->tok.sinks);
   *st = fresh;
 }
 
@@ -705,8 +674,9 @@ pkv_status pkv_append_frame(pkv_t h, int sid, int layer, const void* k, const vo
 pkv_status pkv_rollback_last_frame(pkv_t h, int sid, void* cuda_stream) {
   Stream* st = nullptr;
   if (pkv_status r = get_stream(h, sid, &st)) return r;
-  if (!st->pending) return fail(h, PKV_ERR_STATE, "nothing to roll back");
   cudaStream_t s = as_stream(cuda_stream);
+  if (st->cfg.mode == kModeTokens) return token_rollback(h, st, s);
+  if (!st->pending) return fail(h, PKV_ERR_STATE, "nothing to roll back");
   if (st->cfg.mode == PKV_MODE_CHUNKED) {
     const int slot = st->u_slot;
     PushSegment g = seg(st->d_chunks + (long long)slot * st->ppc, st->u_old_pages + st->u_n_new - 1,
@@ -802,6 +772,7 @@ pkv_status pkv_evict_window(pkv_t h, int sid, void* cuda_stream) {
   if (pkv_status r = get_stream(h, sid, &st)) return r;
   cudaStream_t s = as_stream(cuda_stream);
   const pkv_stream_cfg& c = st->cfg;
+  if (c.mode == kModeTokens) return token_evict(h, st, s);
   if (c.mode == PKV_MODE_CHUNKED) {
     const int Wc = c.sliding_window_num;
     std::vector<PushSegment> segs;
@@ -1254,6 +1225,8 @@ pkv_status pkv_attend_batched(pkv_t h, const void* q, const int* q_off, const in
       if (sids[k] == sids[i]) return fail(h, PKV_ERR_INVALID, "stream %d listed twice", sids[i]);
     Stream* st = nullptr;
     if (pkv_status r = get_stream(h, sids[i], &st)) return r;
+    if (st->cfg.mode == kModeTokens)
+      return fail(h, PKV_ERR_STATE, "stream %d is a token stream: use pkv_attend_tokens", sids[i]);
     const int n_q = q_off[i + 1] - q_off[i];
     if (n_q < 1 || q_off[i + 1] > (1 << 20))
       return fail(h, PKV_ERR_INVALID, "stream %d: query rows %d..%d", sids[i], q_off[i], q_off[i + 1]);
@@ -1371,6 +1344,10 @@ pkv_status pkv_export_state(pkv_t h, int sid, int32_t* host_buf, size_t cap_word
   if (st->cfg.mode == PKV_MODE_FRAME) {
     int32_t w[6] = {st->n_scale, st->win_count, st->n_special, st->sp_len, st->kept, st->pending};
     buf.insert(buf.end(), w, w + 6);
+  } else if (st->cfg.mode == kModeTokens) {
+    const TokenCounts& t = st->tok;
+    int32_t w[5] = {t.len, tok_live_front(t), tok_live_back(t), t.gap1, t.pending};
+    buf.insert(buf.end(), w, w + 5);
   } else {
     buf.push_back(st->n_chunks);
     buf.push_back(st->c_open);
@@ -1476,6 +1453,8 @@ pkv_status pkv_attend_noalloc(pkv_t h, const void* q, int n_q, int sid, int laye
                               float sm_scale, void* cuda_stream) {
   Stream* st = nullptr;
   if (pkv_status r = get_stream(h, sid, &st)) return r;
+  if (st->cfg.mode == kModeTokens)
+    return fail(h, PKV_ERR_STATE, "stream %d is a token stream: use pkv_attend_tokens", sid);
   if (st->cfg.mode == PKV_MODE_CHUNKED) {
     if (!st->c_open) return fail(h, PKV_ERR_STATE, "no open chunk");
     const int cur = (st->c_head + st->n_chunks - 1) % st->cfg.sliding_window_num;
