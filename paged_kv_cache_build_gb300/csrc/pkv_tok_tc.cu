@@ -1,0 +1,513 @@
+// Causal attention of a token stream's last tokens over its pages on the
+// 5th-generation tensor cores (tcgen05 + TMEM): chunks of a prompt, where a KV head
+// has many query rows (tokens x query heads of the group).
+//
+//   out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),   s_j = log2(e) sm_scale q . k_j
+//
+// Bounds: at head_dim 64 a 128 x 64 tile of scores is 2 x 256 matrix-unit cycles of
+// 4096 multiply-adds, and 256 cycles of the SM's 32 exponentials a cycle, so the
+// softmax must run beside the products without a pause. What stalls it is latency:
+// S must come back from the matrix unit and P go to it. So a CTA runs four
+// independent pipelines ("lanes"), each 128 query rows with its own S and O in
+// TMEM, its own issuing thread and its own four softmax warps (a thread per row);
+// while one waits for its products the others exponentiate. The lanes are MT
+// blocks of 128 rows times 4 / MT interleaved parts of the key tiles (MT = 4: 512
+// rows, every tile; 2: every second tile; 1: every fourth), joined at the end.
+//
+// Warps: 0-15 softmax (lane = warp / 4), 16-19 MMA issuers, 20 the producer, which
+// fills a ring of 64-slot K and V tiles by bulk copies (pages are stored as ready
+// operands); on E4M3 pages it fills a ring of codes, and warps 21-24 convert them
+// into the operand ring (code * 2^e is exact in bf16).
+//
+// A lane's cycle: QK into S, softmax (P = 2^(S - m) as bf16 over the first half of
+// S), PV into O; the thread that issues them gives the order. m is a reference
+// that need not be the running maximum, for it cancels: it moves to the row's maximum
+// on the first tile and when a row's sum of a tile exceeds 2^64, so that most tiles
+// take one pass over S. P is rounded to bf16 (2^-9 relative) for the matrix unit; sums
+// are taken before that rounding, in fp32.
+// Every wait is bounded; one that gives up sets the device error word.
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "pkv_ptx.cuh"
+#include "pkv_tokens.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kLanes = 4;
+constexpr int kBN = kTokTile;
+constexpr int kSoftmaxWarps = 4 * kLanes;
+constexpr int kIssuer0 = kSoftmaxWarps;
+constexpr int kProducer = kIssuer0 + kLanes;
+constexpr int kConvert0 = kProducer + 1;
+constexpr int kConvertWarps = 4;
+template <bool FP8>
+constexpr int kThreads = 32 * (kConvert0 + (FP8 ? kConvertWarps : 0));
+constexpr int kQThreads = 32 * kProducer;      // softmax warps and issuers
+// The ring's stages belong to one part of the tiles each: a multiple of 4 / MT.
+template <int MT, bool FP8>
+constexpr int kRing = FP8 && MT == 4 ? 6 : 8;
+constexpr int kCodeRing = 4;
+constexpr int kCodeBytes = kBN * (kHeadDim + 1);
+// TMEM: S of lane i at 64 i, O at 256 + 64 i
+constexpr uint32_t kTmemCols = 512;
+constexpr float kSumLimit = 18446744073709551616.0f;   // 2^64
+
+template <int MT, bool FP8>
+struct __align__(1024) TcSmem {
+  uint8_t q[MT][128 * 128];
+  union {
+    struct {
+      uint8_t k[kRing<MT, FP8>][kBN * 128];
+      uint8_t v[kRing<MT, FP8>][kBN * 128];
+    };
+    float o[kLanes - MT + (MT == 4)][kHeadDim][128];   // parts 1.. of the tiles, for the join
+  };
+  uint8_t code[FP8 ? kCodeRing : 1][FP8 ? 2 * kCodeBytes : 16];
+  float ml[kLanes][128][2];
+  uint64_t kv_full[kRing<MT, FP8>];
+  uint64_t kv_empty[kRing<MT, FP8>];
+  uint64_t code_full[kCodeRing];
+  uint64_t code_empty[kCodeRing];
+  uint64_t s_full[kLanes];
+  uint64_t p_full[kLanes];
+  uint64_t done[kLanes];
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float s, float c) {
+  asm("{\n .reg .b64 d, m, k;\n mov.b64 d, {%2, %3};\n mov.b64 m, {%4, %4};\n mov.b64 k, {%5, %5};\n"
+      " fma.rn.f32x2 d, d, m, k;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(a), "=f"(b)
+      : "f"(x), "f"(y), "f"(s), "f"(c));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+  asm("{\n .reg .b64 d, m;\n mov.b64 d, {%0, %1};\n mov.b64 m, {%2, %3};\n add.rn.f32x2 d, d, m;\n"
+      " mov.b64 {%0, %1}, d;\n}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+
+// Four E4M3 codes to bf16 pairs times 2^e: a code's bits, shifted to bf16's places,
+// are its value times 2^-120 (subnormal codes become bf16 subnormals), so one exact
+// product with 2^(120 + e) remains, or two where that is no bf16 number (e > 7).
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w, bool high, uint32_t scale) {
+  const uint32_t x = __byte_perm(w, 0u, high ? 0x3424 : 0x1404);   // the codes in the high bytes
+  return mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), scale);
+}
+
+template <int MT, bool FP8>
+__global__ void __launch_bounds__(kThreads<FP8>, 1) token_tc_kernel(const __grid_constant__ TokenAttendArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  TcSmem<MT, FP8>& sm = *reinterpret_cast<TcSmem<MT, FP8>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr int kS = kRing<MT, FP8>;
+  constexpr int kParts = kLanes / MT;
+  static_assert(kS % kParts == 0, "a stage's tiles belong to one part");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kS; ++s) {
+      mbar_init(&sm.kv_full[s], FP8 ? kConvertWarps : 1);
+      mbar_init(&sm.kv_empty[s], MT);
+    }
+    for (int s = 0; s < kCodeRing; ++s) {
+      mbar_init(&sm.code_full[s], 1);
+      mbar_init(&sm.code_empty[s], kConvertWarps);
+    }
+    for (int i = 0; i < kLanes; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.done[i], 1);
+    }
+    sm.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == kIssuer0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
+                     smem_u32(&sm.tmem_base)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  const TokenWork w = token_work(a, blockIdx.x);
+  const TokenQuery& t = a.item[w.item];
+  const TokTiles tiles = tok_tiles(w.p0, w.p1, a.window, a.sinks);
+  const int j0 = (int)((long long)tiles.n * w.split / t.splits);
+  const int j1 = (int)((long long)tiles.n * (w.split + 1) / t.splits);
+  const int nT = j1 - j0;
+  const int G = a.group, Ps = a.pool.page_size;
+  // lane i: rows 128 m .. of the CTA's, tiles j with j % kParts == part
+  const int li = warp < kSoftmaxWarps ? warp >> 2 : warp - kIssuer0;
+  const int m_blk = li % MT, part = li / MT;
+  const int lrows = min(128, w.rows - 128 * m_blk);          // <= 0: the lane has none
+  const int lp0 = t.pos0 + (w.r0 + 128 * m_blk) / G;
+  const int lp1 = lrows > 0 ? t.pos0 + (w.r0 + 128 * m_blk + lrows - 1) / G : -1;
+  // whether the lane's rows see anything of the tile that starts at position b
+  const int lwin = tok_window_lo(lp0, a.window);
+  const auto lane_needs = [&](int b) {
+    return lrows > 0 && b <= lp1 && (b + kBN > lwin || b < a.sinks);
+  };
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp < kProducer) {
+    // Q rows as swizzled operand tiles; rows behind the last one as zeros
+    for (int i = threadIdx.x; i < MT * 128 * 8; i += kQThreads) {
+      const int r = i >> 3, c = i & 7;
+      uint4 val = make_uint4(0u, 0u, 0u, 0u);
+      if (r < w.rows) {
+        const int rr = w.r0 + r;
+        val = __ldg(reinterpret_cast<const uint4*>(a.q + (t.row0 + rr / G) * a.q_stride +
+                                                   (w.head * G + rr % G) * kHeadDim + c * 8));
+      }
+      *reinterpret_cast<uint4*>(&sm.q[r >> 7][(r & 127) * 128 + (swizzle_chunk(r & 7, c) << 4)]) = val;
+    }
+    fence_proxy_async();
+    asm volatile("bar.sync 1, %0;\n" ::"r"(kQThreads) : "memory");
+  }
+
+  if (warp == kProducer) {
+    // ---------------------------------------------------------------- producer
+    const int rows = Ps >= kBN ? kBN : Ps;               // slots per block
+    const int per = kBN / rows;
+    constexpr uint32_t kOperand = FP8 ? kCodeBytes : kBN * 128;   // bytes of K or V in a tile
+    constexpr int kRingN = FP8 ? kCodeRing : kS;
+    uint64_t* const full = FP8 ? sm.code_full : sm.kv_full;
+    uint64_t* const empty = FP8 ? sm.code_empty : sm.kv_empty;
+    const uint32_t block_bytes = kOperand / per;
+    constexpr long long kRowBytes = FP8 ? kHeadDim + 1 : 2 * kHeadDim;
+    const long long plane = (long long)Ps * kRowBytes;
+    int batch = -1, ids = 0, issued = 0;
+    for (int j = 0; j < nT; ++j) {
+      const int s = j % kRingN;
+      if (!mbar_wait(&empty[s], ((j / kRingN) & 1) ^ 1, abort, a.err)) break;
+      const int b = tok_tile(tiles, j0 + j) * kBN;
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], 2u * kOperand);
+#pragma unroll
+      for (int pp = 0; pp < kBN / 16; ++pp) {
+        if (pp >= per) break;
+        const int f = b + pp * rows;
+        // blocks behind the last page repeat it: their slots are masked
+        const int e = min(f / Ps, t.n_pages - 1);
+        if ((e >> 5) != batch) {                 // the next 32 page ids, one per lane
+          batch = e >> 5;
+          const int i = batch * 32 + lane;
+          ids = i < t.n_pages ? t.pages[i] : 0;
+        }
+        int page = __shfl_sync(0xffffffffu, ids, e & 31);
+        if (lane == 0) {
+          if (page < 0 || page >= a.pool.pool_pages) {
+            atomicOr(a.err, kErrPageRange);
+            page = 0;
+          }
+          const uint8_t* src = reinterpret_cast<const uint8_t*>(a.pool.base) +
+                               (long long)page * a.pool.page_bytes + w.head * plane + (f % Ps) * kRowBytes;
+          const uint32_t bar = smem_u32(&full[s]);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            uint8_t* dst = FP8 ? sm.code[s] + kv * kCodeBytes : (kv ? sm.v[s] : sm.k[s]);
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
+                "[%3];\n" ::"r"(smem_u32(dst + pp * block_bytes)),
+                "l"(src + kv * a.pool.heads * plane), "r"(block_bytes), "r"(bar)
+                : "memory");
+          }
+        }
+      }
+      issued = j + 1;
+    }
+    // no copy may still be landing when the CTA joins or ends
+    if (lane == 0)
+      for (int j = max(0, issued - kRingN); j < issued; ++j)
+        mbar_wait(&full[j % kRingN], (j / kRingN) & 1, abort, a.err, false);
+  } else if (FP8 && warp >= kConvert0) {
+    // ------------------------------------------------- E4M3 tiles to operands
+    // 4 lanes a row, 16 codes a lane; 8 rows of K and of V a warp at a time
+    const int B = Ps >= kBN ? kBN : Ps;          // rows of a code block
+    const int cw = warp - kConvert0;
+    for (int j = 0; j < nT; ++j) {
+      const int c8 = j % kCodeRing, s = j % kS;
+      if (!mbar_wait(&sm.code_full[c8], (j / kCodeRing) & 1, abort, a.err)) break;
+      if (!mbar_wait(&sm.kv_empty[s], ((j / kS) & 1) ^ 1, abort, a.err)) break;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int kv = u >> 1;
+        const int r = cw * 16 + (u & 1) * 8 + (lane >> 2), q4 = lane & 3;
+        const uint8_t* blk = sm.code[c8] + kv * kCodeBytes + (r & ~(B - 1)) * (kHeadDim + 1);
+        const int rb = r & (B - 1);
+        const uint4 c = *reinterpret_cast<const uint4*>(blk + rb * kHeadDim + 16 * q4);
+        const int e = (int8_t)blk[B * kHeadDim + rb];
+        const uint32_t s1 = (uint32_t)(127 + 120 + min(e, 7)) << 7;
+        const uint32_t sc = s1 | (s1 << 16);
+        uint32_t o[8] = {codes_to_bf16(c.x, false, sc), codes_to_bf16(c.x, true, sc),
+                         codes_to_bf16(c.y, false, sc), codes_to_bf16(c.y, true, sc),
+                         codes_to_bf16(c.z, false, sc), codes_to_bf16(c.z, true, sc),
+                         codes_to_bf16(c.w, false, sc), codes_to_bf16(c.w, true, sc)};
+        if (e > 7) {
+          const uint32_t s2 = (uint32_t)(127 + e - 7) << 7;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], s2 | (s2 << 16));
+        }
+        uint8_t* row = (kv ? sm.v[s] : sm.k[s]) + r * 128;
+        *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4 + 1) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.kv_full[s]);
+        mbar_arrive(&sm.code_empty[c8]);
+      }
+    }
+  } else if (warp >= kIssuer0 && warp < kProducer) {
+    // ------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdQK = idesc_bf16(128, kBN, false);
+      constexpr uint32_t kIdPV = idesc_bf16(128, kHeadDim, true);
+      const uint64_t qa = sdesc(smem_u32(&sm.q[m_blk][0]));
+      const uint32_t t_s = tmem + 64 * li, t_o = tmem + 256 + 64 * li;
+      uint32_t n = 0;                            // tiles of the lane so far
+      for (int j = part; j < nT; j += kParts) {
+        const int s = j % kS;
+        if (!mbar_wait(&sm.kv_full[s], (j / kS) & 1, abort, a.err)) break;
+        if (!lane_needs(tok_tile(tiles, j0 + j) * kBN)) {
+          mbar_arrive(&sm.kv_empty[s]);
+          continue;
+        }
+        tc_fence_after();
+        const uint64_t kb = sdesc(smem_u32(sm.k[s]));
+#pragma unroll
+        for (int kk = 0; kk < kHeadDim / 16; ++kk) tc_mma(t_s, qa + 2 * kk, kb + 2 * kk, kIdQK, kk > 0);
+        // S of this tile; with it, every earlier product of the lane is done
+        tc_commit(&sm.s_full[li]);
+        if (!mbar_wait(&sm.p_full[li], n & 1, abort, a.err)) break;
+        tc_fence_after();
+        const uint64_t vb = sdesc(smem_u32(sm.v[s]));
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          tc_mma_ts(t_o, t_s + 8 * kk, vb + 128 * kk, kIdPV, (n > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(&sm.kv_empty[s]);
+        ++n;
+      }
+      tc_commit(&sm.done[li]);
+      mbar_wait(&sm.done[li], 0, abort, a.err, false);
+    }
+  } else if (warp < kSoftmaxWarps) {
+    // ---------------------------------------------------------------- softmax
+    const int wq = warp & 3, r = wq * 32 + lane;           // row of the lane's 128
+    const uint32_t t_lane = (uint32_t)(wq * 32) << 16;
+    const uint32_t t_s = tmem + t_lane + 64 * li, t_o = tmem + t_lane + 256 + 64 * li;
+    const int p = t.pos0 + (w.r0 + 128 * m_blk + min(r, max(lrows, 1) - 1)) / G;
+    const float sl2 = a.scale_log2;
+    float m_run = -INFINITY, l_run = 0.f;
+    uint32_t n = 0;
+    bool alive = true;
+    for (int j = part; j < nT; j += kParts) {
+      const int b = tok_tile(tiles, j0 + j) * kBN;
+      if (!lane_needs(b)) continue;
+      const uint64_t bits = tok_tile_full(b, lp0, lp1, a.window, a.sinks) ? ~0ull
+                                                                          : tok_mask(b, p, a.window, a.sinks);
+      if (!mbar_wait(&sm.s_full[li], n & 1, abort, a.err)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t pk[kBN / 2];
+      float sum0, sum1, alpha = 1.f;
+      bool rescale = false;
+      // P and its sum against the reference m_run
+      const auto exponentiate = [&]() {
+        const float m_ref = m_run == -INFINITY ? 0.f : m_run;
+        sum0 = sum1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < kBN; c += 32) {
+          float v[32];
+          PKV_TMEM_LD32(t_s + c, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld();
+          if (bits != ~0ull) {
+            const uint32_t half = (uint32_t)(bits >> c);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((half >> i) & 1u)) v[i] = -INFINITY;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float x, y;
+            fma2(x, y, v[i], v[i + 1], sl2, -m_ref);
+            x = fast_exp2(x);
+            y = fast_exp2(y);
+            pk[(c + i) >> 1] = pack_bf16(x, y);
+            add2(sum0, sum1, x, y);
+          }
+        }
+      };
+      exponentiate();
+      const bool redo = m_run == -INFINITY || !(sum0 + sum1 <= kSumLimit);
+      if (__any_sync(0xffffffffu, redo)) {
+        // the row's maximum becomes its reference (S is still in TMEM)
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kBN; c += 32) {
+          float v[32];
+          PKV_TMEM_LD32(t_s + c, reinterpret_cast<uint32_t*>(v));
+          tmem_wait_ld();
+          const uint32_t half = (uint32_t)(bits >> c);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if ((half >> i) & 1u) mx = fmaxf(mx, v[i]);
+        }
+        mx *= sl2;
+        if (redo && mx > m_run) {
+          if (m_run != -INFINITY) {
+            alpha = fast_exp2(m_run - mx);
+            l_run *= alpha;
+            rescale = true;
+          }
+          m_run = mx;
+        }
+        exponentiate();
+      }
+      l_run += sum0 + sum1;
+      PKV_TMEM_ST32(t_s, pk);
+      tmem_wait_st();
+      if (__any_sync(0xffffffffu, rescale)) {
+        // S of this tile means that the lane's earlier products are done
+#pragma unroll
+        for (int c = 0; c < kHeadDim; c += 16) {
+          uint32_t o[16];
+          PKV_TMEM_LD16(t_o + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          PKV_TMEM_ST16(t_o + c, o);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[li]);
+      ++n;
+    }
+    alive = alive && mbar_wait(&sm.done[li], 0, abort, a.err);
+    tc_fence_after();
+    if (kParts > 1) {
+      // ---- join the parts of the tiles: parts 1.. leave O, m and l to part 0
+      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps * 32) : "memory");   // the ring is free
+      if (part > 0) {
+#pragma unroll
+        for (int c = 0; c < kHeadDim; c += 16) {
+          uint32_t o[16];
+          PKV_TMEM_LD16(t_o + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sm.o[li - MT][c + i][r] = n > 0 ? __uint_as_float(o[i]) : 0.f;
+        }
+        sm.ml[li][r][0] = m_run;
+        sm.ml[li][r][1] = l_run;
+      }
+      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps * 32) : "memory");
+    }
+    if (alive && part == 0 && wq * 32 < lrows) {
+      float f0 = 1.f, fp[kParts];
+      if (kParts > 1) {
+        float mm = m_run;
+#pragma unroll
+        for (int i = 1; i < kParts; ++i) mm = fmaxf(mm, sm.ml[li + i * MT][r][0]);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        f0 = fast_exp2(m_run - ref);
+        l_run *= f0;
+#pragma unroll
+        for (int i = 1; i < kParts; ++i) {
+          fp[i] = fast_exp2(sm.ml[li + i * MT][r][0] - ref);
+          l_run += fp[i] * sm.ml[li + i * MT][r][1];
+        }
+        m_run = mm;
+      }
+      const float inv = t.splits > 1 ? 1.f : (l_run > 0.f ? 1.f / l_run : 0.f);
+      const int rr = w.r0 + 128 * m_blk + r;
+      const long long pr = (long long)blockIdx.x * a.rows + 128 * m_blk + r;
+      uint16_t* out = a.out + ((long long)(t.row0 + rr / G) * a.heads * G + w.head * G + rr % G) * kHeadDim;
+#pragma unroll
+      for (int c = 0; c < kHeadDim; c += 16) {
+        uint32_t o[16];
+        PKV_TMEM_LD16(t_o + c, o);
+        tmem_wait_ld();
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          f[i] = n > 0 ? __uint_as_float(o[i]) : 0.f;
+          if (kParts > 1) {
+            f[i] *= f0;
+#pragma unroll
+            for (int k = 1; k < kParts; ++k) f[i] += fp[k] * sm.o[k * MT + m_blk - MT][c + i][r];
+          }
+          f[i] *= inv;
+        }
+        if (r < lrows) {
+          if (t.splits == 1) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8)
+              *reinterpret_cast<uint4*>(out + c + i) =
+                  make_uint4(pack_bf16(f[i], f[i + 1]), pack_bf16(f[i + 2], f[i + 3]),
+                             pack_bf16(f[i + 4], f[i + 5]), pack_bf16(f[i + 6], f[i + 7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + c + i) =
+                  make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+          }
+        }
+      }
+      if (t.splits > 1 && r < lrows) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m_run, l_run);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuer0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kTmemCols));
+  }
+}
+
+template <int MT, bool FP8>
+cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(TcSmem<MT, FP8>) + 1024;
+  static_assert(smem <= 232448, "shared memory of a CTA");
+  static std::atomic<unsigned long long> configured{0};   // a bit per device
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev >= 64 || !(configured.load() & bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(token_tc_kernel<MT, FP8>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) configured.fetch_or(bit);
+  }
+  const cudaError_t e = launch_pdl(token_tc_kernel<MT, FP8>, dim3(a.ctas), dim3(kThreads<FP8>), smem, s, a);
+  count_launches(1);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s) {
+  if (a.pool.fp8)
+    return a.rows == 128 ? launch_tc<1, true>(a, s) : a.rows == 256 ? launch_tc<2, true>(a, s) : launch_tc<4, true>(a, s);
+  return a.rows == 128 ? launch_tc<1, false>(a, s) : a.rows == 256 ? launch_tc<2, false>(a, s) : launch_tc<4, false>(a, s);
+}
+
+}  // namespace pkv

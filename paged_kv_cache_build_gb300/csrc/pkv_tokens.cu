@@ -344,7 +344,6 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = h->d_err;
   int tiles[kMaxTokenBatch];
-  int most = 0;
   for (int i = 0; i < n; ++i) {
     const Stream& st = h->streams[sids[i]];
     const TokenCounts& t = st.tok;
@@ -360,32 +359,53 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
     it.n = rows;
     it.pos0 = t.len - rows;
     it.n_pages = t.n_pages;
-    most = std::max(most, rows);
   }
-  const long long most_rows = (long long)most * group;
-  a.rows = most_rows <= 8 ? 8 : most_rows <= 16 ? 16 : kTokenFewRows;
-  for (int i = 0; i < a.n; ++i) {
-    TokenQuery& it = a.item[i];
-    it.blocks = ceil_div((long long)it.n * group, a.rows);
-    // the longest table of the item's blocks: the last one's, without a window
-    tiles[i] = 0;
-    for (int b : {0, it.blocks - 1}) {
-      const int r0 = b * a.rows, r1 = std::min(r0 + a.rows, it.n * group) - 1;
-      tiles[i] = std::max(tiles[i], tok_tiles(it.pos0 + r0 / group, it.pos0 + r1 / group, window, sinks).n);
-    }
-  }
-  plan_splits(&a, tiles, h->num_sms * token_few_ctas_per_sm(a.rows));
-  bool split = false;
-  for (int i = 0; i < a.n; ++i) split = split || a.item[i].splits > 1;
-  if (split) {
-    const size_t rows = (size_t)a.ctas * a.rows;
-    if (pkv_status r = ensure_scratch(h, rows * (kHeadDim + 2) * sizeof(float))) return r;
-    a.part_o = h->d_scratch;
-    a.part_ml = h->d_scratch + rows * kHeadDim;
-  }
+  // one launch per kernel shape: the streams' rows per KV head decide
   cudaStream_t s = as_stream(cuda_stream);
-  PKV_CUDA(h, launch_token_few(a, s));
-  if (split) PKV_CUDA(h, launch_token_combine(a, s));
+  const int n_items = a.n;
+  TokenQuery all[kMaxTokenBatch];
+  std::copy(a.item, a.item + n_items, all);
+  for (int pass = 0; pass < 2; ++pass) {         // the first grows the scratch, if it must
+    size_t need = 0;
+    for (const int shape : {kTokenFewRows, 128, 256, 512}) {
+      const int below = shape == kTokenFewRows ? 0 : shape == 128 ? kTokenFewRows : shape / 2;
+      a.n = 0;
+      int most = 0;
+      for (int i = 0; i < n_items; ++i) {
+        const long long r = (long long)all[i].n * group;
+        if (r <= below || (r > shape && shape < 512)) continue;
+        a.item[a.n++] = all[i];
+        most = std::max(most, (int)std::min<long long>(r, shape));
+      }
+      if (a.n == 0) continue;
+      const bool few = shape == kTokenFewRows;
+      a.rows = !few ? shape : most <= 8 ? 8 : most <= 16 ? 16 : kTokenFewRows;
+      for (int i = 0; i < a.n; ++i) {
+        TokenQuery& it = a.item[i];
+        it.blocks = ceil_div((long long)it.n * group, a.rows);
+        // the longest table of the item's blocks: the last one's, without a window
+        tiles[i] = 0;
+        for (int b : {0, it.blocks - 1}) {
+          const int r0 = b * a.rows, r1 = std::min(r0 + a.rows, it.n * group) - 1;
+          tiles[i] = std::max(tiles[i], tok_tiles(it.pos0 + r0 / group, it.pos0 + r1 / group, window, sinks).n);
+        }
+      }
+      plan_splits(&a, tiles, h->num_sms * (few ? token_few_ctas_per_sm(a.rows) : 1));
+      bool split = false;
+      for (int i = 0; i < a.n; ++i) split = split || a.item[i].splits > 1;
+      if (split) {
+        const size_t rows = (size_t)a.ctas * a.rows;
+        need = std::max(need, rows * (kHeadDim + 2) * sizeof(float));
+        a.part_o = h->d_scratch;
+        a.part_ml = h->d_scratch + rows * kHeadDim;
+      }
+      if (pass == 0) continue;
+      PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, s));
+      if (split) PKV_CUDA(h, launch_token_combine(a, s));
+    }
+    if (pass == 0)
+      if (pkv_status r = ensure_scratch(h, need)) return r;
+  }
   return PKV_OK;
 }
 
