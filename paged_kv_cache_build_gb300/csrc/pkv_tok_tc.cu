@@ -4,31 +4,33 @@
 //
 //   out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),   s_j = log2(e) sm_scale q . k_j
 //
-// Bounds: at head_dim 64 a 128 x 64 tile of scores is 2 x 256 matrix-unit cycles of
-// 4096 multiply-adds, and 256 cycles of the SM's 32 exponentials a cycle, so the
-// softmax must run beside the products without a pause. What stalls it is latency:
-// S must come back from the matrix unit and P go to it. So a CTA runs four
-// independent pipelines ("lanes"), each 128 query rows with its own S and O in
-// TMEM, its own issuing thread and its own four softmax warps (a thread per row);
-// while one waits for its products the others exponentiate. The lanes are MT
-// blocks of 128 rows times 4 / MT interleaved parts of the key tiles (MT = 4: 512
-// rows, every tile; 2: every second tile; 1: every fourth), joined at the end.
+// Bounds: at head_dim 64 a 128 x 128 step is 512 cycles of the matrix unit (256 for
+// each product) and 512 of the SM's 32 exponentials a cycle, so the softmax must run
+// beside the products without a pause. A CTA has two lanes of 128 query rows, each
+// with four softmax warps (a thread per row) and its own O in TMEM; the scores of
+// their steps go round three TMEM buffers of 128 columns, so that a lane's next S
+// is ready when it has written its P. The lanes are two blocks of 128 rows (MT = 2),
+// or, for up to 128 rows, one block over every second step of the keys (MT = 1),
+// joined at the end.
 //
-// Warps: 0-15 softmax (lane = warp / 4), 16-19 MMA issuers, 20 the producer, which
-// fills a ring of 64-slot K and V tiles by bulk copies (pages are stored as ready
-// operands); on E4M3 pages it fills a ring of codes, and warps 21-24 convert them
-// into the operand ring (code * 2^e is exact in bf16).
+// Warps: 0-7 softmax (lane = warp / 4); 8 issues QK, 9 and 10 the lanes' PV: a warp
+// that issues products spends most of its time in waits and in filling the matrix
+// unit's queue, and one for all of them left the unit idle half the time; 11 the
+// producer, which fills a ring of 128-slot K and V steps by bulk copies (pages are
+// stored as ready operands); on E4M3 pages it fills a ring of codes, and warps 12 on
+// convert them into the operand ring (code * 2^e is exact in bf16).
 //
-// A lane's cycle: QK into S, softmax (P = 2^(S - m) as bf16 over the first half of
-// S), PV into O; the thread that issues them gives the order. m is a reference
-// that need not be the running maximum, for it cancels: it moves to the row's maximum
-// on the first tile and when a row's sum of a tile exceeds 2^64, so that most tiles
-// take one pass over S. P is rounded to bf16 (2^-9 relative) for the matrix unit; sums
-// are taken before that rounding, in fp32.
+// x counts the steps of both lanes in turn; step x uses S buffer x % 3, and P(x) is
+// written over the first half of S(x). QK(x) waits for PV(x - 3), PV(x) for P(x).
+// m is a reference that need not be the running maximum, for it
+// cancels: it moves to the row's maximum on the first step and when a row's sum of a
+// step exceeds 2^64, so that most steps take one pass over S. P is rounded to bf16
+// (2^-9 relative) for the matrix unit; sums are taken before that rounding, in fp32.
 // Every wait is bounded; one that gives up sets the device error word.
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "pkv_ptx.cuh"
 #include "pkv_tokens.cuh"
@@ -37,44 +39,62 @@ namespace pkv {
 
 namespace {
 
-constexpr int kLanes = 4;
-constexpr int kBN = kTokTile;
+constexpr int kLanes = 2;
+constexpr int kStep = 2 * kTokTile;            // slots per step
 constexpr int kSoftmaxWarps = 4 * kLanes;
-constexpr int kIssuer0 = kSoftmaxWarps;
-constexpr int kProducer = kIssuer0 + kLanes;
+constexpr int kIssueQK = kSoftmaxWarps;
+constexpr int kIssuePV = kIssueQK + 1;
+constexpr int kProducer = kIssuePV + kLanes;
 constexpr int kConvert0 = kProducer + 1;
-constexpr int kConvertWarps = 4;
 template <bool FP8>
-constexpr int kThreads = 32 * (kConvert0 + (FP8 ? kConvertWarps : 0));
+constexpr int kConvertWarps = FP8 ? 8 : 0;
+template <bool FP8>
+constexpr int kThreads = 32 * (kConvert0 + kConvertWarps<FP8>);
 constexpr int kQThreads = 32 * kProducer;      // softmax warps and issuers
-// The ring's stages belong to one part of the tiles each: a multiple of 4 / MT.
-template <int MT, bool FP8>
-constexpr int kRing = FP8 && MT == 4 ? 6 : 8;
-constexpr int kCodeRing = 4;
-constexpr int kCodeBytes = kBN * (kHeadDim + 1);
-// TMEM: S of lane i at 64 i, O at 256 + 64 i
-constexpr uint32_t kTmemCols = 512;
+// Registers: bf16 pages, 168 for everyone; E4M3 pages, 96 at launch, of which the
+// others leave some to the softmax warpgroups.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 168, kOtherRegs = 48;
+static_assert(kSoftmaxRegs * kSoftmaxWarps + kOtherRegs * (kThreads<true> / 32 - kSoftmaxWarps) <=
+                  kLaunchRegs * (kThreads<true> / 32),
+              "the register split is within the launch's registers");
+template <bool FP8>
+constexpr int kRing = FP8 ? 4 : 5;
+constexpr int kCodeRing = 3;
+constexpr int kCodeBytes = kTokTile * (kHeadDim + 1);   // of K or V in a 64-slot tile
+// TMEM: S buffer i at 128 i, O of lane i at 384 + 64 i
+constexpr int kSBufs = 3;
+constexpr uint32_t kTmemO = 384, kTmemCols = 512;
+constexpr int kMaxFlags = 2048;                // steps whose flags are worked out beforehand
 constexpr float kSumLimit = 18446744073709551616.0f;   // 2^64
 
-template <int MT, bool FP8>
+template <bool FP8>
 struct __align__(1024) TcSmem {
-  uint8_t q[MT][128 * 128];
+  uint8_t q[kLanes][128 * 128];
   union {
     struct {
-      uint8_t k[kRing<MT, FP8>][kBN * 128];
-      uint8_t v[kRing<MT, FP8>][kBN * 128];
+      uint8_t k[kRing<FP8>][kStep * 128];
+      uint8_t v[kRing<FP8>][kStep * 128];
     };
-    float o[kLanes - MT + (MT == 4)][kHeadDim][128];   // parts 1.. of the tiles, for the join
+    float o[kHeadDim][128];        // MT = 1: lane 1's part, for the join
   };
-  uint8_t code[FP8 ? kCodeRing : 1][FP8 ? 2 * kCodeBytes : 16];
-  float ml[kLanes][128][2];
-  uint64_t kv_full[kRing<MT, FP8>];
-  uint64_t kv_empty[kRing<MT, FP8>];
+  uint8_t code[FP8 ? kCodeRing : 1][FP8 ? 4 * kCodeBytes : 16];   // tile 0: K, V; tile 1: K, V
+  float ml[128][2];
+  uint64_t kv_full[kRing<FP8>];
+  uint64_t kv_empty[kRing<FP8>];
   uint64_t code_full[kCodeRing];
   uint64_t code_empty[kCodeRing];
-  uint64_t s_full[kLanes];
-  uint64_t p_full[kLanes];
-  uint64_t done[kLanes];
+  uint64_t s_full[kSBufs];
+  uint64_t p_full[kLanes][kSBufs];   // of the lane's step in the buffer
+  uint64_t pv_done[kSBufs];
+  uint64_t o_done[kLanes];       // every PV of the lane
+  uint64_t done[kLanes + 1];     // an issuer's products are all done (lanes' PV, QK)
+  uint8_t flags[kMaxFlags];      // per step: see step_flags
+  // the CTA's work, kept here for the roles to read what they need of it
+  TokenWork work;
+  TokTiles tiles;
+  int j0, n_tiles;               // its 64-slot tiles; step i has tiles 2 i and 2 i + 1
+  int row0, pos0, n_pages, splits;
+  const int32_t* pages;
   uint32_t tmem_base;
   int abort;
 };
@@ -92,6 +112,15 @@ __device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
       : "f"(x), "f"(y));
 }
 
+// An arrival without a branch around it.
+__device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool yes) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n"
+      " @p mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"((int)yes)
+      : "memory");
+}
+
 // Four E4M3 codes to bf16 pairs times 2^e: a code's bits, shifted to bf16's places,
 // are its value times 2^-120 (subnormal codes become bf16 subnormals), so one exact
 // product with 2^(120 + e) remains, or two where that is no bf16 number (e > 7).
@@ -105,33 +134,84 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t w, bool high, uint32_
   return mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), scale);
 }
 
+// A lane's rows: 128 m .. of the CTA's (none: n <= 0), and the tiles that they see.
+struct LaneRows {
+  int n;
+  TokSpan span;
+};
+__device__ __forceinline__ LaneRows lane_rows(const TokenAttendArgs& a, const TokenWork& w, int pos0, int m) {
+  LaneRows l;
+  l.n = min(128, w.rows - 128 * m);
+  const int r0 = w.r0 + 128 * m;
+  l.span = tok_span(pos0 + r0 / a.group, pos0 + (r0 + l.n - 1) / a.group, a.window, a.sinks);
+  if (l.n <= 0) {                // nothing is needed, nothing whole
+    l.span.hi = -1;
+    l.span.f1 = 0;
+  }
+  return l;
+}
+
+// What the lanes see of step i: bits 2 l: lane l needs it; 2 l + 1: it sees it whole.
+__device__ __forceinline__ int step_flags(const TokTiles& tiles, int j0, int n_tiles, int i, const TokSpan& s0,
+                                          const TokSpan& s1) {
+  const int t0 = tok_tile(tiles, j0 + 2 * i);
+  const bool two = 2 * i + 1 < n_tiles;
+  const int t1 = two ? tok_tile(tiles, j0 + 2 * i + 1) : 0;
+  const auto lane = [&](const TokSpan& s) {
+    return (s.needs(t0) || (two && s.needs(t1)) ? 1 : 0) | (two && s.whole(t0) && s.whole(t1) ? 2 : 0);
+  };
+  return lane(s0) | lane(s1) << 2;
+}
+
+// A wait of a whole warp, with one outcome for all of it: control flow stays uniform.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  if (__all_sync(0xffffffffu, mbar_test(smem_u32(bar), parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
+}
+
 template <int MT, bool FP8>
 __global__ void __launch_bounds__(kThreads<FP8>, 1) token_tc_kernel(const __grid_constant__ TokenAttendArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  TcSmem<MT, FP8>& sm = *reinterpret_cast<TcSmem<MT, FP8>*>(
+  TcSmem<FP8>& sm = *reinterpret_cast<TcSmem<FP8>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  constexpr int kS = kRing<MT, FP8>;
-  constexpr int kParts = kLanes / MT;
-  static_assert(kS % kParts == 0, "a stage's tiles belong to one part");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kS = kRing<FP8>;
+  // warp-uniform, and known to be
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kS; ++s) {
-      mbar_init(&sm.kv_full[s], FP8 ? kConvertWarps : 1);
+      mbar_init(&sm.kv_full[s], FP8 ? kConvertWarps<FP8> : 1);
       mbar_init(&sm.kv_empty[s], MT);
     }
     for (int s = 0; s < kCodeRing; ++s) {
       mbar_init(&sm.code_full[s], 1);
-      mbar_init(&sm.code_empty[s], kConvertWarps);
+      mbar_init(&sm.code_empty[s], FP8 ? kConvertWarps<FP8> : 1);
     }
-    for (int i = 0; i < kLanes; ++i) {
+    for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 4);
-      mbar_init(&sm.done[i], 1);
+      for (int l = 0; l < kLanes; ++l) mbar_init(&sm.p_full[l][i], 4);
+      mbar_init(&sm.pv_done[i], 1);
     }
+    for (int l = 0; l < kLanes; ++l) mbar_init(&sm.o_done[l], 1);
+    for (int l = 0; l <= kLanes; ++l) mbar_init(&sm.done[l], 1);
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == kIssuer0) {
+  if (threadIdx.x == 32) {
+    const TokenWork w = token_work(a, blockIdx.x);
+    const TokenQuery& t = a.item[w.item];
+    const TokTiles tiles = tok_tiles(w.p0, w.p1, a.window, a.sinks);
+    const int steps = (tiles.n + 1) / 2;
+    sm.work = w;
+    sm.tiles = tiles;
+    sm.j0 = 2 * (int)((long long)steps * w.split / t.splits);
+    sm.n_tiles = min(tiles.n, 2 * (int)((long long)steps * (w.split + 1) / t.splits)) - sm.j0;
+    sm.row0 = t.row0;
+    sm.pos0 = t.pos0;
+    sm.n_pages = t.n_pages;
+    sm.splits = t.splits;
+    sm.pages = t.pages;
+  }
+  if (warp == kIssueQK) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      smem_u32(&sm.tmem_base)),
                  "r"(kTmemCols));
@@ -140,37 +220,25 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1) token_tc_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
-  const TokenWork w = token_work(a, blockIdx.x);
-  const TokenQuery& t = a.item[w.item];
-  const TokTiles tiles = tok_tiles(w.p0, w.p1, a.window, a.sinks);
-  const int j0 = (int)((long long)tiles.n * w.split / t.splits);
-  const int j1 = (int)((long long)tiles.n * (w.split + 1) / t.splits);
-  const int nT = j1 - j0;
-  const int G = a.group, Ps = a.pool.page_size;
-  // lane i: rows 128 m .. of the CTA's, tiles j with j % kParts == part
-  const int li = warp < kSoftmaxWarps ? warp >> 2 : warp - kIssuer0;
-  const int m_blk = li % MT, part = li / MT;
-  const int lrows = min(128, w.rows - 128 * m_blk);          // <= 0: the lane has none
-  const int lp0 = t.pos0 + (w.r0 + 128 * m_blk) / G;
-  const int lp1 = lrows > 0 ? t.pos0 + (w.r0 + 128 * m_blk + lrows - 1) / G : -1;
-  // whether the lane's rows see anything of the tile that starts at position b
-  const int lwin = tok_window_lo(lp0, a.window);
-  const auto lane_needs = [&](int b) {
-    return lrows > 0 && b <= lp1 && (b + kBN > lwin || b < a.sinks);
-  };
+  const TokenWork& w = sm.work;
+  const int G = a.group;
   pdl_wait();
   pdl_trigger();
 
   if (warp < kProducer) {
+    // the steps' flags
+    const TokSpan s0 = lane_rows(a, w, sm.pos0, 0).span;
+    const TokSpan s1 = MT == 2 ? lane_rows(a, w, sm.pos0, 1).span : s0;
+    for (int i = threadIdx.x; 2 * i < sm.n_tiles && i < kMaxFlags; i += kQThreads)
+      sm.flags[i] = (uint8_t)step_flags(sm.tiles, sm.j0, sm.n_tiles, i, s0, s1);
     // Q rows as swizzled operand tiles; rows behind the last one as zeros
     for (int i = threadIdx.x; i < MT * 128 * 8; i += kQThreads) {
       const int r = i >> 3, c = i & 7;
       uint4 val = make_uint4(0u, 0u, 0u, 0u);
       if (r < w.rows) {
         const int rr = w.r0 + r;
-        val = __ldg(reinterpret_cast<const uint4*>(a.q + (t.row0 + rr / G) * a.q_stride +
+        val = __ldg(reinterpret_cast<const uint4*>(a.q + (sm.row0 + rr / G) * a.q_stride +
                                                    (w.head * G + rr % G) * kHeadDim + c * 8));
       }
       *reinterpret_cast<uint4*>(&sm.q[r >> 7][(r & 127) * 128 + (swizzle_chunk(r & 7, c) << 4)]) = val;
@@ -181,31 +249,37 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1) token_tc_kernel(const __grid
 
   if (warp == kProducer) {
     // ---------------------------------------------------------------- producer
-    const int rows = Ps >= kBN ? kBN : Ps;               // slots per block
-    const int per = kBN / rows;
-    constexpr uint32_t kOperand = FP8 ? kCodeBytes : kBN * 128;   // bytes of K or V in a tile
+    if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    const int Ps = a.pool.page_size;
+    const int nT = sm.n_tiles, j0 = sm.j0, n_pages = sm.n_pages, head = w.head;
+    const TokTiles tiles = sm.tiles;
+    const int32_t* pages = sm.pages;
+    const int rows = min(Ps, kTokTile);                  // slots per block
+    const int per = kTokTile / rows;
+    constexpr uint32_t kOperand = FP8 ? kCodeBytes : kTokTile * 128;   // bytes of K or V in a tile
     constexpr int kRingN = FP8 ? kCodeRing : kS;
     uint64_t* const full = FP8 ? sm.code_full : sm.kv_full;
     uint64_t* const empty = FP8 ? sm.code_empty : sm.kv_empty;
     const uint32_t block_bytes = kOperand / per;
     constexpr long long kRowBytes = FP8 ? kHeadDim + 1 : 2 * kHeadDim;
     const long long plane = (long long)Ps * kRowBytes;
+    const int nS = (nT + 1) / 2;
     int batch = -1, ids = 0, issued = 0;
-    for (int j = 0; j < nT; ++j) {
-      const int s = j % kRingN;
-      if (!mbar_wait(&empty[s], ((j / kRingN) & 1) ^ 1, abort, a.err)) break;
-      const int b = tok_tile(tiles, j0 + j) * kBN;
-      if (lane == 0) mbar_arrive_expect_tx(&full[s], 2u * kOperand);
-#pragma unroll
-      for (int pp = 0; pp < kBN / 16; ++pp) {
-        if (pp >= per) break;
-        const int f = b + pp * rows;
+    for (int i = 0; i < nS; ++i) {
+      const int s = i % kRingN;
+      if (!mbar_wait(&empty[s], ((i / kRingN) & 1) ^ 1, abort, a.err)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], 4u * kOperand);
+      const uint32_t bar = smem_u32(&full[s]);
+      for (int x = 0; x < 2 * per; ++x) {
+        const int half = x / per, pp = x - half * per;
+        // a last step of one tile takes it twice: the second is masked
+        const int f = tok_tile(tiles, j0 + min(2 * i + half, nT - 1)) * kTokTile + pp * rows;
         // blocks behind the last page repeat it: their slots are masked
-        const int e = min(f / Ps, t.n_pages - 1);
+        const int e = min(f / Ps, n_pages - 1);
         if ((e >> 5) != batch) {                 // the next 32 page ids, one per lane
           batch = e >> 5;
-          const int i = batch * 32 + lane;
-          ids = i < t.n_pages ? t.pages[i] : 0;
+          const int at = batch * 32 + lane;
+          ids = at < n_pages ? pages[at] : 0;
         }
         int page = __shfl_sync(0xffffffffu, ids, e & 31);
         if (lane == 0) {
@@ -214,11 +288,11 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1) token_tc_kernel(const __grid
             page = 0;
           }
           const uint8_t* src = reinterpret_cast<const uint8_t*>(a.pool.base) +
-                               (long long)page * a.pool.page_bytes + w.head * plane + (f % Ps) * kRowBytes;
-          const uint32_t bar = smem_u32(&full[s]);
+                               (long long)page * a.pool.page_bytes + head * plane + (f % Ps) * kRowBytes;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            uint8_t* dst = FP8 ? sm.code[s] + kv * kCodeBytes : (kv ? sm.v[s] : sm.k[s]);
+            uint8_t* dst = FP8 ? sm.code[s] + (2 * half + kv) * kCodeBytes
+                               : (kv ? sm.v[s] : sm.k[s]) + half * kTokTile * 128;
             asm volatile(
                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
                 "[%3];\n" ::"r"(smem_u32(dst + pp * block_bytes)),
@@ -227,219 +301,307 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1) token_tc_kernel(const __grid
           }
         }
       }
-      issued = j + 1;
+      issued = i + 1;
     }
     // no copy may still be landing when the CTA joins or ends
     if (lane == 0)
-      for (int j = max(0, issued - kRingN); j < issued; ++j)
-        mbar_wait(&full[j % kRingN], (j / kRingN) & 1, abort, a.err, false);
-  } else if (FP8 && warp >= kConvert0) {
-    // ------------------------------------------------- E4M3 tiles to operands
-    // 4 lanes a row, 16 codes a lane; 8 rows of K and of V a warp at a time
-    const int B = Ps >= kBN ? kBN : Ps;          // rows of a code block
-    const int cw = warp - kConvert0;
-    for (int j = 0; j < nT; ++j) {
-      const int c8 = j % kCodeRing, s = j % kS;
-      if (!mbar_wait(&sm.code_full[c8], (j / kCodeRing) & 1, abort, a.err)) break;
-      if (!mbar_wait(&sm.kv_empty[s], ((j / kS) & 1) ^ 1, abort, a.err)) break;
+      for (int i = max(0, issued - kRingN); i < issued; ++i)
+        mbar_wait(&full[i % kRingN], (i / kRingN) & 1, abort, a.err, false);
+  } else if (warp >= kConvert0) {
+    // ------------------------------------------------- E4M3 steps to operands
+    // 4 lanes a row, 16 codes a lane; 8 rows of K or of V a warp at a time
+    if constexpr (FP8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+      const int B = min(kTokTile, a.pool.page_size);     // rows of a code block
+      const int nS = (sm.n_tiles + 1) / 2;
+      const int cw = warp - kConvert0;
+      for (int i = 0; i < nS; ++i) {
+        const int c8 = i % kCodeRing, s = i % kS;
+        if (!mbar_wait(&sm.code_full[c8], (i / kCodeRing) & 1, abort, a.err)) break;
+        if (!mbar_wait(&sm.kv_empty[s], ((i / kS) & 1) ^ 1, abort, a.err)) break;
+#pragma unroll 2
+        for (int u = cw; u < 4 * kTokTile / 8; u += kConvertWarps<FP8>) {
+          const int op = u >> 3;                         // tile 0: K, V; tile 1: K, V
+          const int r = (u & 7) * 8 + (lane >> 2), q4 = lane & 3;
+          const uint8_t* blk = sm.code[c8] + op * kCodeBytes + (r & ~(B - 1)) * (kHeadDim + 1);
+          const int rb = r & (B - 1);
+          const uint4 c = *reinterpret_cast<const uint4*>(blk + rb * kHeadDim + 16 * q4);
+          const int e = (int8_t)blk[B * kHeadDim + rb];
+          const uint32_t s1 = (uint32_t)(127 + 120 + min(e, 7)) << 7;
+          const uint32_t sc = s1 | (s1 << 16);
+          uint32_t o[8] = {codes_to_bf16(c.x, false, sc), codes_to_bf16(c.x, true, sc),
+                           codes_to_bf16(c.y, false, sc), codes_to_bf16(c.y, true, sc),
+                           codes_to_bf16(c.z, false, sc), codes_to_bf16(c.z, true, sc),
+                           codes_to_bf16(c.w, false, sc), codes_to_bf16(c.w, true, sc)};
+          if (e > 7) {
+            const uint32_t s2 = (uint32_t)(127 + e - 7) << 7;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int kv = u >> 1;
-        const int r = cw * 16 + (u & 1) * 8 + (lane >> 2), q4 = lane & 3;
-        const uint8_t* blk = sm.code[c8] + kv * kCodeBytes + (r & ~(B - 1)) * (kHeadDim + 1);
-        const int rb = r & (B - 1);
-        const uint4 c = *reinterpret_cast<const uint4*>(blk + rb * kHeadDim + 16 * q4);
-        const int e = (int8_t)blk[B * kHeadDim + rb];
-        const uint32_t s1 = (uint32_t)(127 + 120 + min(e, 7)) << 7;
-        const uint32_t sc = s1 | (s1 << 16);
-        uint32_t o[8] = {codes_to_bf16(c.x, false, sc), codes_to_bf16(c.x, true, sc),
-                         codes_to_bf16(c.y, false, sc), codes_to_bf16(c.y, true, sc),
-                         codes_to_bf16(c.z, false, sc), codes_to_bf16(c.z, true, sc),
-                         codes_to_bf16(c.w, false, sc), codes_to_bf16(c.w, true, sc)};
-        if (e > 7) {
-          const uint32_t s2 = (uint32_t)(127 + e - 7) << 7;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], s2 | (s2 << 16));
+            for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], s2 | (s2 << 16));
+          }
+          uint8_t* row = ((op & 1) ? sm.v[s] : sm.k[s]) + (64 * (op >> 1) + r) * 128;
+          *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4 + 1) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        uint8_t* row = (kv ? sm.v[s] : sm.k[s]) + r * 128;
-        *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4 + 1) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm.kv_full[s]);
-        mbar_arrive(&sm.code_empty[c8]);
+        fence_proxy_async();
+        __syncwarp();
+        mbar_arrive_if(&sm.kv_full[s], lane == 0);
+        mbar_arrive_if(&sm.code_empty[c8], lane == 0);
       }
     }
-  } else if (warp >= kIssuer0 && warp < kProducer) {
-    // ------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdQK = idesc_bf16(128, kBN, false);
+  } else if (warp >= kIssueQK) {
+    // ------------------------------------------------------------ MMA issuers
+    if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    const auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint32_t tmem = (uint32_t)uniform((int)sm.tmem_base);
+    const int nT = uniform(sm.n_tiles), nS = (nT + 1) / 2;
+    const int nX = MT == 2 ? 2 * nS : nS;
+    const int j0 = uniform(sm.j0);
+    const uint32_t k0 = smem_u32(sm.k[0]), v0 = smem_u32(sm.v[0]), q0 = smem_u32(sm.q[0]);
+    const auto flags = [&](int i) {
+      if (i < kMaxFlags) return uniform(sm.flags[i]);
+      const TokSpan s0 = lane_rows(a, sm.work, sm.pos0, 0).span;
+      return uniform(step_flags(sm.tiles, j0, nT, i, s0, MT == 2 ? lane_rows(a, sm.work, sm.pos0, 1).span : s0));
+    };
+    if (warp == kIssueQK) {
+      constexpr uint32_t kIdQK = idesc_bf16(128, kStep, false);
+      int s = 0, buf = 0;
+      int f = nX > 0 ? flags(0) : 0;
+      uint32_t kv_phase = 0, phase = 1;            // phase: of the buffer's last PV (none yet: passes)
+      for (int x = 0; x < nX; ++x) {
+        const int l = x & 1;
+        if ((MT == 1 || l == 0) && !mbar_wait_warp(&sm.kv_full[s], kv_phase, abort, a.err)) break;
+        if (!mbar_wait_warp(&sm.pv_done[buf], phase, abort, a.err)) break;
+        if ((f >> (2 * (MT == 2 ? l : 0))) & 1) {
+          tc_fence_after();
+          const uint64_t qa = sdesc(q0 + (MT == 2 ? l * (128 * 128) : 0)), kb = sdesc(k0 + s * (kStep * 128));
+#pragma unroll
+          for (int kk = 0; kk < kHeadDim / 16; ++kk)
+            tc_mma_warp(tmem + kStep * buf, qa + 2 * kk, kb + 2 * kk, kIdQK, kk > 0);
+        }
+        tc_commit_warp(&sm.s_full[buf]);
+        if (x + 1 < nX && (MT == 1 || l == 1)) f = flags(MT == 2 ? (x + 1) >> 1 : x + 1);
+        if (++buf == kSBufs) {
+          buf = 0;
+          phase ^= 1;
+        }
+        if ((MT == 1 || l == 1) && ++s == kS) {
+          s = 0;
+          kv_phase ^= 1;
+        }
+      }
+      tc_commit_warp(&sm.done[kLanes]);
+      mbar_wait(&sm.done[kLanes], 0, abort, a.err, false);
+    } else {
       constexpr uint32_t kIdPV = idesc_bf16(128, kHeadDim, true);
-      const uint64_t qa = sdesc(smem_u32(&sm.q[m_blk][0]));
-      const uint32_t t_s = tmem + 64 * li, t_o = tmem + 256 + 64 * li;
-      uint32_t n = 0;                            // tiles of the lane so far
-      for (int j = part; j < nT; j += kParts) {
-        const int s = j % kS;
-        if (!mbar_wait(&sm.kv_full[s], (j / kS) & 1, abort, a.err)) break;
-        if (!lane_needs(tok_tile(tiles, j0 + j) * kBN)) {
-          mbar_arrive(&sm.kv_empty[s]);
-          continue;
+      const int l = warp - kIssuePV;
+      int buf = l, s = MT == 2 ? 0 : l % kS;
+      uint32_t phase[kSBufs] = {0, 0, 0}, kv_phase = 0;
+      uint32_t some = 0;
+      for (int x = l; x < nX; x += 2) {
+        // everything that does not need P comes before the wait for it
+        const bool needed = (flags(MT == 2 ? x >> 1 : x) >> (2 * (MT == 2 ? l : 0))) & 1;
+        if (!mbar_wait_warp(&sm.kv_full[s], kv_phase, abort, a.err)) break;
+        const uint32_t ph = buf == 0 ? phase[0] : buf == 1 ? phase[1] : phase[2];
+        if (!mbar_wait_warp(&sm.p_full[l][buf], ph, abort, a.err)) break;
+        if (needed) {
+          tc_fence_after();
+          const uint64_t vb = sdesc(v0 + s * (kStep * 128));
+          const uint32_t t_p = tmem + kStep * buf, t_o = tmem + kTmemO + 64 * l;
+#pragma unroll
+          for (int kk = 0; kk < kStep / 16; ++kk)
+            tc_mma_ts_warp(t_o, t_p + 8 * kk, vb + 128 * kk, kIdPV, kk > 0 ? 1u : some);
+          some = 1;
         }
-        tc_fence_after();
-        const uint64_t kb = sdesc(smem_u32(sm.k[s]));
-#pragma unroll
-        for (int kk = 0; kk < kHeadDim / 16; ++kk) tc_mma(t_s, qa + 2 * kk, kb + 2 * kk, kIdQK, kk > 0);
-        // S of this tile; with it, every earlier product of the lane is done
-        tc_commit(&sm.s_full[li]);
-        if (!mbar_wait(&sm.p_full[li], n & 1, abort, a.err)) break;
-        tc_fence_after();
-        const uint64_t vb = sdesc(smem_u32(sm.v[s]));
-#pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          tc_mma_ts(t_o, t_s + 8 * kk, vb + 128 * kk, kIdPV, (n > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(&sm.kv_empty[s]);
-        ++n;
+        tc_commit_warp(&sm.pv_done[buf]);
+        tc_commit_warp(&sm.kv_empty[s]);
+        tc_commit_warp(&sm.o_done[l]);
+        if (buf == 0) phase[0] ^= 1;
+        else if (buf == 1) phase[1] ^= 1;
+        else phase[2] ^= 1;
+        buf = buf + 2 >= kSBufs ? buf + 2 - kSBufs : buf + 2;
+        s += MT == 2 ? 1 : 2;
+        if (s >= kS) {
+          s -= kS;
+          kv_phase ^= 1;
+        }
       }
-      tc_commit(&sm.done[li]);
-      mbar_wait(&sm.done[li], 0, abort, a.err, false);
+      tc_commit_warp(&sm.done[l]);
+      mbar_wait(&sm.done[l], 0, abort, a.err, false);
     }
-  } else if (warp < kSoftmaxWarps) {
+  } else {
     // ---------------------------------------------------------------- softmax
+    if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    const int li = warp >> 2, m_blk = MT == 2 ? li : 0;
     const int wq = warp & 3, r = wq * 32 + lane;           // row of the lane's 128
-    const uint32_t t_lane = (uint32_t)(wq * 32) << 16;
-    const uint32_t t_s = tmem + t_lane + 64 * li, t_o = tmem + t_lane + 256 + 64 * li;
-    const int p = t.pos0 + (w.r0 + 128 * m_blk + min(r, max(lrows, 1) - 1)) / G;
+    const LaneRows rows = lane_rows(a, sm.work, sm.pos0, m_blk);
+    const int p = sm.pos0 + (w.r0 + 128 * m_blk + min(r, max(rows.n, 1) - 1)) / G;
+    const uint32_t tmem = sm.tmem_base + ((uint32_t)(wq * 32) << 16);
+    const uint32_t t_o = tmem + kTmemO + 64 * li;
     const float sl2 = a.scale_log2;
+    const TokTiles tiles = sm.tiles;
+    const int j0 = sm.j0, nT = sm.n_tiles;
+    const int nX = MT == 2 ? 2 * ((nT + 1) / 2) : (nT + 1) / 2;
     float m_run = -INFINITY, l_run = 0.f;
-    uint32_t n = 0;
-    bool alive = true;
-    for (int j = part; j < nT; j += kParts) {
-      const int b = tok_tile(tiles, j0 + j) * kBN;
-      if (!lane_needs(b)) continue;
-      const uint64_t bits = tok_tile_full(b, lp0, lp1, a.window, a.sinks) ? ~0ull
-                                                                          : tok_mask(b, p, a.window, a.sinks);
-      if (!mbar_wait(&sm.s_full[li], n & 1, abort, a.err)) {
+    bool some = false, alive = true;
+    int buf = li;
+    uint32_t phase = 0;
+    const auto step = [&](int x) {               // the lane's flags of step x
+      const int i = MT == 2 ? x >> 1 : x;
+      if (i < kMaxFlags) return (int)sm.flags[i] >> (2 * m_blk);
+      return step_flags(tiles, j0, nT, i, rows.span, rows.span);
+    };
+    int f_next = li < nX ? step(li) : 0;
+    for (int x = li; x < nX; x += 2) {
+      const uint32_t t_s = tmem + kStep * buf;
+      const int i = MT == 2 ? x >> 1 : x;
+      const int f = f_next;
+      const bool whole = f & 2;
+      if (!mbar_wait_warp(&sm.s_full[buf], phase, abort, a.err)) {
         alive = false;
         break;
       }
-      tc_fence_after();
-      uint32_t pk[kBN / 2];
-      float sum0, sum1, alpha = 1.f;
-      bool rescale = false;
-      // P and its sum against the reference m_run
-      const auto exponentiate = [&]() {
-        const float m_ref = m_run == -INFINITY ? 0.f : m_run;
-        sum0 = sum1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < kBN; c += 32) {
-          float v[32];
-          PKV_TMEM_LD32(t_s + c, reinterpret_cast<uint32_t*>(v));
-          tmem_wait_ld();
-          if (bits != ~0ull) {
-            const uint32_t half = (uint32_t)(bits >> c);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((half >> i) & 1u)) v[i] = -INFINITY;
+      if (f & 1) {
+        tc_fence_after();
+        uint32_t pk[kStep / 2];
+        float sum0, sum1;
+        const auto tile_bits = [&](int j) {      // the row's view of the CTA's j-th tile
+          return j < nT ? tok_mask(tok_tile(tiles, j0 + j) * kTokTile, p, a.window, a.sinks) : 0ull;
+        };
+        // P and its sum against the reference m_run
+        const auto exponentiate = [&](auto masked) {
+          const float m_ref = m_run == -INFINITY ? 0.f : m_run;
+          uint64_t bits[2] = {0, 0};
+          if constexpr (masked) {
+            bits[0] = tile_bits(2 * i);
+            bits[1] = tile_bits(2 * i + 1);
           }
+          sum0 = sum1 = 0.f;
+          float v[2][32];
+          PKV_TMEM_LD32(t_s, reinterpret_cast<uint32_t*>(v[0]));
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float x, y;
-            fma2(x, y, v[i], v[i + 1], sl2, -m_ref);
-            x = fast_exp2(x);
-            y = fast_exp2(y);
-            pk[(c + i) >> 1] = pack_bf16(x, y);
-            add2(sum0, sum1, x, y);
+          for (int c = 0; c < kStep; c += 32) {
+            float (&u)[32] = v[(c >> 5) & 1];
+            tmem_wait_ld();
+            if (c + 32 < kStep) PKV_TMEM_LD32(t_s + c + 32, reinterpret_cast<uint32_t*>(v[((c >> 5) & 1) ^ 1]));
+            if constexpr (masked) {
+              const uint32_t part = (uint32_t)(bits[c >> 6] >> (c & 63));
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((part >> k) & 1u)) u[k] = -INFINITY;
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float e0, e1;
+              fma2(e0, e1, u[k], u[k + 1], sl2, -m_ref);
+              e0 = fast_exp2(e0);
+              e1 = fast_exp2(e1);
+              pk[(c + k) >> 1] = pack_bf16(e0, e1);
+              add2(sum0, sum1, e0, e1);
+            }
+          }
+        };
+        // a second pass, after the rows that need it have moved their reference
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          if (whole) exponentiate(std::false_type{});
+          else exponentiate(std::true_type{});
+          const bool redo = m_run == -INFINITY || !(sum0 + sum1 <= kSumLimit);
+          if (pass == 1 || !__any_sync(0xffffffffu, redo)) break;
+          // the row's maximum becomes its reference (S is still in TMEM)
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kStep; c += 16) {
+            float v[16];
+            PKV_TMEM_LD16(t_s + c, reinterpret_cast<uint32_t*>(v));
+            tmem_wait_ld();
+            const uint32_t part = (uint32_t)(tile_bits(2 * i + c / kTokTile) >> (c & 63));
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if ((part >> k) & 1u) mx = fmaxf(mx, v[k]);
+          }
+          mx *= sl2;
+          float alpha = 1.f;
+          bool rescale = false;
+          if (redo && mx > m_run) {
+            if (m_run != -INFINITY) {
+              alpha = fast_exp2(m_run - mx);
+              l_run *= alpha;
+              rescale = true;
+            }
+            m_run = mx;
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
+            // O moves to the new reference, once PV(x - 2) is done. A parity names a
+            // phase only when the one before it is over; PV(x - 6) is, since S(x) is.
+            const int n = x >> 1;
+            for (int k = max(0, n - 2); k < n && alive; ++k)
+              alive = mbar_wait_warp(&sm.o_done[li], k & 1, abort, a.err);
+            if (!alive) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kHeadDim; c += 16) {
+              uint32_t o[16];
+              PKV_TMEM_LD16(t_o + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              PKV_TMEM_ST16(t_o + c, o);
+            }
+            tmem_wait_st();
           }
         }
-      };
-      exponentiate();
-      const bool redo = m_run == -INFINITY || !(sum0 + sum1 <= kSumLimit);
-      if (__any_sync(0xffffffffu, redo)) {
-        // the row's maximum becomes its reference (S is still in TMEM)
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kBN; c += 32) {
-          float v[32];
-          PKV_TMEM_LD32(t_s + c, reinterpret_cast<uint32_t*>(v));
-          tmem_wait_ld();
-          const uint32_t half = (uint32_t)(bits >> c);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if ((half >> i) & 1u) mx = fmaxf(mx, v[i]);
-        }
-        mx *= sl2;
-        if (redo && mx > m_run) {
-          if (m_run != -INFINITY) {
-            alpha = fast_exp2(m_run - mx);
-            l_run *= alpha;
-            rescale = true;
-          }
-          m_run = mx;
-        }
-        exponentiate();
-      }
-      l_run += sum0 + sum1;
-      PKV_TMEM_ST32(t_s, pk);
-      tmem_wait_st();
-      if (__any_sync(0xffffffffu, rescale)) {
-        // S of this tile means that the lane's earlier products are done
-#pragma unroll
-        for (int c = 0; c < kHeadDim; c += 16) {
-          uint32_t o[16];
-          PKV_TMEM_LD16(t_o + c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          PKV_TMEM_ST16(t_o + c, o);
-        }
+        l_run += sum0 + sum1;
+        PKV_TMEM_ST32(t_s, pk);
+        PKV_TMEM_ST32(t_s + 32, (pk + 32));
+        if (x + 2 < nX) f_next = step(x + 2);
         tmem_wait_st();
+        some = true;
+        tc_fence_before();
+      } else if (x + 2 < nX) {
+        f_next = step(x + 2);
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[li]);
-      ++n;
+      mbar_arrive_if(&sm.p_full[li][buf], lane == 0);
+      // buffer and phase of x + 2
+      buf += 2;
+      if (buf >= kSBufs) {
+        buf -= kSBufs;
+        phase ^= 1;
+      }
     }
     alive = alive && mbar_wait(&sm.done[li], 0, abort, a.err);
     tc_fence_after();
-    if (kParts > 1) {
-      // ---- join the parts of the tiles: parts 1.. leave O, m and l to part 0
+    if (MT == 1) {
+      // ---- join the lanes: lane 1 leaves O, m and l to lane 0
       asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps * 32) : "memory");   // the ring is free
-      if (part > 0) {
+      if (li == 1) {
 #pragma unroll
         for (int c = 0; c < kHeadDim; c += 16) {
           uint32_t o[16];
           PKV_TMEM_LD16(t_o + c, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sm.o[li - MT][c + i][r] = n > 0 ? __uint_as_float(o[i]) : 0.f;
+          for (int k = 0; k < 16; ++k) sm.o[c + k][r] = some ? __uint_as_float(o[k]) : 0.f;
         }
-        sm.ml[li][r][0] = m_run;
-        sm.ml[li][r][1] = l_run;
+        sm.ml[r][0] = m_run;
+        sm.ml[r][1] = l_run;
       }
       asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps * 32) : "memory");
     }
-    if (alive && part == 0 && wq * 32 < lrows) {
-      float f0 = 1.f, fp[kParts];
-      if (kParts > 1) {
-        float mm = m_run;
-#pragma unroll
-        for (int i = 1; i < kParts; ++i) mm = fmaxf(mm, sm.ml[li + i * MT][r][0]);
-        const float ref = mm == -INFINITY ? 0.f : mm;
+    if (alive && (MT == 2 || li == 0) && wq * 32 < rows.n) {
+      float f0 = 1.f, f1 = 0.f;
+      if (MT == 1) {
+        const float m1 = sm.ml[r][0], mm = fmaxf(m_run, m1), ref = mm == -INFINITY ? 0.f : mm;
         f0 = fast_exp2(m_run - ref);
-        l_run *= f0;
-#pragma unroll
-        for (int i = 1; i < kParts; ++i) {
-          fp[i] = fast_exp2(sm.ml[li + i * MT][r][0] - ref);
-          l_run += fp[i] * sm.ml[li + i * MT][r][1];
-        }
+        f1 = fast_exp2(m1 - ref);
+        l_run = l_run * f0 + sm.ml[r][1] * f1;
         m_run = mm;
       }
-      const float inv = t.splits > 1 ? 1.f : (l_run > 0.f ? 1.f / l_run : 0.f);
+      const bool split = sm.splits > 1;
+      const float inv = split ? 1.f : (l_run > 0.f ? 1.f / l_run : 0.f);
       const int rr = w.r0 + 128 * m_blk + r;
       const long long pr = (long long)blockIdx.x * a.rows + 128 * m_blk + r;
-      uint16_t* out = a.out + ((long long)(t.row0 + rr / G) * a.heads * G + w.head * G + rr % G) * kHeadDim;
+      uint16_t* out = a.out + ((long long)(sm.row0 + rr / G) * a.heads * G + w.head * G + rr % G) * kHeadDim;
 #pragma unroll
       for (int c = 0; c < kHeadDim; c += 16) {
         uint32_t o[16];
@@ -447,45 +609,41 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1) token_tc_kernel(const __grid
         tmem_wait_ld();
         float f[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          f[i] = n > 0 ? __uint_as_float(o[i]) : 0.f;
-          if (kParts > 1) {
-            f[i] *= f0;
-#pragma unroll
-            for (int k = 1; k < kParts; ++k) f[i] += fp[k] * sm.o[k * MT + m_blk - MT][c + i][r];
-          }
-          f[i] *= inv;
+        for (int k = 0; k < 16; ++k) {
+          f[k] = some ? __uint_as_float(o[k]) : 0.f;
+          if (MT == 1) f[k] = f[k] * f0 + sm.o[c + k][r] * f1;
+          f[k] *= inv;
         }
-        if (r < lrows) {
-          if (t.splits == 1) {
+        if (r < rows.n) {
+          if (!split) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 8)
-              *reinterpret_cast<uint4*>(out + c + i) =
-                  make_uint4(pack_bf16(f[i], f[i + 1]), pack_bf16(f[i + 2], f[i + 3]),
-                             pack_bf16(f[i + 4], f[i + 5]), pack_bf16(f[i + 6], f[i + 7]));
+            for (int k = 0; k < 16; k += 8)
+              *reinterpret_cast<uint4*>(out + c + k) =
+                  make_uint4(pack_bf16(f[k], f[k + 1]), pack_bf16(f[k + 2], f[k + 3]),
+                             pack_bf16(f[k + 4], f[k + 5]), pack_bf16(f[k + 6], f[k + 7]));
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + c + i) =
-                  make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + c + k) =
+                  make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
           }
         }
       }
-      if (t.splits > 1 && r < lrows) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m_run, l_run);
+      if (split && r < rows.n) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m_run, l_run);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssuer0) {
+  if (warp == kIssueQK) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kTmemCols));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tmem_base), "r"(kTmemCols));
   }
 }
 
 template <int MT, bool FP8>
 cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
-  constexpr int smem = (int)sizeof(TcSmem<MT, FP8>) + 1024;
+  constexpr int smem = (int)sizeof(TcSmem<FP8>) + 1024;
   static_assert(smem <= 232448, "shared memory of a CTA");
   static std::atomic<unsigned long long> configured{0};   // a bit per device
   int dev = 0;
@@ -495,6 +653,10 @@ cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(token_tc_kernel<MT, FP8>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    // a warpgroup that asks for more registers than the launch brought would wait for ever
+    cudaFuncAttributes attr;
+    if (cudaError_t e2 = cudaFuncGetAttributes(&attr, token_tc_kernel<MT, FP8>)) return e2;
+    if (FP8 && attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
     if (dev < 64) configured.fetch_or(bit);
   }
   const cudaError_t e = launch_pdl(token_tc_kernel<MT, FP8>, dim3(a.ctas), dim3(kThreads<FP8>), smem, s, a);
@@ -505,9 +667,8 @@ cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s) {
-  if (a.pool.fp8)
-    return a.rows == 128 ? launch_tc<1, true>(a, s) : a.rows == 256 ? launch_tc<2, true>(a, s) : launch_tc<4, true>(a, s);
-  return a.rows == 128 ? launch_tc<1, false>(a, s) : a.rows == 256 ? launch_tc<2, false>(a, s) : launch_tc<4, false>(a, s);
+  if (a.pool.fp8) return a.rows == 128 ? launch_tc<1, true>(a, s) : launch_tc<2, true>(a, s);
+  return a.rows == 128 ? launch_tc<1, false>(a, s) : launch_tc<2, false>(a, s);
 }
 
 }  // namespace pkv

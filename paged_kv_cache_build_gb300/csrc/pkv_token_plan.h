@@ -119,6 +119,24 @@ PKV_HD bool tok_tile_full(int b, int p0, int p1, int window, int sinks) {
 PKV_HD uint64_t tok_low_bits(int n) {
   return n <= 0 ? 0ull : (n >= 64 ? ~0ull : ((1ull << n) - 1ull));
 }
+// The tiles (by number) that queries at positions p0 .. p1 see something of, and
+// those that all of them see whole.
+struct TokSpan {
+  int front, lo, hi;             // needed: t < front (and <= hi), or lo <= t <= hi
+  int full_front, f0, f1;        // whole: t < full_front, or f0 <= t < f1
+  PKV_HD bool needs(int t) const { return t <= hi && (t >= lo || t < front); }
+  PKV_HD bool whole(int t) const { return t < f1 && (t >= f0 || t < full_front); }
+};
+PKV_HD TokSpan tok_span(int p0, int p1, int window, int sinks) {
+  TokSpan s;
+  s.front = (sinks + kTokTile - 1) / kTokTile;
+  s.lo = tok_window_lo(p0, window) / kTokTile;
+  s.hi = p1 / kTokTile;
+  s.full_front = sinks / kTokTile;
+  s.f0 = (tok_window_lo(p1, window) + kTokTile - 1) / kTokTile;
+  s.f1 = (p0 + 1) / kTokTile;
+  return s;
+}
 // Bit i: whether slot b + i is seen from position p.
 PKV_HD uint64_t tok_mask(int b, int p, int window, int sinks) {
   return tok_low_bits(p - b + 1) & (~tok_low_bits(tok_window_lo(p, window) - b) | tok_low_bits(sinks - b));

@@ -15,8 +15,8 @@ namespace {
 
 constexpr int kMaxRows = 1 << 24;    // token rows of one call
 constexpr int kMaxGroup = 128;       // query heads per KV head
-// Split-KV partials: at most this many CTAs' rows (kernel CTAs of a call that
-// splits: see plan_splits), allocated when the first token stream opens.
+// Split-KV partials, allocated when the first token stream opens; plan_splits cuts
+// no finer than they hold.
 constexpr size_t kTokenScratchBytes = size_t(64) << 20;
 
 bool misaligned(const void* p) { return !p || !aligned16(p); }
@@ -69,39 +69,46 @@ void rows_args(pkv_t h, int layer, TokenRowsArgs* a) {
   a->err = h->d_err;
 }
 
-// Splits of the items' key ranges over CTAs, given each item's (block, KV head)
-// pairs and the tiles that its longest block sees, and the CTAs that run at once.
-// Each split costs a CTA's start (kStart tiles' time) and its share of the join,
-// so the ranges are cut as little as fills the card once: the largest piece length
-// L with sum(pairs * ceil(tiles / L)) within `slots`, and no cut below kMinPiece.
-constexpr int kMinPiece = 8;
-void plan_splits(TokenAttendArgs* a, const int* tiles, int slots) {
-  long long pairs = 0;
+// What a kernel's CTA costs, in the time of one 64-slot tile: its start and end, and
+// (when it leaves partial results) their share of the join. As measured: decode steps
+// take 0.25 us a tile and 3 us a CTA, the matrix-unit kernel 0.5 us and 5 us.
+struct CtaCost {
+  int slots;                     // CTAs that run at once
+  int fixed, join;
+  int min_piece;                 // tiles below which a range is not cut
+  int max_ctas;                  // whose partial results the scratch holds
+};
+
+// Splits of the items' key ranges over CTAs, given the tiles that an item's first
+// and last block see. All ranges are cut into pieces of one length (at most); of the
+// lengths most/1, most/2, .. the one whose waves of CTAs are estimated to end first.
+void plan_splits(TokenAttendArgs* a, const int* first, const int* last, const CtaCost& c) {
   int most = 1;
-  for (int i = 0; i < a->n; ++i) {
-    pairs += (long long)a->item[i].blocks * a->heads;
-    most = std::max(most, tiles[i]);
-  }
-  const auto ctas = [&](int piece) {
-    long long c = 0;
-    for (int i = 0; i < a->n; ++i)
-      c += (long long)a->item[i].blocks * a->heads * ceil_div(tiles[i], piece);
-    return c;
-  };
-  int piece = most;
-  if (pairs < slots) {
-    int lo = std::min(kMinPiece, most), hi = most;     // ctas(hi) fits
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (ctas(mid) <= slots) hi = mid;
-      else lo = mid + 1;
+  for (int i = 0; i < a->n; ++i) most = std::max({most, first[i], last[i]});
+  int best = most;
+  double best_t = 0;
+  for (int s = 1; s == 1 || most / s >= c.min_piece; ++s) {
+    const int piece = ceil_div(most, s);
+    double ctas = 0, work = 0;
+    for (int i = 0; i < a->n; ++i) {
+      const double pairs = (double)a->item[i].blocks * a->heads;
+      const int splits = ceil_div(std::max(first[i], last[i]), piece);
+      ctas += pairs * splits;
+      work += pairs * (0.5 * (first[i] + last[i]) + splits * (c.fixed + (splits > 1 ? c.join : 0)));
     }
-    piece = lo;
+    if (s > 1 && ctas > c.max_ctas) break;
+    const double waves = std::max(1.0, std::ceil(ctas / c.slots));
+    const double t = std::max(waves * work / ctas, (double)piece + c.fixed);
+    if (s == 1 || t < best_t * 0.97) {
+      best_t = t;
+      best = piece;
+    }
+    if (ctas > 8.0 * c.slots || s >= 64) break;
   }
   int cta = 0;
   for (int i = 0; i < a->n; ++i) {
     TokenQuery& t = a->item[i];
-    t.splits = std::max(1, ceil_div(tiles[i], piece));
+    t.splits = std::max(1, ceil_div(std::max(first[i], last[i]), best));
     t.cta0 = cta;
     cta += t.blocks * a->heads * t.splits;
   }
@@ -343,7 +350,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   const float scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt((float)h->D);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = h->d_err;
-  int tiles[kMaxTokenBatch];
+  int first[kMaxTokenBatch], last[kMaxTokenBatch];
   for (int i = 0; i < n; ++i) {
     const Stream& st = h->streams[sids[i]];
     const TokenCounts& t = st.tok;
@@ -367,13 +374,13 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   std::copy(a.item, a.item + n_items, all);
   for (int pass = 0; pass < 2; ++pass) {         // the first grows the scratch, if it must
     size_t need = 0;
-    for (const int shape : {kTokenFewRows, 128, 256, 512}) {
-      const int below = shape == kTokenFewRows ? 0 : shape == 128 ? kTokenFewRows : shape / 2;
+    for (const int shape : {kTokenFewRows, 128, 256}) {
+      const int below = shape == kTokenFewRows ? 0 : shape == 128 ? kTokenFewRows : 128;
       a.n = 0;
       int most = 0;
       for (int i = 0; i < n_items; ++i) {
         const long long r = (long long)all[i].n * group;
-        if (r <= below || (r > shape && shape < 512)) continue;
+        if (r <= below || (r > shape && shape < 256)) continue;
         a.item[a.n++] = all[i];
         most = std::max(most, (int)std::min<long long>(r, shape));
       }
@@ -383,14 +390,17 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
       for (int i = 0; i < a.n; ++i) {
         TokenQuery& it = a.item[i];
         it.blocks = ceil_div((long long)it.n * group, a.rows);
-        // the longest table of the item's blocks: the last one's, without a window
-        tiles[i] = 0;
-        for (int b : {0, it.blocks - 1}) {
+        const auto block_tiles = [&](int b) {
           const int r0 = b * a.rows, r1 = std::min(r0 + a.rows, it.n * group) - 1;
-          tiles[i] = std::max(tiles[i], tok_tiles(it.pos0 + r0 / group, it.pos0 + r1 / group, window, sinks).n);
-        }
+          return tok_tiles(it.pos0 + r0 / group, it.pos0 + r1 / group, window, sinks).n;
+        };
+        first[i] = block_tiles(0);
+        last[i] = block_tiles(it.blocks - 1);
       }
-      plan_splits(&a, tiles, h->num_sms * (few ? token_few_ctas_per_sm(a.rows) : 1));
+      const int room = (int)(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)));
+      const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(a.rows), 10, 2, 4, room}
+                               : CtaCost{h->num_sms, 10, 4, 8, room};
+      plan_splits(&a, first, last, cost);
       bool split = false;
       for (int i = 0; i < a.n; ++i) split = split || a.item[i].splits > 1;
       if (split) {

@@ -123,7 +123,7 @@ constexpr int kTokenFewRows = 32;
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s);
 // Resident CTAs per SM of that kernel.
 int token_few_ctas_per_sm(int rows);
-// Attention of 128, 256 or 512 query rows per CTA (a.rows), one CTA per SM.
+// Attention of 128 or 256 query rows per CTA (a.rows), one CTA per SM.
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s);
 // Joins the splits of the items that have several.
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s);

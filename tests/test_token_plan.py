@@ -123,6 +123,20 @@ def test_tiles_and_masks(plan):
             want_full = bool(every[b:b + 64].all()) and b + 64 <= len(every)
             got_full = bool(plan.plan_full(b, p0, p1, window, sinks))
             assert not got_full or want_full
+            assert bool(plan.plan_whole(tile, p0, p1, window, sinks)) == got_full
+            assert bool(plan.plan_needs(tile, p0, p1, window, sinks)) >= bool(seen[b:b + 64].any())
+            if got_full:
+                assert plan.plan_needs(tile, p0, p1, window, sinks)
+        # part of the rows: no tile that they see is left out
+        q0 = rng.randrange(p0, p1 + 1)
+        q1 = rng.randrange(q0, p1 + 1)
+        part = np.zeros(p1 + 65, dtype=bool)
+        for p in range(q0, q1 + 1):
+            part |= visible(p, p1 + 65, window, sinks)
+        for tile in sorted(set((np.flatnonzero(part) // 64).tolist())):
+            assert plan.plan_needs(tile, q0, q1, window, sinks) and tile in tiles
+        for tile in tiles:
+            b = tile * 64
             for p in {p0, p1, (p0 + p1) // 2}:
                 bits = plan.plan_mask(b, p, window, sinks)
                 want = visible(p, b + 64, window, sinks)[b:]

@@ -42,5 +42,7 @@ int plan_tiles(int p0, int p1, int window, int sinks, int* out, int cap) {
   return r.n;
 }
 int plan_full(int b, int p0, int p1, int window, int sinks) { return tok_tile_full(b, p0, p1, window, sinks); }
+int plan_needs(int tile, int p0, int p1, int window, int sinks) { return tok_span(p0, p1, window, sinks).needs(tile); }
+int plan_whole(int tile, int p0, int p1, int window, int sinks) { return tok_span(p0, p1, window, sinks).whole(tile); }
 unsigned long long plan_mask(int b, int p, int window, int sinks) { return tok_mask(b, p, window, sinks); }
 }
