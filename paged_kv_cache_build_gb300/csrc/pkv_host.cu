@@ -308,6 +308,7 @@ pkv_status pkv_destroy(pkv_t h) {
   if (h->d_err) cudaFree(h->d_err);
   if (h->d_scratch) cudaFree(h->d_scratch);
   if (h->d_select) cudaFree(h->d_select);
+  if (h->d_joined) cudaFree(h->d_joined);
   if (h->d_km) cudaFree(h->d_km);
   if (h->d_km_len) cudaFree(h->d_km_len);
   delete h;

@@ -11,9 +11,9 @@
 // producer warp keeps a ring of 64-slot tiles filled by bulk copies (the pages are
 // stored as ready operands, so a block of slots is one copy of K and one of V); each
 // of four warps takes every fourth tile whole, holds its own m, sum and O, and the
-// four are joined at the end. Long tables are split over CTAs, whose partial
-// results a second kernel joins. The products run on warp-level matrix
-// instructions with the 8 to 32 query rows on the N side: S^T = K Q^T and
+// four are joined at the end. Long tables are split over CTAs; the one that ends last
+// of a row block's splits joins their partial results. The products run on warp-level matrix
+// instructions with the 8 or 16 query rows on the N side: S^T = K Q^T and
 // O^T += V^T P^T.
 //
 // bf16 pages: P is rounded to bf16 (2^-9 relative) for the second product. E4M3
@@ -34,30 +34,28 @@ namespace {
 
 constexpr int kWarps = 4;                        // consumer warps
 constexpr int kThreads = (kWarps + 1) * 32;      // and the producer
-constexpr int kBlocks = kTokTile / 16;           // page blocks in a tile, at most
 
 template <bool FP8>
 constexpr int kTileBytes = FP8 ? kTokTile * (kHeadDim + 1) : kTokTile * kHeadDim * 2;   // K or V
-// Two CTAs an SM with about 96 KB of tiles each; 32 rows need a register file of
-// their own (one CTA, twice the ring).
-template <int NT>
-constexpr int kCtasPerSm = NT == 4 ? 1 : 2;
-template <int NT, bool FP8>
-constexpr int kRing = (FP8 ? 11 : 6) * (2 / kCtasPerSm<NT>);
+// Two CTAs an SM with about 96 KB of tiles each
+constexpr int kCtasPerSm = 2;
+template <bool FP8>
+constexpr int kRing = FP8 ? 11 : 6;
 
 template <int NT, bool FP8>
 struct __align__(1024) FewSmem {
   union {
     struct {
-      uint8_t k[kRing<NT, FP8>][kTileBytes<FP8>];
-      uint8_t v[kRing<NT, FP8>][kTileBytes<FP8>];
+      uint8_t k[kRing<FP8>][kTileBytes<FP8>];
+      uint8_t v[kRing<FP8>][kTileBytes<FP8>];
     };
     float o[kWarps][NT * 8][kHeadDim];           // after the last tile: the warps' O
   };
   float ml[kWarps][NT * 8][2];
-  uint64_t full[kRing<NT, FP8>];
-  uint64_t empty[kRing<NT, FP8>];
+  uint64_t full[kRing<FP8>];
+  uint64_t empty[kRing<FP8>];
   int abort;
+  int last;
 };
 
 __device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -88,13 +86,59 @@ __device__ __forceinline__ float max8(float x) {   // over the 8 lanes of a quer
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
 
+// Values d .. d + 3 of a row whose splits' partial results start at row pr0:
+// o = sum_s 2^(m_s - M) o_s, l = sum_s 2^(m_s - M) l_s, M = max_s m_s, in order.
+template <int kFold>
+__device__ __forceinline__ float4 join_splits(const TokenAttendArgs& a, long long pr0, int splits, int d,
+                                              float* l_out) {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < splits; s0 += kFold) {
+    float2 ml[kFold];
+    float4 ov[kFold];
+#pragma unroll
+    for (int k = 0; k < kFold; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + k < splits) {
+        const long long pr = pr0 + (long long)(s0 + k) * a.rows;
+        ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + pr * 2));
+        ov[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + pr * kHeadDim + d));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFold; ++k) {
+      if (!(ml[k].y > 0.f)) continue;
+      const float m_new = fmaxf(m, ml[k].x);
+      const float c = fast_exp2(m - m_new), w = fast_exp2(ml[k].x - m_new);
+      l = l * c + w * ml[k].y;
+      o.x = o.x * c + w * ov[k].x;
+      o.y = o.y * c + w * ov[k].y;
+      o.z = o.z * c + w * ov[k].z;
+      o.w = o.w * c + w * ov[k].w;
+      m = m_new;
+    }
+  }
+  *l_out = l;
+  return o;
+}
+// Values d .. d + 3 of the CTA's row r, divided by the row's sum.
+__device__ __forceinline__ void write_row(const TokenAttendArgs& a, const TokenQuery& t, const TokenWork& w, int r,
+                                          int d, const float4& o, float l) {
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const int rr = w.r0 + r;
+  uint16_t* dst = a.out + ((long long)(t.row0 + rr / a.group) * a.heads * a.group + w.head * a.group +
+                           rr % a.group) * kHeadDim + d;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+}
+
 template <int NT, bool FP8>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     token_few_kernel(const __grid_constant__ TokenAttendArgs a) {
   extern __shared__ uint8_t smem_raw[];
   FewSmem<NT, FP8>& sm = *reinterpret_cast<FewSmem<NT, FP8>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  constexpr int kS = kRing<NT, FP8>;
+  constexpr int kS = kRing<FP8>;
   static_assert(kS > kWarps, "the order of the stages' releases");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -119,48 +163,47 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>)
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
-    const int rows = Ps >= kTokTile ? kTokTile : Ps;     // slots per block
-    const int per = kTokTile / rows;
+    // The page blocks of the next 32 / per tiles, one per lane: their addresses are
+    // worked out together, and a tile then costs a wait and its lanes' copies.
+    const int rows = min(Ps, kTokTile);                  // slots per block
+    const int per = kTokTile / rows, group = 32 / per;
     const uint32_t block_bytes = (uint32_t)kTileBytes<FP8> / per;
-    // byte offset of a slot block in a (kv, head) plane, and of this head's planes
-    const long long row_bytes = FP8 ? kHeadDim + 1 : 2 * kHeadDim;
-    const long long plane = (long long)Ps * row_bytes;
-    int batch = -1, ids = 0, issued = 0;
-    for (int j = 0; j < nT; ++j) {
-      const int s = j % kS;
-      if (!mbar_wait(&sm.empty[s], ((j / kS) & 1) ^ 1, abort, a.err)) break;
-      const int b = tok_tile(tiles, j0 + j) * kTokTile;
-      if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2u * kTileBytes<FP8>);
-#pragma unroll
-      for (int pp = 0; pp < kBlocks; ++pp) {
-        if (pp >= per) break;
-        const int f = b + pp * rows;
+    constexpr long long kRowBytes = FP8 ? kHeadDim + 1 : 2 * kHeadDim;
+    const long long plane = (long long)Ps * kRowBytes;   // of a head's K or V in a page
+    const uint32_t dst = (lane % per) * block_bytes;     // the lane's block in a tile
+    int issued = 0;
+    for (int base = 0; base < nT && issued == base; base += group) {
+      const uint8_t* src = nullptr;
+      if (base + lane / per < nT) {
+        const int f = tok_tile(tiles, j0 + base + lane / per) * kTokTile + (lane % per) * rows;
         // blocks behind the last page repeat it: their slots are masked
-        const int e = min(f / Ps, t.n_pages - 1);
-        if ((e >> 5) != batch) {                 // the next 32 page ids, one per lane
-          batch = e >> 5;
-          const int i = batch * 32 + lane;
-          ids = i < t.n_pages ? t.pages[i] : 0;
+        const int e = f / Ps;
+        int page = t.pages[min(e, t.n_pages - 1)];
+        if (page < 0 || page >= a.pool.pool_pages) {
+          atomicOr(a.err, kErrPageRange);
+          page = 0;
         }
-        int page = __shfl_sync(0xffffffffu, ids, e & 31);
-        if (lane == 0) {
-          if (page < 0 || page >= a.pool.pool_pages) {
-            atomicOr(a.err, kErrPageRange);
-            page = 0;
-          }
-          const uint8_t* src = reinterpret_cast<const uint8_t*>(a.pool.base) +
-                               (long long)page * a.pool.page_bytes + w.head * plane + (f % Ps) * row_bytes;
+        src = reinterpret_cast<const uint8_t*>(a.pool.base) + (long long)page * a.pool.page_bytes +
+              w.head * plane + (f - e * Ps) * kRowBytes;
+      }
+      const int end = min(nT, base + group);
+      for (int j = base; j < end; ++j) {
+        const int s = j % kS;
+        if (!mbar_wait(&sm.empty[s], ((j / kS) & 1) ^ 1, abort, a.err)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], 2u * kTileBytes<FP8>);
+        __syncwarp();
+        if (lane / per == j - base) {
           const uint32_t bar = smem_u32(&sm.full[s]);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv)
             asm volatile(
                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, "
-                "[%3];\n" ::"r"(smem_u32((kv ? sm.v[s] : sm.k[s]) + pp * block_bytes)),
+                "[%3];\n" ::"r"(smem_u32(kv ? sm.v[s] : sm.k[s]) + dst),
                 "l"(src + kv * a.pool.heads * plane), "r"(block_bytes), "r"(bar)
                 : "memory");
         }
+        issued = j + 1;
       }
-      issued = j + 1;
     }
     // no copy may still be landing when the ring is used for the join
     if (lane == 0)
@@ -412,7 +455,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>)
       }
   }
   __syncthreads();
-  if (*abort) return;
   // 16 lanes a row, 4 values a lane
   for (int x = threadIdx.x; x < w.rows * 16; x += kThreads) {
     const int r = x >> 4, d = (x & 15) * 4;
@@ -432,21 +474,35 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<NT>)
       ov.w += f * p.w;
     }
     if (t.splits == 1) {
-      const float inv = ll > 0.f ? 1.f / ll : 0.f;
-      const int rr = w.r0 + r;
-      uint16_t* dst = a.out + ((long long)(t.row0 + rr / a.group) * a.heads * a.group +
-                               w.head * a.group + rr % a.group) * kHeadDim + d;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(ov.x * inv, ov.y * inv), pack_bf16(ov.z * inv, ov.w * inv));
+      write_row(a, t, w, r, d, ov, ll);
     } else {
       const long long pr = (long long)blockIdx.x * a.rows + r;
-      *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + d) = ov;
-      if (d == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(mm, ll);
+      __stcg(reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + d), ov);
+      if (d == 0) __stcg(reinterpret_cast<float2*>(a.part_ml + pr * 2), make_float2(mm, ll));
     }
+  }
+  if (t.splits == 1) return;
+  // ---- the CTA that ends last of its splits joins them, in their order
+  __threadfence();
+  __syncthreads();
+  const int cta0 = blockIdx.x - w.split;
+  if (threadIdx.x == 0) {
+    const unsigned before = atomicAdd(a.joined + cta0, 1u);
+    sm.last = before == (unsigned)t.splits - 1u;
+    if (sm.last) a.joined[cta0] = 0;             // for the next call
+  }
+  __syncthreads();
+  if (!sm.last) return;
+  __threadfence();
+  for (int x = threadIdx.x; x < w.rows * 16; x += kThreads) {
+    const int r = x >> 4, d = (x & 15) * 4;
+    float l = 0.f;
+    const float4 o = join_splits<12>(a, (long long)cta0 * a.rows + r, t.splits, d, &l);
+    write_row(a, t, w, r, d, o, l);
   }
 }
 
-// Joins the splits: o = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s, M = max_s m_s,
-// 16 threads a (token, query head), the splits in order.
+// For the matrix-unit kernel's splits: 16 threads a (token, query head).
 __global__ void __launch_bounds__(256) token_combine_kernel(const __grid_constant__ TokenAttendArgs a,
                                                             long long pairs) {
   pdl_wait();
@@ -464,36 +520,8 @@ __global__ void __launch_bounds__(256) token_combine_kernel(const __grid_constan
   const int r = (row - t.row0) * a.group + qh % a.group;
   const int block = r / a.rows;
   const int cta = t.cta0 + ((t.blocks - 1 - block) * a.heads + head) * t.splits;
-  const long long pr0 = (long long)cta * a.rows + r % a.rows;
-  constexpr int kFold = 8;
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < t.splits; s0 += kFold) {
-    float2 ml[kFold];
-    float4 ov[kFold];
-#pragma unroll
-    for (int k = 0; k < kFold; ++k) {
-      ml[k] = make_float2(-INFINITY, 0.f);
-      ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s0 + k < t.splits) {
-        const long long pr = pr0 + (long long)(s0 + k) * a.rows;
-        ml[k] = __ldg(reinterpret_cast<const float2*>(a.part_ml + pr * 2));
-        ov[k] = __ldg(reinterpret_cast<const float4*>(a.part_o + pr * kHeadDim + d));
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kFold; ++k) {
-      if (!(ml[k].y > 0.f)) continue;
-      const float m_new = fmaxf(m, ml[k].x);
-      const float c = fast_exp2(m - m_new), w = fast_exp2(ml[k].x - m_new);
-      l = l * c + w * ml[k].y;
-      o.x = o.x * c + w * ov[k].x;
-      o.y = o.y * c + w * ov[k].y;
-      o.z = o.z * c + w * ov[k].z;
-      o.w = o.w * c + w * ov[k].w;
-      m = m_new;
-    }
-  }
+  float l = 0.f;
+  const float4 o = join_splits<8>(a, (long long)cta * a.rows + r % a.rows, t.splits, d, &l);
   const float inv = l > 0.f ? 1.f / l : 0.f;
   *reinterpret_cast<uint2*>(a.out + ((long long)row * H + qh) * kHeadDim + d) =
       make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
@@ -502,7 +530,7 @@ __global__ void __launch_bounds__(256) token_combine_kernel(const __grid_constan
 template <int NT, bool FP8>
 cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
   constexpr int smem = (int)sizeof(FewSmem<NT, FP8>) + 1024;
-  static_assert((smem + 1024) * kCtasPerSm<NT> <= 228 * 1024, "shared memory per SM");
+  static_assert((smem + 1024) * kCtasPerSm <= 228 * 1024, "shared memory per SM");
   static std::atomic<unsigned long long> configured{0};   // a bit per device
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
@@ -520,12 +548,11 @@ cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int token_few_ctas_per_sm(int rows) { return rows == 32 ? kCtasPerSm<4> : kCtasPerSm<1>; }
+int token_few_ctas_per_sm() { return kCtasPerSm; }
 
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s) {
-  if (a.pool.fp8)
-    return a.rows == 8 ? launch_few<1, true>(a, s) : a.rows == 16 ? launch_few<2, true>(a, s) : launch_few<4, true>(a, s);
-  return a.rows == 8 ? launch_few<1, false>(a, s) : a.rows == 16 ? launch_few<2, false>(a, s) : launch_few<4, false>(a, s);
+  if (a.pool.fp8) return a.rows == 8 ? launch_few<1, true>(a, s) : launch_few<2, true>(a, s);
+  return a.rows == 8 ? launch_few<1, false>(a, s) : launch_few<2, false>(a, s);
 }
 
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s) {

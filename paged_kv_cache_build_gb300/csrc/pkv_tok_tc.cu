@@ -254,41 +254,45 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1) token_tc_kernel(const __grid
     const int nT = sm.n_tiles, j0 = sm.j0, n_pages = sm.n_pages, head = w.head;
     const TokTiles tiles = sm.tiles;
     const int32_t* pages = sm.pages;
+    // The page blocks of the next 32 / per steps, one per lane: their addresses are
+    // worked out together, and a step then costs a wait and its lanes' copies.
     const int rows = min(Ps, kTokTile);                  // slots per block
-    const int per = kTokTile / rows;
+    const int half_blocks = kTokTile / rows, per = 2 * half_blocks, group = 32 / per;
     constexpr uint32_t kOperand = FP8 ? kCodeBytes : kTokTile * 128;   // bytes of K or V in a tile
     constexpr int kRingN = FP8 ? kCodeRing : kS;
     uint64_t* const full = FP8 ? sm.code_full : sm.kv_full;
     uint64_t* const empty = FP8 ? sm.code_empty : sm.kv_empty;
-    const uint32_t block_bytes = kOperand / per;
+    const uint32_t block_bytes = kOperand / half_blocks;
     constexpr long long kRowBytes = FP8 ? kHeadDim + 1 : 2 * kHeadDim;
-    const long long plane = (long long)Ps * kRowBytes;
+    const long long plane = (long long)Ps * kRowBytes;   // of a head's K or V in a page
     const int nS = (nT + 1) / 2;
-    int batch = -1, ids = 0, issued = 0;
-    for (int i = 0; i < nS; ++i) {
-      const int s = i % kRingN;
-      if (!mbar_wait(&empty[s], ((i / kRingN) & 1) ^ 1, abort, a.err)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&full[s], 4u * kOperand);
-      const uint32_t bar = smem_u32(&full[s]);
-      for (int x = 0; x < 2 * per; ++x) {
-        const int half = x / per, pp = x - half * per;
+    // the lane's block: of the step's tile `half`, its pp-th
+    const int half = lane % per / half_blocks, pp = lane % half_blocks;
+    int issued = 0;
+    for (int base = 0; base < nS && issued == base; base += group) {
+      const uint8_t* src = nullptr;
+      if (base + lane / per < nS) {
         // a last step of one tile takes it twice: the second is masked
-        const int f = tok_tile(tiles, j0 + min(2 * i + half, nT - 1)) * kTokTile + pp * rows;
+        const int j = min(2 * (base + lane / per) + half, nT - 1);
+        const int f = tok_tile(tiles, j0 + j) * kTokTile + pp * rows;
         // blocks behind the last page repeat it: their slots are masked
-        const int e = min(f / Ps, n_pages - 1);
-        if ((e >> 5) != batch) {                 // the next 32 page ids, one per lane
-          batch = e >> 5;
-          const int at = batch * 32 + lane;
-          ids = at < n_pages ? pages[at] : 0;
+        const int e = f / Ps;
+        int page = pages[min(e, n_pages - 1)];
+        if (page < 0 || page >= a.pool.pool_pages) {
+          atomicOr(a.err, kErrPageRange);
+          page = 0;
         }
-        int page = __shfl_sync(0xffffffffu, ids, e & 31);
-        if (lane == 0) {
-          if (page < 0 || page >= a.pool.pool_pages) {
-            atomicOr(a.err, kErrPageRange);
-            page = 0;
-          }
-          const uint8_t* src = reinterpret_cast<const uint8_t*>(a.pool.base) +
-                               (long long)page * a.pool.page_bytes + head * plane + (f % Ps) * kRowBytes;
+        src = reinterpret_cast<const uint8_t*>(a.pool.base) + (long long)page * a.pool.page_bytes +
+              head * plane + (f - e * Ps) * kRowBytes;
+      }
+      const int end = min(nS, base + group);
+      for (int i = base; i < end; ++i) {
+        const int s = i % kRingN;
+        if (!mbar_wait(&empty[s], ((i / kRingN) & 1) ^ 1, abort, a.err)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], 4u * kOperand);
+        __syncwarp();
+        if (lane / per == i - base) {
+          const uint32_t bar = smem_u32(&full[s]);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             uint8_t* dst = FP8 ? sm.code[s] + (2 * half + kv) * kCodeBytes
@@ -300,8 +304,8 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1) token_tc_kernel(const __grid
                 : "memory");
           }
         }
+        issued = i + 1;
       }
-      issued = i + 1;
     }
     // no copy may still be landing when the CTA joins or ends
     if (lane == 0)

@@ -19,6 +19,8 @@ constexpr int kMaxGroup = 128;       // query heads per KV head
 // no finer than they hold.
 constexpr size_t kTokenScratchBytes = size_t(64) << 20;
 
+constexpr int kTokenJoins = 16384;   // counters of the splits' joins
+
 bool misaligned(const void* p) { return !p || !aligned16(p); }
 
 // The batch's streams, each named once and a token stream; row offsets that start
@@ -163,6 +165,15 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
   st.tbl_cap = (int)std::min<size_t>(cap, (size_t)h->P);
   const size_t words = cap + 2 * (size_t)st.tbl_cap;
   if (pkv_status r = ensure_scratch(h, kTokenScratchBytes)) return r;
+  if (!h->d_joined) {
+    unsigned* p = nullptr;
+    PKV_CUDA(h, cudaMalloc(&p, kTokenJoins * sizeof(unsigned)));
+    if (cudaError_t e2 = cudaMemset(p, 0, kTokenJoins * sizeof(unsigned))) {
+      cudaFree(p);
+      return cuda_fail(h, e2, "stream_open_tokens cudaMemset");
+    }
+    h->d_joined = p;
+  }
   cudaError_t e = cudaMalloc(&st.d_mem, words * sizeof(int32_t));
   if (e != cudaSuccess) return cuda_fail(h, e, "stream_open_tokens cudaMalloc");
   e = cudaMemset(st.d_mem, 0, words * sizeof(int32_t));
@@ -386,7 +397,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
       }
       if (a.n == 0) continue;
       const bool few = shape == kTokenFewRows;
-      a.rows = !few ? shape : most <= 8 ? 8 : most <= 16 ? 16 : kTokenFewRows;
+      a.rows = !few ? shape : most <= 8 ? 8 : kTokenFewRows;
       for (int i = 0; i < a.n; ++i) {
         TokenQuery& it = a.item[i];
         it.blocks = ceil_div((long long)it.n * group, a.rows);
@@ -397,8 +408,8 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
         first[i] = block_tiles(0);
         last[i] = block_tiles(it.blocks - 1);
       }
-      const int room = (int)(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)));
-      const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(a.rows), 10, 2, 4, room}
+      const int room = std::min<int>(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
+      const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 10, 2, 4, room}
                                : CtaCost{h->num_sms, 10, 4, 8, room};
       plan_splits(&a, first, last, cost);
       bool split = false;
@@ -408,10 +419,11 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
         need = std::max(need, rows * (kHeadDim + 2) * sizeof(float));
         a.part_o = h->d_scratch;
         a.part_ml = h->d_scratch + rows * kHeadDim;
+        a.joined = h->d_joined;
       }
       if (pass == 0) continue;
       PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, s));
-      if (split) PKV_CUDA(h, launch_token_combine(a, s));
+      if (split && !few) PKV_CUDA(h, launch_token_combine(a, s));
     }
     if (pass == 0)
       if (pkv_status r = ensure_scratch(h, need)) return r;
