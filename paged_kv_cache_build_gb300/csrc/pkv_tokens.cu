@@ -167,8 +167,8 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
   if (pkv_status r = ensure_scratch(h, kTokenScratchBytes)) return r;
   if (!h->d_joined) {
     unsigned* p = nullptr;
-    PKV_CUDA(h, cudaMalloc(&p, kTokenJoins * sizeof(unsigned)));
-    if (cudaError_t e2 = cudaMemset(p, 0, kTokenJoins * sizeof(unsigned))) {
+    PKV_CUDA(h, cudaMalloc(&p, (kTokenJoins + 2) * sizeof(unsigned)));
+    if (cudaError_t e2 = cudaMemset(p, 0, (kTokenJoins + 2) * sizeof(unsigned))) {
       cudaFree(p);
       return cuda_fail(h, e2, "stream_open_tokens cudaMemset");
     }
@@ -361,6 +361,8 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   const float scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt((float)h->D);
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = h->d_err;
+  a.joined = h->d_joined;
+  a.tickets = h->d_joined + kTokenJoins;
   int first[kMaxTokenBatch], last[kMaxTokenBatch];
   for (int i = 0; i < n; ++i) {
     const Stream& st = h->streams[sids[i]];
@@ -419,10 +421,9 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
         need = std::max(need, rows * (kHeadDim + 2) * sizeof(float));
         a.part_o = h->d_scratch;
         a.part_ml = h->d_scratch + rows * kHeadDim;
-        a.joined = h->d_joined;
       }
       if (pass == 0) continue;
-      PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, s));
+      PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, h->num_sms, s));
       if (split && !few) PKV_CUDA(h, launch_token_combine(a, s));
     }
     if (pass == 0)

@@ -245,6 +245,28 @@ def test_rows_of_very_different_size(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 5, 40, 130, 700])
+def test_scores_that_grow(new, fp8):
+    """Scores that rise by about one factor of two from key to key: every step moves
+    the references of all rows, and what was summed before with them."""
+    p = Pool(300, 16, 2, fp8, seed=new)
+    sid, n = p.open(3000), 2000 + new
+    g = torch.Generator(device="cuda").manual_seed(new)
+    u = torch.where(torch.rand((1, 2, 64), generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    k = (u * (torch.arange(n, device="cuda") / 100.0).view(-1, 1, 1)).bfloat16()
+    v = torch.randn((n, 2, 64), generator=g, device="cuda").bfloat16()
+    q = (u.repeat_interleave(2, 1) * 8 + torch.randn((new, 4, 64), generator=g, device="cuda")).bfloat16()
+    p.cache.append_tokens(p.cache.token_batch([sid], [n]), k, v)
+    out = p.cache.attend_tokens(p.cache.token_batch([sid], [new]), q)
+    p.cache.sync()
+    kk, vv, qq = stored(k, fp8), stored(v, fp8), f64(q)
+    ref = causal_attend_fp64(qq, kk, vv, 2000, 0, 0, SCALE)
+    err = np.abs(f64(out) - ref)
+    assert (err <= tolerance(qq, kk, vv, ref, 2000, 0, 0, SCALE)).all()
+    p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 def test_a_served_run(fp8):
     """Prompts, single tokens, drafts accepted in part, eviction, a stream closed and
     its pages used again, over two layers: the pages follow the oracle, and every
