@@ -60,10 +60,11 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
 // Drain waits (in-flight copies and MMAs before TMEM is freed) pass
 // honor_abort = false: they are bounded but never cut short.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          int* err, bool honor_abort = true) {
+                                          int* err, bool honor_abort = true,
+                                          uint32_t limit = kSpinLimit) {
   const uint32_t addr = smem_u32(bar);
   if (mbar_test(addr, parity)) return true;
-  for (uint32_t i = 0; i < kSpinLimit; ++i) {
+  for (uint32_t i = 0; i < limit; ++i) {
     if (mbar_try_wait(addr, parity)) return true;
     if ((i & 255u) == 255u) {
       if (honor_abort && *abort) return false;

@@ -167,8 +167,8 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
   if (pkv_status r = ensure_scratch(h, kTokenScratchBytes)) return r;
   if (!h->d_joined) {
     unsigned* p = nullptr;
-    PKV_CUDA(h, cudaMalloc(&p, (kTokenJoins + 2) * sizeof(unsigned)));
-    if (cudaError_t e2 = cudaMemset(p, 0, (kTokenJoins + 2) * sizeof(unsigned))) {
+    PKV_CUDA(h, cudaMalloc(&p, kTokenJoins * sizeof(unsigned)));
+    if (cudaError_t e2 = cudaMemset(p, 0, kTokenJoins * sizeof(unsigned))) {
       cudaFree(p);
       return cuda_fail(h, e2, "stream_open_tokens cudaMemset");
     }
@@ -362,7 +362,6 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = h->d_err;
   a.joined = h->d_joined;
-  a.tickets = h->d_joined + kTokenJoins;
   int first[kMaxTokenBatch], last[kMaxTokenBatch];
   for (int i = 0; i < n; ++i) {
     const Stream& st = h->streams[sids[i]];
@@ -387,13 +386,13 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   std::copy(a.item, a.item + n_items, all);
   for (int pass = 0; pass < 2; ++pass) {         // the first grows the scratch, if it must
     size_t need = 0;
-    for (const int shape : {kTokenFewRows, 128, 256}) {
-      const int below = shape == kTokenFewRows ? 0 : shape == 128 ? kTokenFewRows : 128;
+    for (const int shape : {kTokenFewRows, 128, 256, 512}) {
+      const int below = shape == kTokenFewRows ? 0 : shape == 128 ? kTokenFewRows : shape / 2;
       a.n = 0;
       int most = 0;
       for (int i = 0; i < n_items; ++i) {
         const long long r = (long long)all[i].n * group;
-        if (r <= below || (r > shape && shape < 256)) continue;
+        if (r <= below || (r > shape && shape < 512)) continue;
         a.item[a.n++] = all[i];
         most = std::max(most, (int)std::min<long long>(r, shape));
       }
@@ -423,7 +422,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
         a.part_ml = h->d_scratch + rows * kHeadDim;
       }
       if (pass == 0) continue;
-      PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, h->num_sms, s));
+      PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, s));
       if (split && !few) PKV_CUDA(h, launch_token_combine(a, s));
     }
     if (pass == 0)

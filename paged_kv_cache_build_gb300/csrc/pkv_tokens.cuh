@@ -71,7 +71,6 @@ struct TokenAttendArgs {
   float scale_log2;                 // sm_scale * log2(e)
   float* part_o;                    // [cta][rows][64], unnormalised
   float* part_ml;                   // [cta][rows][2]: max (log2 units) and sum
-  unsigned* tickets;                // [2]: items taken, CTAs that have ended; 0 between calls
   unsigned* joined;                 // [cta]: splits of the row block that have ended; 0 between calls
   int* err;
   int n;
@@ -125,9 +124,8 @@ constexpr int kTokenFewRows = 16;
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s);
 // Resident CTAs per SM of that kernel.
 int token_few_ctas_per_sm();
-// Attention of 128 or 256 query rows at a time (a.rows), a CTA per SM that takes the
-// a.ctas items one after the other.
-cudaError_t launch_token_tc(const TokenAttendArgs& a, int num_sms, cudaStream_t s);
+// Attention of 128, 256 or 512 query rows per CTA (a.rows), one CTA per SM.
+cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s);
 // Joins the splits of the items that have several (launch_token_few does so itself).
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s);
 
