@@ -25,8 +25,7 @@ __device__ __forceinline__ int page_of(const TokenRowsArgs& a, const TokenRows& 
   return page;
 }
 
-// U quads per warp: the source rows of all of them are loaded before any is stored.
-template <int U>
+// Few rows: a warp per quad and plane.
 __global__ void __launch_bounds__(kWarps * 32) token_append_kernel(const __grid_constant__ TokenRowsArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -34,35 +33,33 @@ __global__ void __launch_bounds__(kWarps * 32) token_append_kernel(const __grid_
   const int H2 = 2 * a.pool.heads, Ps = a.pool.page_size;
   const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int hh = (int)(w % H2);
-  const long long unit0 = w / H2 * (kQuad * U) + (lane >> 3);
+  const long long unit = w / H2 * kQuad + (lane >> 3);
+  if (unit >= a.units) return;                   // the same for the 8 lanes of a token
   const int kv = hh >= a.pool.heads ? 1 : 0, h = hh - kv * a.pool.heads;
-  const uint16_t* src = kv ? a.v : a.k;
-  const long long stride = kv ? a.v_stride : a.k_stride;
-  uint4 val[U];
-  int at[U], pos[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long unit = unit0 + u * kQuad;
-    at[u] = -1;
-    val[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (unit >= a.units) continue;
-    at[u] = find_item<TokenRows, &TokenRows::unit0>(a.item, a.n, (int)unit);
-    const TokenRows& it = a.item[at[u]];
-    const int i = (int)unit - it.unit0;
-    pos[u] = it.pos0 + i;
-    if (i < it.n)
-      val[u] = __ldg(reinterpret_cast<const uint4*>(src + (it.row0 + i) * stride + h * kHeadDim + c * 8));
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (at[u] < 0) continue;         // the same for the 8 lanes of a token
-    const TokenRows& it = a.item[at[u]];
-    const int pi = pos[u] / Ps, slot = pos[u] - pi * Ps;
-    const int page = page_of(a, it, pi);
-    if (page < 0) continue;
-    if (a.is_meta && slot == 0 && hh == 0 && c == 0) it.pages[pi] = page;
-    store_row_chunk(a.pool, page, kv, h, slot, c, val[u]);
-  }
+  const TokenRows& it = a.item[find_item<TokenRows, &TokenRows::unit0>(a.item, a.n, (int)unit)];
+  const int i = (int)unit - it.unit0, pos = it.pos0 + i;
+  uint4 val = make_uint4(0u, 0u, 0u, 0u);
+  if (i < it.n)
+    val = __ldg(reinterpret_cast<const uint4*>((kv ? a.v : a.k) + (it.row0 + i) * (kv ? a.v_stride : a.k_stride) +
+                                               h * kHeadDim + c * 8));
+  const int pi = pos / Ps, slot = pos - pi * Ps;
+  const int page = page_of(a, it, pi);
+  if (page < 0) return;
+  if (a.is_meta && slot == 0 && hh == 0 && c == 0) it.pages[pi] = page;
+  store_row_chunk(a.pool, page, kv, h, slot, c, val);
+}
+
+// Two codes (the low bytes) to a bf16 pair times sc, a power of two. Exact: a code has
+// 4 significant bits.
+__device__ __forceinline__ uint32_t decode2(uint32_t pair, float sc) {
+  uint32_t f, r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(f) : "h"((uint16_t)pair));
+  float lo, hi;
+  asm("{\n .reg .f16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n"
+      : "=f"(lo), "=f"(hi)
+      : "r"(f));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi * sc), "f"(lo * sc));
+  return r;
 }
 
 // Chunk c (values 8 c .. 8 c + 7) of a stored row, as bf16.
@@ -78,21 +75,10 @@ __device__ __forceinline__ uint4 load_row_chunk(const PoolView& pv, int page, in
   const float sc = __uint_as_float((uint32_t)(127 + e) << 23);   // 2^e, |e| <= 126
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint16_t pair = (uint16_t)((i < 2 ? codes.x : codes.y) >> (16 * (i & 1)));
-    uint32_t f;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(f) : "h"(pair));
-    float lo, hi;
-    asm("{\n .reg .f16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n"
-        : "=f"(lo), "=f"(hi)
-        : "r"(f));
-    // exact: a code has 4 significant bits
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(w[i]) : "f"(hi * sc), "f"(lo * sc));
-  }
+  for (int i = 0; i < 4; ++i) w[i] = decode2((i < 2 ? codes.x : codes.y) >> (16 * (i & 1)), sc);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int U>
 __global__ void __launch_bounds__(kWarps * 32) token_read_kernel(const __grid_constant__ TokenRowsArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -100,31 +86,178 @@ __global__ void __launch_bounds__(kWarps * 32) token_read_kernel(const __grid_co
   const int H2 = 2 * a.pool.heads, Ps = a.pool.page_size;
   const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int hh = (int)(w % H2);
-  const long long unit0 = w / H2 * (kQuad * U) + (lane >> 3);
+  const long long unit = w / H2 * kQuad + (lane >> 3);
+  if (unit >= a.units) return;
   const int kv = hh >= a.pool.heads ? 1 : 0, h = hh - kv * a.pool.heads;
-  uint4 val[U];
-  long long row[U];
-  int page[U], slot[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long unit = unit0 + u * kQuad;
-    page[u] = -1;
-    if (unit >= a.units) continue;
-    const TokenRows& it = a.item[find_item<TokenRows, &TokenRows::unit0>(a.item, a.n, (int)unit)];
-    const int i = (int)unit - it.unit0;
-    const int pos = it.pos0 + i, pi = pos / Ps;
-    slot[u] = pos - pi * Ps;
-    row[u] = it.row0 + i;
-    page[u] = page_of(a, it, pi);
+  const TokenRows& it = a.item[find_item<TokenRows, &TokenRows::unit0>(a.item, a.n, (int)unit)];
+  const int i = (int)unit - it.unit0, pos = it.pos0 + i, pi = pos / Ps;
+  const int page = page_of(a, it, pi);
+  if (page < 0) return;
+  uint16_t* const dst = (kv ? a.v : a.k) + ((long long)(it.row0 + i) * a.pool.heads + h) * kHeadDim + c * 8;
+  *reinterpret_cast<uint4*>(dst) = load_row_chunk(a.pool, page, kv, h, pos - pi * Ps, c);
+}
+
+// Many rows: a block takes 32 tokens and works out their places in the pages once; its
+// warps go over the (K or V, head) planes, the rows of two planes on their way before
+// the first is stored.
+constexpr int kManyTokens = 32;
+
+// Places of a block's tokens in plane 0 (K of head 0): code or row, exponent byte, and
+// the token's row in the packed tensors (-1: zeros).
+struct Places {
+  uint8_t* row[kManyTokens];         // null: no token
+  uint8_t* exp[kManyTokens];
+  int src[kManyTokens];
+  int slot[kManyTokens];
+};
+
+template <bool READ>
+__device__ __forceinline__ void find_places(const TokenRowsArgs& a, Places& p) {
+  if (threadIdx.x < kManyTokens) {
+    const int unit = blockIdx.x * kManyTokens + threadIdx.x, Ps = a.pool.page_size;
+    uint8_t *row = nullptr, *exp = nullptr;
+    int src = -1, slot = 0;
+    if (unit < a.units) {
+      const TokenRows& it = a.item[find_item<TokenRows, &TokenRows::unit0>(a.item, a.n, unit)];
+      const int i = unit - it.unit0, pos = it.pos0 + i, pi = pos / Ps;
+      const int page = page_of(a, it, pi);
+      slot = pos - pi * Ps;
+      if (i < it.n) src = it.row0 + i;
+      if (page >= 0) {
+        uint8_t* const base = reinterpret_cast<uint8_t*>(a.pool.base) + (long long)page * a.pool.page_bytes;
+        row = base + (a.pool.fp8 ? fp8_code_off(a.pool.heads, Ps, 0, 0, slot) : (long long)slot * kHeadDim * 2);
+        exp = base + fp8_exp_off(a.pool.heads, Ps, 0, 0, slot);
+        if (!READ && a.is_meta && slot == 0) it.pages[pi] = page;
+      }
+    }
+    p.row[threadIdx.x] = row;
+    p.exp[threadIdx.x] = exp;
+    p.src[threadIdx.x] = src;
+    p.slot[threadIdx.x] = slot;
   }
+  __syncthreads();
+}
+
+// Eight bf16 values to E4M3 codes of v * 2^-e (fp8_row_exponent's e, of the row that 8
+// neighbouring lanes hold), with all arithmetic on pairs. The largest magnitude's bits
+// as an integer are E * 128 + mantissa, and e = E - 135, one more where the mantissa is
+// above 0.75: a carry. v * 2^-e is exact in bf16 but for values that no code reaches.
+__device__ __forceinline__ uint2 quantise8(const uint4& val, int* e_out) {
+  const uint32_t w[4] = {val.x, val.y, val.z, val.w};
+  uint32_t big = 0;
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (page[u] >= 0) val[u] = load_row_chunk(a.pool, page[u], kv, h, slot[u], c);
-  uint16_t* dst = kv ? a.v : a.k;
-  const long long stride = (long long)a.pool.heads * kHeadDim;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t mag = w[i] & 0x7FFF7FFFu;
+    asm("max.bf16x2 %0, %0, %1;\n" : "+r"(big) : "r"(mag));
+  }
+  const unsigned group = 0xFFu << (threadIdx.x & 24);
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (page[u] >= 0) *reinterpret_cast<uint4*>(dst + row[u] * stride + h * kHeadDim + c * 8) = val[u];
+  for (int d = 1; d < 8; d <<= 1) {
+    const uint32_t other = __shfl_xor_sync(group, big, d);
+    asm("max.bf16x2 %0, %0, %1;\n" : "+r"(big) : "r"(other));
+  }
+  const int top = max((int)(big & 0xFFFFu), (int)(big >> 16));
+  const int e = top == 0 ? 0 : max(((top + 31) >> 7) - 135, -126);
+  *e_out = e;
+  const uint32_t s1 = (uint32_t)(127 - e) << 7, scale = s1 | (s1 << 16);   // 2^-e, -120 <= -e <= 126
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x;
+    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(x) : "r"(w[i]), "r"(scale));
+    c[i] = fp8_pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kWarps * 32) token_append_many_kernel(const __grid_constant__ TokenRowsArgs a) {
+  __shared__ Places p;
+  pdl_wait();
+  pdl_trigger();
+  find_places<false>(a, p);
+  const int lane = threadIdx.x & 31, c = lane & 7, t0 = lane >> 3, H = a.pool.heads;
+  const long long plane = (long long)a.pool.page_size * (FP8 ? kHeadDim + 1 : 2 * kHeadDim);
+  constexpr int kU = kManyTokens / kQuad;
+  for (int hh = threadIdx.x >> 5; hh < 2 * H; hh += kWarps) {
+    const int kv = hh >= H ? 1 : 0, h = hh - kv * H;
+    const long long stride = kv ? a.v_stride : a.k_stride;
+    const uint16_t* const rows = (kv ? a.v : a.k) + h * kHeadDim + c * 8;
+    uint4 val[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int src = p.src[u * kQuad + t0];
+      val[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (src >= 0) val[u] = __ldg(reinterpret_cast<const uint4*>(rows + src * stride));
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int t = u * kQuad + t0;
+      uint8_t* const row = p.row[t];
+      if (FP8) {
+        int e;
+        const uint2 codes = quantise8(val[u], &e);
+        if (row) *reinterpret_cast<uint2*>(row + hh * plane + 8 * c) = codes;
+        if (row && c == 0) p.exp[t][hh * plane] = (uint8_t)(int8_t)e;
+      } else if (row) {
+        *reinterpret_cast<uint4*>(row + hh * plane + (swizzle_chunk(p.slot[t], c) << 4)) = val[u];
+      }
+    }
+  }
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kWarps * 32) token_read_many_kernel(const __grid_constant__ TokenRowsArgs a) {
+  __shared__ Places p;
+  pdl_wait();
+  pdl_trigger();
+  find_places<true>(a, p);
+  const int lane = threadIdx.x & 31, H = a.pool.heads;
+  const long long plane = (long long)a.pool.page_size * (FP8 ? kHeadDim + 1 : 2 * kHeadDim);
+  const long long stride = (long long)H * kHeadDim;
+  // lanes of 16 bytes in the page: 4 a row of codes, 8 a row of bf16
+  constexpr int kPer = FP8 ? 4 : 8, kRows = 32 / kPer, kU = kManyTokens / kRows;
+  const int c = lane % kPer, t0 = lane / kPer;
+  constexpr int kPlanes = FP8 ? 2 : 1;         // on their way at a time
+  for (int h0 = (threadIdx.x >> 5) * kPlanes; h0 < 2 * H; h0 += kWarps * kPlanes) {
+    uint4 val[kPlanes][kU];
+    int exps[kPlanes];
+#pragma unroll
+    for (int q = 0; q < kPlanes; ++q) {        // 2 H planes: pairs are whole
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int t = u * kRows + t0;
+        const uint8_t* const row = p.row[t] + (h0 + q) * plane;
+        if (p.row[t])
+          val[q][u] = *reinterpret_cast<const uint4*>(row + ((FP8 ? c : swizzle_chunk(p.slot[t], c)) << 4));
+      }
+      if (FP8) exps[q] = p.exp[lane] ? (int)(int8_t)p.exp[lane][(h0 + q) * plane] : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < kPlanes; ++q) {
+      const int hh = h0 + q, kv = hh >= H ? 1 : 0, h = hh - kv * H;
+      uint16_t* const rows = (kv ? a.v : a.k) + h * kHeadDim + c * (FP8 ? 16 : 8);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int t = u * kRows + t0;
+        uint16_t* const dst = rows + p.src[t] * stride;
+        if (FP8) {
+          const int e = __shfl_sync(0xffffffffu, exps[q], t);
+          const float sc = __uint_as_float((uint32_t)(127 + e) << 23);   // 2^e, |e| <= 126
+          const uint32_t w[4] = {val[q][u].x, val[q][u].y, val[q][u].z, val[q][u].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = decode2(w[i >> 1] >> (16 * (i & 1)), sc);
+          if (p.row[t]) {
+            *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+        } else if (p.row[t]) {
+          *reinterpret_cast<uint4*>(dst) = val[q][u];
+        }
+      }
+    }
+  }
 }
 
 __global__ void __launch_bounds__(256) token_drop_kernel(const __grid_constant__ TokenDropArgs a) {
@@ -141,31 +274,33 @@ __global__ void __launch_bounds__(256) token_drop_kernel(const __grid_constant__
   }
 }
 
-// Above this many (token, K or V, head) rows each warp takes several quads.
-constexpr long long kManyRows = 152LL * 2 * kWarps * kQuad * 4;
+// Tokens from which a block takes 32 of them: enough blocks to fill the SMs. (Below, a
+// warp per quad and plane: 64 single tokens of 8 heads take 4.2 us instead of TODO.)
+constexpr int kManyUnits = 152 * 16;
 
-template <int U>
 int row_blocks(const TokenRowsArgs& a) {
-  const long long warps = ((long long)a.units + kQuad * U - 1) / (kQuad * U) * 2 * a.pool.heads;
+  const long long warps = ((long long)a.units + kQuad - 1) / kQuad * 2 * a.pool.heads;
   return (int)((warps + kWarps - 1) / kWarps);
 }
 
 }  // namespace
 
 cudaError_t launch_token_append(const TokenRowsArgs& a, cudaStream_t s) {
-  const bool many = 2LL * a.units * a.pool.heads >= kManyRows;
-  const cudaError_t e =
-      many ? launch_pdl(token_append_kernel<4>, dim3(row_blocks<4>(a)), dim3(kWarps * 32), 0, s, a)
-           : launch_pdl(token_append_kernel<1>, dim3(row_blocks<1>(a)), dim3(kWarps * 32), 0, s, a);
+  const bool many = a.units >= kManyUnits;
+  const int blocks = many ? (a.units + kManyTokens - 1) / kManyTokens : row_blocks(a);
+  auto* const kernel = !many ? token_append_kernel
+                       : a.pool.fp8 ? token_append_many_kernel<true> : token_append_many_kernel<false>;
+  const cudaError_t e = launch_pdl(kernel, dim3(blocks), dim3(kWarps * 32), 0, s, a);
   count_launches(1);
   return e;
 }
 
 cudaError_t launch_token_read(const TokenRowsArgs& a, cudaStream_t s) {
-  const bool many = 2LL * a.units * a.pool.heads >= kManyRows;
-  const cudaError_t e =
-      many ? launch_pdl(token_read_kernel<4>, dim3(row_blocks<4>(a)), dim3(kWarps * 32), 0, s, a)
-           : launch_pdl(token_read_kernel<1>, dim3(row_blocks<1>(a)), dim3(kWarps * 32), 0, s, a);
+  const bool many = a.units >= kManyUnits;
+  const int blocks = many ? (a.units + kManyTokens - 1) / kManyTokens : row_blocks(a);
+  auto* const kernel = !many ? token_read_kernel
+                       : a.pool.fp8 ? token_read_many_kernel<true> : token_read_many_kernel<false>;
+  const cudaError_t e = launch_pdl(kernel, dim3(blocks), dim3(kWarps * 32), 0, s, a);
   count_launches(1);
   return e;
 }

@@ -202,6 +202,40 @@ def test_read_back(page, fp8):
     p.cache.close()
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("page,heads", [(16, 3), (256, 1), (64, 5)])
+def test_many_rows_written_and_read(page, heads, fp8):
+    """Thousands of rows in a call, ragged, from strided tensors, of every size that a
+    bf16 row may have, over pages that were used before."""
+    from paged_kv_cache_build_gb300 import PagedKVCache
+    counts = [1800, 0, 7, 1501, 333]
+    n = sum(counts)
+    cache = PagedKVCache(sum(-(-c // page) for c in counts) + 1, page, heads, fp8=fp8)
+    g = torch.Generator(device="cuda").manual_seed(page)
+    both = torch.randn((n, 2 * heads + 1, 64), generator=g, device="cuda")
+    both *= torch.exp2(torch.randint(-120, 119, (n, 2 * heads + 1, 1), generator=g, device="cuda").float())
+    both *= torch.exp2(torch.randint(-12, 1, (n, 2 * heads + 1, 64), generator=g, device="cuda").float())
+    both = both.bfloat16()
+    both[5] = 0
+    k, v = both[:, :heads], both[:, heads:2 * heads]
+    for turn in range(2):
+        sids = [cache.open_token_stream(c + 1) for c in counts]
+        batch = cache.token_batch(sids, counts)
+        cache.append_tokens(batch, k, v)
+        # one row further: its page's other slots, zeros or old rows, are not read
+        cache.append_tokens(cache.token_batch(sids[:1], [1]), k[:1], v[:1])
+        kk, vv = cache.read_tokens(batch, [0] * len(counts))
+        np.testing.assert_array_equal(f64(kk), stored(k, fp8))
+        np.testing.assert_array_equal(f64(vv), stored(v, fp8))
+        one, _ = cache.read_tokens(cache.token_batch(sids[:1], [1]))
+        np.testing.assert_array_equal(f64(one), stored(k[:1], fp8))
+        cache.sync()
+        for s in sids:
+            cache.close_stream(s)
+        k, v = v, k
+    cache.close()
+
+
 def test_quantised_extremes_round_trip():
     """Rows of zeros, of one value, of the largest and smallest magnitudes, at the
     borders of the exponent: the stored codes are the oracle's."""
