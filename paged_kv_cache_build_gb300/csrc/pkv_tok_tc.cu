@@ -208,17 +208,28 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
   pdl_trigger();
 
   if (warp < kProducer) {
-    // Q rows as swizzled operand tiles; rows behind the last one as zeros
-    for (int i = threadIdx.x; i < MT * 128 * 8; i += kQThreads) {
-      const int r = i >> 3, c = i & 7;
-      uint4 val = make_uint4(0u, 0u, 0u, 0u);
-      if (r < w.rows) {
-        const int rr = w.r0 + r;
-        val = __ldg(reinterpret_cast<const uint4*>(a.q + (sm.row0 + rr / G) * a.q_stride +
-                                                   (w.head * G + rr % G) * kHeadDim + c * 8));
+    // Q rows as swizzled operand tiles, all on their way at once; rows behind the last
+    // one as zeros
+    // (row r + kQThreads / 8 is dt tokens and dm members of the group further)
+    constexpr int kStepRows = kQThreads / 8;
+    const int c = threadIdx.x & 7, dt = kStepRows / G, dm = kStepRows - dt * G;
+    int r = threadIdx.x >> 3, tok = (w.r0 + r) / G, mem = w.r0 + r - tok * G;
+    for (; r < MT * 128; r += kStepRows) {
+      const bool there = r < w.rows;
+      const uint16_t* src = a.q;
+      if (there) src += (sm.row0 + tok) * a.q_stride + (w.head * G + mem) * kHeadDim + c * 8;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                       smem_u32(&sm.q[r >> 7][(r & 127) * 128 + (swizzle_chunk(r & 7, c) << 4)])),
+                   "l"(src), "r"(there ? 16 : 0)
+                   : "memory");
+      tok += dt;
+      mem += dm;
+      if (mem >= G) {
+        mem -= G;
+        ++tok;
       }
-      *reinterpret_cast<uint4*>(&sm.q[r >> 7][(r & 127) * 128 + (swizzle_chunk(r & 7, c) << 4)]) = val;
     }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
     fence_proxy_async();
     asm volatile("bar.sync 1, %0;\n" ::"r"(kQThreads) : "memory");
   }
@@ -530,42 +541,63 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
         }
         m_run = mm;
       }
-      const float inv = sm.splits > 1 ? 1.f : (l_run > 0.f ? 1.f / l_run : 0.f);
+      const bool split = sm.splits > 1;
+      const float inv = split ? 1.f : (l_run > 0.f ? 1.f / l_run : 0.f);
       const int rr = w.r0 + 128 * m_blk + r;
       const long long pr = (long long)blockIdx.x * a.rows + 128 * m_blk + r;
-      uint16_t* out = a.out + ((long long)(sm.row0 + rr / G) * a.heads * G + w.head * G + rr % G) * kHeadDim;
+      // the row's place in out, or in the partial results
+      uint8_t* const row_out =
+          split ? reinterpret_cast<uint8_t*>(a.part_o + pr * kHeadDim)
+                : reinterpret_cast<uint8_t*>(
+                      a.out + ((long long)(sm.row0 + rr / G) * a.heads * G + w.head * G + rr % G) * kHeadDim);
+      // A thread has a row, but a warp writes rows of 128 bytes by 8 lanes each (a store of
+      // 32 lanes to 32 rows costs 32 cycles): through the row block's Q tile, which no
+      // product reads any more. bf16 rows go in one pass, fp32 partials in two.
+      uint8_t* const stage = sm.q[m_blk] + wq * 32 * 128;
+      const int n_rows = min(32, rows.n - wq * 32);
+      for (int half = 0; half < (split ? 2 : 1); ++half) {
+#pragma unroll 1
+        for (int c = 0; c < (split ? 32 : kHeadDim); c += 16) {
+          const int col = 32 * half + c;
+          uint32_t o[16];
+          PKV_TMEM_LD16(t_o + col, o);
+          tmem_wait_ld();
+          float f[16];
 #pragma unroll
-      for (int c = 0; c < kHeadDim; c += 16) {
-        uint32_t o[16];
-        PKV_TMEM_LD16(t_o + c, o);
-        tmem_wait_ld();
-        float f[16];
+          for (int i = 0; i < 16; ++i) {
+            f[i] = n > 0 ? __uint_as_float(o[i]) : 0.f;
+            if (kParts > 1) {
+              f[i] *= f0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          f[i] = n > 0 ? __uint_as_float(o[i]) : 0.f;
-          if (kParts > 1) {
-            f[i] *= f0;
-#pragma unroll
-            for (int k = 1; k < kParts; ++k) f[i] += fp[k] * sm.o[k * MT + m_blk - MT][c + i][r];
+              for (int k = 1; k < kParts; ++k) f[i] += fp[k] * sm.o[k * MT + m_blk - MT][col + i][r];
+            }
+            f[i] *= inv;
           }
-          f[i] *= inv;
-        }
-        if (r < rows.n) {
-          if (sm.splits == 1) {
+          if (!split) {
 #pragma unroll
             for (int i = 0; i < 16; i += 8)
-              *reinterpret_cast<uint4*>(out + c + i) =
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (swizzle_chunk(lane, (c + i) >> 3) << 4)) =
                   make_uint4(pack_bf16(f[i], f[i + 1]), pack_bf16(f[i + 2], f[i + 3]),
                              pack_bf16(f[i + 4], f[i + 5]), pack_bf16(f[i + 6], f[i + 7]));
           } else {
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(a.part_o + pr * kHeadDim + c + i) =
+              *reinterpret_cast<float4*>(stage + lane * 128 + (swizzle_chunk(lane, (c + i) >> 2) << 4)) =
                   make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
           }
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 4 * i + (lane >> 3);
+          uint8_t* const to = reinterpret_cast<uint8_t*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row_out), row));
+          const uint4 val = *reinterpret_cast<const uint4*>(stage + row * 128 + (swizzle_chunk(row, lane & 7) << 4));
+          if (row < n_rows) *reinterpret_cast<uint4*>(to + 128 * half + 16 * (lane & 7)) = val;
+        }
+        __syncwarp();
       }
-      if (sm.splits > 1 && r < rows.n) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m_run, l_run);
+      if (split && r < rows.n) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m_run, l_run);
     }
   }
 
