@@ -37,25 +37,24 @@ constexpr int kThreads = (kWarps + 1) * 32;      // and the producer
 
 template <bool FP8>
 constexpr int kTileBytes = FP8 ? kTokTile * (kHeadDim + 1) : kTokTile * kHeadDim * 2;   // K or V
-// CTAs an SM, with about 200 KB of tiles between them. E4M3 tiles take more
-// instructions a byte: a third CTA's warps hide their latency (NT = 1: 37.7 -> TODO us).
-template <int NT, bool FP8>
-constexpr int kCtasPerSm = FP8 && NT == 1 ? 3 : 2;
-template <int NT, bool FP8>
-constexpr int kRing = FP8 ? (NT == 1 ? 8 : 11) : 6;
+// Two CTAs an SM with about 96 KB of tiles each. (A third one on E4M3 pages, at 128
+// registers, measured the same.)
+constexpr int kCtasPerSm = 2;
+template <bool FP8>
+constexpr int kRing = FP8 ? 11 : 6;
 
 template <int NT, bool FP8>
 struct __align__(1024) FewSmem {
   union {
     struct {
-      uint8_t k[kRing<NT, FP8>][kTileBytes<FP8>];
-      uint8_t v[kRing<NT, FP8>][kTileBytes<FP8>];
+      uint8_t k[kRing<FP8>][kTileBytes<FP8>];
+      uint8_t v[kRing<FP8>][kTileBytes<FP8>];
     };
     float o[kWarps][NT * 8][kHeadDim];           // after the last tile: the warps' O
   };
   float ml[kWarps][NT * 8][2];
-  uint64_t full[kRing<NT, FP8>];
-  uint64_t empty[kRing<NT, FP8>];
+  uint64_t full[kRing<FP8>];
+  uint64_t empty[kRing<FP8>];
   int abort;
   int last;
 };
@@ -135,12 +134,12 @@ __device__ __forceinline__ void write_row(const TokenAttendArgs& a, const TokenQ
 }
 
 template <int NT, bool FP8>
-__global__ void __launch_bounds__(kThreads, (kCtasPerSm<NT, FP8>))
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     token_few_kernel(const __grid_constant__ TokenAttendArgs a) {
   extern __shared__ uint8_t smem_raw[];
   FewSmem<NT, FP8>& sm = *reinterpret_cast<FewSmem<NT, FP8>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  constexpr int kS = kRing<NT, FP8>;
+  constexpr int kS = kRing<FP8>;
   static_assert(kS > kWarps, "the order of the stages' releases");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -532,7 +531,7 @@ __global__ void __launch_bounds__(256) token_combine_kernel(const __grid_constan
 template <int NT, bool FP8>
 cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
   constexpr int smem = (int)sizeof(FewSmem<NT, FP8>) + 1024;
-  static_assert((smem + 1024) * kCtasPerSm<NT, FP8> <= 228 * 1024, "shared memory per SM");
+  static_assert((smem + 1024) * kCtasPerSm <= 228 * 1024, "shared memory per SM");
   static std::atomic<unsigned long long> configured{0};   // a bit per device
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
@@ -550,7 +549,7 @@ cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int token_few_ctas_per_sm(int rows, bool fp8) { return rows == 8 && fp8 ? kCtasPerSm<1, true> : kCtasPerSm<2, true>; }
+int token_few_ctas_per_sm() { return kCtasPerSm; }
 
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s) {
   if (a.pool.fp8) return a.rows == 8 ? launch_few<1, true>(a, s) : launch_few<2, true>(a, s);

@@ -410,7 +410,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
         last[i] = block_tiles(it.blocks - 1);
       }
       const int room = std::min<int>(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
-      const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(a.rows, h->fp8), 20, 4, 8, room}
+      const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 20, 4, 8, room}
                                : CtaCost{h->num_sms, 10, 4, 8, room};
       plan_splits(&a, first, last, cost);
       bool split = false;

@@ -123,7 +123,7 @@ cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s);
 constexpr int kTokenFewRows = 16;
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s);
 // Resident CTAs per SM of that kernel.
-int token_few_ctas_per_sm(int rows, bool fp8);
+int token_few_ctas_per_sm();
 // Attention of 128, 256 or 512 query rows per CTA (a.rows), one CTA per SM.
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s);
 // Joins the splits of the items that have several (launch_token_few does so itself).
