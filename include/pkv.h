@@ -456,7 +456,8 @@ pkv_status pkv_attend_noalloc(pkv_t h, const void* q, int n_q, int stream_id, in
  * with that window, except those that hold the first `sinks` tokens; such streams
  * are for attention with a window of at most that size on every layer. window = 0
  * keeps every token. Allocates the page list (4 bytes per page of max_tokens) and,
- * once per handle, 64 MiB of split-KV scratch, so that no token call allocates.
+ * once per handle, 64 MiB for split attention calls, which stay where they are until
+ * pkv_destroy (pkv_scratch_info does not count them), so that no token call allocates.
  * Errors: INVALID (null argument, max_tokens outside 1 .. 2^28, negative window or
  * sinks, sinks above max_tokens or without a window), OOM (max_streams already
  * open), CUDA (the allocation failed). */
@@ -504,10 +505,10 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* stream_ids, const int* pos
  * stream's first `sinks` tokens stay visible beside it.
  * q: device bf16 [row_off[n]][q_heads][64], rows q_stride apart; out: the same,
  * contiguous. fp32 accumulation and softmax; the probabilities are rounded to bf16
- * (bf16 pages) or f16 (E4M3 pages, q rounded to f16 as well) for the second
- * product. sm_scale <= 0 means 1 / sqrt(64). Results depend on the batch only by
+ * for the second product, or, in streams with up to 64 rows x query heads per KV head
+ * on E4M3 pages, to f16 (and q as well). sm_scale <= 0 means 1 / sqrt(64). Results depend on the batch only by
  * rounding (the split of the keys is chosen for the whole call) and are the same
- * bits for the same call. The handle's scratch is shared by its calls: order them
+ * bits for the same call. The handle's partial results are shared by its calls: order them
  * on one CUDA stream.
  * Errors: INVALID (shape, stride, layer, q_heads, negative window or sinks, sinks
  * without a window, a null or unaligned pointer), STATE (not a token stream; more

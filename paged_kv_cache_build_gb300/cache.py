@@ -50,6 +50,8 @@ class TokenBatch:
             raise ValueError("one count per stream")
         if any(c < 0 for c in counts):
             raise ValueError("counts must not be negative")
+        if any(s >> 31 not in (0, -1) for s in sids):
+            raise ValueError("a stream id is no 32-bit number")
         n = len(sids)
         off = [0]
         for c in counts:
@@ -313,6 +315,8 @@ class PagedKVCache:
         """pkv_stream_open_tokens: a causal stream of up to max_tokens tokens; with a
         window, evict_window(sid) frees what no later query of such a window sees
         (the first `sinks` tokens' pages stay)."""
+        if any(x >> 31 not in (0, -1) for x in (max_tokens, window, sinks)):
+            raise ValueError("max_tokens, window and sinks must be 32-bit numbers")
         sid = ctypes.c_int(-1)
         self._check(self.lib.pkv_stream_open_tokens(self.h, max_tokens, window, sinks, ctypes.byref(sid)))
         return sid.value
@@ -370,6 +374,8 @@ class PagedKVCache:
         if pos0 is not None:
             if len(pos0) != batch.n:
                 raise ValueError("one first position per stream")
+            if any(p >> 31 not in (0, -1) for p in pos0):
+                raise ValueError("a position is no 32-bit number")
             first = (ctypes.c_int * batch.n)(*pos0)
         self._check(self.lib.pkv_read_tokens(self.h, batch.n, batch.sids, first, batch.row_off, layer,
                                              outs[0].data_ptr(), outs[1].data_ptr(), self._stream(stream)))
@@ -379,6 +385,8 @@ class PagedKVCache:
         """pkv_attend_tokens: causal attention of the batch's rows (the last tokens of
         its streams) with q, [batch rows][q_heads][64]; q_heads is a multiple of the
         cache's heads. window, sinks: see pkv_attend_tokens."""
+        if window >> 31 not in (0, -1) or sinks >> 31 not in (0, -1):   # C would cut them short
+            raise ValueError("window and sinks must be 32-bit numbers (window 0: none)")
         qp, qs = self._rows(q, "q", batch)
         if out is None:
             out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)

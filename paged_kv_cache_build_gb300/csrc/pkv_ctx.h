@@ -67,9 +67,10 @@ struct pkv_ctx {
   int* d_km_len = nullptr;       // its tags per (layer, page): valid length, or -1
   int select_kept = -1;          // entries in that kept list (the last call's); -1: none yet
   int num_sms = 0;
+  float* d_token_part = nullptr; // token attention: partial results of split calls
   unsigned* d_joined = nullptr;  // token attention: counters of the splits' joins, 0 between calls
-  std::vector<unsigned> seen;    // per stream id: the last batch that named it
-  unsigned batch_no = 0;
+  std::vector<unsigned long long> seen;   // per stream id: the last batch that named it
+  unsigned long long batch_no = 0;
   std::string last_error;
 };
 

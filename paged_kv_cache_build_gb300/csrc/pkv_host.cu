@@ -238,7 +238,7 @@ static pkv_status create_cache(int pool_pages, int page_size, int heads, int hea
   // FP8 pages: 64 code bytes and one exponent byte per row; bf16 pages: 128 bytes per row
   h->page_bytes = fp8 ? 2LL * heads * page_size * (head_dim + 1) : 2LL * h->page_elems;
   h->streams.resize(max_streams);
-  h->seen.assign(max_streams, 0u);
+  h->seen.assign(max_streams, 0ull);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   h->device = dev;
@@ -308,6 +308,7 @@ pkv_status pkv_destroy(pkv_t h) {
   if (h->d_err) cudaFree(h->d_err);
   if (h->d_scratch) cudaFree(h->d_scratch);
   if (h->d_select) cudaFree(h->d_select);
+  if (h->d_token_part) cudaFree(h->d_token_part);
   if (h->d_joined) cudaFree(h->d_joined);
   if (h->d_km) cudaFree(h->d_km);
   if (h->d_km_len) cudaFree(h->d_km_len);

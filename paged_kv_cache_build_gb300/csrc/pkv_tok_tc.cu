@@ -23,7 +23,7 @@
 // into O, and QK of the next tile behind it. Its issuing warp stays converged (see
 // tc_mma_warp) and has waited for the next tile's K and V before it waits for P. m is a
 // reference that need not be the running maximum, for it cancels: it moves to the row's
-// maximum on the first tile and when a row's sum of a tile exceeds 2^64, so that most
+// maximum on the first tile and when a row's sum of a tile exceeds 2^10, so that most
 // tiles take one pass over S. P is rounded to bf16 (2^-9 relative) for the matrix unit;
 // sums are taken before that rounding, in fp32.
 // Every wait is bounded; one that gives up sets the device error word.
@@ -65,7 +65,7 @@ constexpr int kCodeRing = 4;
 constexpr int kCodeBytes = kBN * (kHeadDim + 1);
 // TMEM: S of lane i at 64 i, O at 256 + 64 i
 constexpr uint32_t kTmemCols = 512;
-constexpr float kSumLimit = 18446744073709551616.0f;   // 2^64
+constexpr float kSumLimit = 1024.0f;           // values up to 2^90 cannot take O past fp32's end
 
 template <int MT, bool FP8>
 struct __align__(1024) TcSmem {

@@ -95,6 +95,8 @@ inline bool tok_holds(const TokenCounts& t, int lo, int sinks) {
 // ---------------------------------------------------------- attention tiles
 constexpr int kTokTile = 64;
 
+PKV_HD int tok_tiles_of(int n) { return n / kTokTile + (n % kTokTile > 0); }   // (n may be INT_MAX)
+
 // The 64-slot tiles that queries at positions p0 .. p1 see: n_front of them from
 // the first on (the sinks), then those from `lo` on, n in all.
 struct TokTiles {
@@ -104,7 +106,7 @@ PKV_HD TokTiles tok_tiles(int p0, int p1, int window, int sinks) {
   TokTiles r;
   const int hi = p1 / kTokTile + 1;
   r.lo = tok_window_lo(p0, window) / kTokTile;
-  r.n_front = (sinks + kTokTile - 1) / kTokTile;
+  r.n_front = tok_tiles_of(sinks);
   if (r.n_front >= r.lo) r.n_front = r.lo = 0;
   r.n = r.n_front + hi - r.lo;
   return r;
@@ -129,7 +131,7 @@ struct TokSpan {
 };
 PKV_HD TokSpan tok_span(int p0, int p1, int window, int sinks) {
   TokSpan s;
-  s.front = (sinks + kTokTile - 1) / kTokTile;
+  s.front = tok_tiles_of(sinks);
   s.lo = tok_window_lo(p0, window) / kTokTile;
   s.hi = p1 / kTokTile;
   s.full_front = sinks / kTokTile;

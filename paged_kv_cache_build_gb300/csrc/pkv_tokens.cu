@@ -15,8 +15,9 @@ namespace {
 
 constexpr int kMaxRows = 1 << 24;    // token rows of one call
 constexpr int kMaxGroup = 128;       // query heads per KV head
-// Split-KV partials, allocated when the first token stream opens; plan_splits cuts
-// no finer than they hold.
+// Split-KV partials, allocated when the handle's first token stream opens and kept until
+// it is destroyed, so that captured calls keep their address; plan_splits cuts no finer
+// than they hold.
 constexpr size_t kTokenScratchBytes = size_t(64) << 20;
 
 constexpr int kTokenJoins = 16384;   // counters of the splits' joins
@@ -33,7 +34,7 @@ pkv_status check_batch(pkv_t h, int n, const int* sids, const int* row_off) {
   PKV_CUDA(h, cudaGetDevice(&dev));
   if (dev != h->device)
     return fail(h, PKV_ERR_INVALID, "the handle lives on device %d, the current device is %d", h->device, dev);
-  const unsigned mark = ++h->batch_no;
+  const unsigned long long mark = ++h->batch_no;
   for (int i = 0; i < n; ++i) {
     Stream* st = nullptr;
     if (pkv_status r = get_stream(h, sids[i], &st)) return r;
@@ -164,7 +165,7 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
   const size_t cap = (size_t)tok_pages(max_tokens, h->Ps);
   st.tbl_cap = (int)std::min<size_t>(cap, (size_t)h->P);
   const size_t words = cap + 2 * (size_t)st.tbl_cap;
-  if (pkv_status r = ensure_scratch(h, kTokenScratchBytes)) return r;
+  if (!h->d_token_part) PKV_CUDA(h, cudaMalloc(&h->d_token_part, kTokenScratchBytes));
   if (!h->d_joined) {
     unsigned* p = nullptr;
     PKV_CUDA(h, cudaMalloc(&p, kTokenJoins * sizeof(unsigned)));
@@ -384,49 +385,48 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   const int n_items = a.n;
   TokenQuery all[kMaxTokenBatch];
   std::copy(a.item, a.item + n_items, all);
-  for (int pass = 0; pass < 2; ++pass) {         // the first grows the scratch, if it must
-    size_t need = 0;
-    for (const int shape : {kTokenFewRows, 128, 256, 512}) {
-      const int below = shape == kTokenFewRows ? 0 : shape == 128 ? kTokenFewRows : shape / 2;
-      a.n = 0;
-      int most = 0;
-      for (int i = 0; i < n_items; ++i) {
-        const long long r = (long long)all[i].n * group;
-        if (r <= below || (r > shape && shape < 512)) continue;
-        a.item[a.n++] = all[i];
-        most = std::max(most, (int)std::min<long long>(r, shape));
-      }
-      if (a.n == 0) continue;
-      const bool few = shape == kTokenFewRows;
-      a.rows = !few ? shape : most <= 8 ? 8 : kTokenFewRows;
-      for (int i = 0; i < a.n; ++i) {
-        TokenQuery& it = a.item[i];
-        it.blocks = ceil_div((long long)it.n * group, a.rows);
-        const auto block_tiles = [&](int b) {
-          const int r0 = b * a.rows, r1 = std::min(r0 + a.rows, it.n * group) - 1;
-          return tok_tiles(it.pos0 + r0 / group, it.pos0 + r1 / group, window, sinks).n;
-        };
-        first[i] = block_tiles(0);
-        last[i] = block_tiles(it.blocks - 1);
-      }
-      const int room = std::min<int>(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
-      const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 20, 4, 8, room}
-                               : CtaCost{h->num_sms, 10, 4, 8, room};
-      plan_splits(&a, first, last, cost);
-      bool split = false;
-      for (int i = 0; i < a.n; ++i) split = split || a.item[i].splits > 1;
-      if (split) {
-        const size_t rows = (size_t)a.ctas * a.rows;
-        need = std::max(need, rows * (kHeadDim + 2) * sizeof(float));
-        a.part_o = h->d_scratch;
-        a.part_ml = h->d_scratch + rows * kHeadDim;
-      }
-      if (pass == 0) continue;
-      PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, s));
-      if (split && !few) PKV_CUDA(h, launch_token_combine(a, s));
+  long long rows_sum = 0;
+  int n_small = 0;
+  for (int i = 0; i < n_items; ++i) {
+    const long long r = (long long)all[i].n * group;
+    if (r <= kTokenFewRows) rows_sum += r, ++n_small;
+  }
+  const int few_rows = h->fp8 || rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
+  for (const int shape : {few_rows, 128, 256, 512}) {
+    const int below = shape == few_rows ? 0 : shape == 128 ? few_rows : shape / 2;
+    a.n = 0;
+    int most = 0;
+    for (int i = 0; i < n_items; ++i) {
+      const long long r = (long long)all[i].n * group;
+      if (r <= below || (r > shape && shape < 512)) continue;
+      a.item[a.n++] = all[i];
+      most = std::max(most, (int)std::min<long long>(r, shape));
     }
-    if (pass == 0)
-      if (pkv_status r = ensure_scratch(h, need)) return r;
+    if (a.n == 0) continue;
+    const bool few = shape == few_rows;
+    a.rows = !few ? shape : most <= 8 ? 8 : 16;
+    for (int i = 0; i < a.n; ++i) {
+      TokenQuery& it = a.item[i];
+      it.blocks = ceil_div((long long)it.n * group, a.rows);
+      const auto block_tiles = [&](int b) {
+        const int r0 = b * a.rows, r1 = std::min(r0 + a.rows, it.n * group) - 1;
+        return tok_tiles(it.pos0 + r0 / group, it.pos0 + r1 / group, window, sinks).n;
+      };
+      first[i] = block_tiles(0);
+      last[i] = block_tiles(it.blocks - 1);
+    }
+    const int room = std::min<int>(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
+    const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 12, 4, 8, room}
+                             : CtaCost{h->num_sms, 10, 4, 8, room};
+    plan_splits(&a, first, last, cost);
+    bool split = false;
+    for (int i = 0; i < a.n; ++i) split = split || a.item[i].splits > 1;
+    if (split) {
+      a.part_o = h->d_token_part;
+      a.part_ml = h->d_token_part + (size_t)a.ctas * a.rows * kHeadDim;
+    }
+    PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, s));
+    if (split && !few) PKV_CUDA(h, launch_token_combine(a, s));
   }
   return PKV_OK;
 }

@@ -596,3 +596,85 @@ def test_another_stream():
     ref = causal_attend_fp64(f64(q), kk, vv, 500, 0, 0, SCALE)
     assert (np.abs(f64(out) - ref) <= tolerance(f64(q), kk, vv, ref, 500, 0, 0, SCALE)).all()
     p.cache.close()
+
+
+def test_no_token_call_allocates():
+    """Token calls have partial results of their own: the scratch of the frame calls,
+    which grows and moves, is not theirs."""
+    for attempt in ("the kernels are loaded", "what is looked at"):
+        p = Pool(300, 16, 2)
+        before = p.cache.scratch_info()
+        sid = p.open()
+        p.append([sid], [4000])
+        q = [p.rows(n, 2 * g) for n, g in ((1, 1), (9, 4), (300, 2))]
+        batches = [p.cache.token_batch([sid], [len(x)]) for x in q]
+        outs = [torch.empty_like(x) for x in q]
+        torch.cuda.synchronize()
+        free = torch.cuda.mem_get_info()[0]
+        for x, b, o in zip(q, batches, outs):
+            p.cache.attend_tokens(b, x, out=o)
+        p.cache.drop_tokens(batches[2])
+        torch.cuda.synchronize()
+        after = torch.cuda.mem_get_info()[0]
+        assert p.cache.scratch_info() == before
+        p.cache.close()
+    assert after == free
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 40, 300])
+def test_large_values_behind_growing_scores(new, fp8):
+    """Values near 2^95 and scores that end 2^80 above the first ones': no sum on the
+    way may leave fp32."""
+    p = Pool(100, 16, 1, fp8)
+    sid, n = p.open(), 640 + new
+    g = torch.Generator(device="cuda").manual_seed(11)
+    k = torch.zeros((n, 1, 64), device="cuda")
+    k[:, :, 0] = torch.arange(n, device="cuda").view(-1, 1) * (8.0 / n)
+    v = torch.randn((n, 1, 64), generator=g, device="cuda") * 2.0 ** 93
+    q = torch.zeros((new, 2, 64), device="cuda")
+    q[:, :, 0] = 56.0                                  # scores up to 56, 80 in powers of two
+    k, v, q = k.bfloat16(), v.bfloat16(), q.bfloat16()
+    p.cache.append_tokens(p.cache.token_batch([sid], [n]), k, v)
+    out = p.cache.attend_tokens(p.cache.token_batch([sid], [new]), q)
+    p.cache.sync()
+    kk, vv, qq = stored(k, fp8), stored(v, fp8), f64(q)
+    ref = causal_attend_fp64(qq, kk, vv, 640, 0, 0, SCALE)
+    assert (np.abs(f64(out) - ref) <= tolerance(qq, kk, vv, ref, 640, 0, 0, SCALE)).all()
+    p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 20, 200])
+def test_largest_window_sinks_and_a_scale(new, fp8):
+    """Windows and sinks up to the largest int see every key; sm_scale is the caller's."""
+    p = Pool(60, 32, 2, fp8)
+    sid = p.open()
+    p.append([sid], [900 + new])
+    batch = p.cache.token_batch([sid], [new])
+    q, every = p.check_attend([sid], [new], 3, sm_scale=0.3)
+    for window, sinks in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1), (7, 900 + new)):
+        assert torch.equal(p.cache.attend_tokens(batch, q, window=window, sinks=sinks, sm_scale=0.3), every)
+    for window, sinks in ((2 ** 31, 0), (2 ** 32 + 5, 0), (5, 2 ** 32)):
+        with pytest.raises(ValueError):
+            p.cache.attend_tokens(batch, q, window=window, sinks=sinks)
+    with pytest.raises(ValueError):
+        p.cache.read_tokens(batch, [2 ** 32])
+    with pytest.raises(ValueError):
+        p.cache.open_token_stream(2 ** 32 + 5)
+    p.cache.sync()
+    p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_drafts_on_either_side_of_the_row_blocks(fp8):
+    """4 .. 68 query rows per KV head, alone and together, small and large on the whole."""
+    p = Pool(400, 16, 2, fp8, max_streams=8)
+    counts = [1, 2, 4, 5, 8, 9, 16, 17]
+    sids = [p.open() for _ in counts]
+    p.append(sids, [500 + 31 * n for n in counts])
+    p.check_attend(sids, counts, 4)
+    p.check_attend(sids[4:], counts[4:], 4)
+    for sid, n in zip(sids, counts):
+        p.check_attend([sid], [n], 4, 100, 5)
+    p.cache.close()

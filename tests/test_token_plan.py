@@ -180,3 +180,25 @@ def test_null_handle_and_batch_refusals_without_gpu():
         TokenBatch([0], [1, 2])
     with pytest.raises(ValueError):
         TokenBatch([0], [-1])
+
+
+@pytest.mark.parametrize("window", [1, 65, 2 ** 31 - 1])
+def test_sinks_of_any_size(plan, window):
+    """Sinks up to the largest int, past every key: the tiles are those without a window."""
+    cap, all_of_them = (ctypes.c_int * 4096)(), (ctypes.c_int * 4096)()
+    for p0, p1 in [(0, 0), (63, 64), (1000, 1500), (2 ** 17, 2 ** 17 + 100)]:
+        n = plan.plan_tiles(p0, p1, 0, 0, all_of_them, 4096)
+        for sinks in (p1 + 1, 2 ** 31 - 64, 2 ** 31 - 63, 2 ** 31 - 1):
+            assert plan.plan_tiles(p0, p1, window, sinks, cap, 4096) == n
+            assert list(cap[:n]) == list(all_of_them[:n])
+            for tile in (0, p1 // 64 // 2, p1 // 64):
+                assert plan.plan_needs(tile, p0, p1, window, sinks)
+                assert plan.plan_whole(tile, p0, p1, window, sinks) == plan.plan_whole(tile, p0, p1, 0, 0)
+                assert plan.plan_mask(64 * tile, p0, window, sinks) == plan.plan_mask(64 * tile, p0, 0, 0)
+
+
+def test_stream_ids_past_32_bits_are_refused():
+    from paged_kv_cache_build_gb300.cache import TokenBatch
+    for sid in (2 ** 31, 2 ** 32, -2 ** 31 - 1):
+        with pytest.raises(ValueError):
+            TokenBatch([sid], [1])
