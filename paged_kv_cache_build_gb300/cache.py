@@ -389,7 +389,7 @@ class PagedKVCache:
             raise ValueError("window and sinks must be 32-bit numbers (window 0: none)")
         qp, qs = self._rows(q, "q", batch)
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != self.device or \
                 not out.is_contiguous():
             raise ValueError(f"out must be a contiguous bf16 tensor {list(q.shape)} on {self.device}")

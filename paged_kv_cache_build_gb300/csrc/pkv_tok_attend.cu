@@ -503,29 +503,68 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
-// For the matrix-unit kernel's splits: 16 threads a (token, query head).
-__global__ void __launch_bounds__(256) token_combine_kernel(const __grid_constant__ TokenAttendArgs a,
-                                                            long long pairs) {
+// For the matrix-unit kernel's splits: 8 threads a (token, query head), 8 values each.
+// The partial results come from L2; loads of four splits are on their way at a time.
+constexpr int kJoinFold = 4;
+__global__ void __launch_bounds__(256, 4) token_combine_kernel(const __grid_constant__ TokenAttendArgs a, int pairs) {
   pdl_wait();
   pdl_trigger();
-  const long long gid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long pair = gid >> 4;
-  const int d = (int)(gid & 15) * 4;
+  const int gid = blockIdx.x * blockDim.x + threadIdx.x;
+  const int pair = gid >> 3, d = (gid & 7) * 8;
   if (pair >= pairs) return;
   const int H = a.heads * a.group;
-  const int row = a.item[0].row0 + (int)(pair / H), qh = (int)(pair % H);
-  const int i = find_item<TokenQuery, &TokenQuery::row0>(a.item, a.n, row);
-  const TokenQuery& t = a.item[i];
-  if (row >= t.row0 + t.n || t.splits == 1) return;
+  const int tok = pair / H, qh = pair - tok * H, row = a.item[0].row0 + tok;
+  const TokenQuery& t = a.item[find_item<TokenQuery, &TokenQuery::row0>(a.item, a.n, row)];
+  const int splits = t.splits;
+  if (row >= t.row0 + t.n || splits == 1) return;
   const int head = qh / a.group;
-  const int r = (row - t.row0) * a.group + qh % a.group;
+  const int r = (row - t.row0) * a.group + qh - head * a.group;
   const int block = r / a.rows;
-  const int cta = t.cta0 + ((t.blocks - 1 - block) * a.heads + head) * t.splits;
-  float l = 0.f;
-  const float4 o = join_splits<8>(a, (long long)cta * a.rows + r % a.rows, t.splits, d, &l);
+  const int cta = t.cta0 + ((t.blocks - 1 - block) * a.heads + head) * splits;
+  const long long pr0 = (long long)cta * a.rows + (r - block * a.rows);
+  const float2* const ml = reinterpret_cast<const float2*>(a.part_ml) + pr0;
+  const float* const part = a.part_o + pr0 * kHeadDim + d;
+  float m = -INFINITY, l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < splits; s0 += kJoinFold) {
+    float4 x[kJoinFold][2];
+    float2 y[kJoinFold];
+#pragma unroll
+    for (int k = 0; k < kJoinFold; ++k) {
+      y[k] = make_float2(-INFINITY, 0.f);
+      x[k][0] = x[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s0 + k < splits) {
+        const long long at = (long long)(s0 + k) * a.rows;
+        y[k] = __ldcg(ml + at);
+        x[k][0] = __ldcg(reinterpret_cast<const float4*>(part + at * kHeadDim));
+        x[k][1] = __ldcg(reinterpret_cast<const float4*>(part + at * kHeadDim + 4));
+      }
+    }
+    float m_new = m;
+#pragma unroll
+    for (int k = 0; k < kJoinFold; ++k) m_new = fmaxf(m_new, y[k].x);
+    const float ref = m_new == -INFINITY ? 0.f : m_new, c = fast_exp2(m - ref);
+    m = m_new;
+    l *= c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= c;
+#pragma unroll
+    for (int k = 0; k < kJoinFold; ++k) {
+      if (s0 + k >= splits) break;
+      const float w = fast_exp2(y[k].x - ref);   // 0: the split's tiles are masked for the row
+      l += w * y[k].y;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        o[4 * i] += w * x[k][i].x;
+        o[4 * i + 1] += w * x[k][i].y;
+        o[4 * i + 2] += w * x[k][i].z;
+        o[4 * i + 3] += w * x[k][i].w;
+      }
+    }
+  }
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<uint2*>(a.out + ((long long)row * H + qh) * kHeadDim + d) =
-      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  *reinterpret_cast<uint4*>(a.out + ((long long)row * H + qh) * kHeadDim + d) =
+      make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                 pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
 }
 
 template <int NT, bool FP8>
@@ -558,9 +597,9 @@ cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s) {
 
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s) {
   const TokenQuery& last = a.item[a.n - 1];
-  const long long pairs = (long long)(last.row0 + last.n - a.item[0].row0) * a.heads * a.group;
-  const cudaError_t e = launch_pdl(token_combine_kernel, dim3((unsigned)((pairs * 16 + 255) / 256)), dim3(256),
-                                   0, s, a, pairs);
+  // (rows x query heads fit 2^27: pkv_attend_tokens)
+  const int pairs = (last.row0 + last.n - a.item[0].row0) * a.heads * a.group;
+  const cudaError_t e = launch_pdl(token_combine_kernel, dim3((pairs + 31) / 32), dim3(256), 0, s, a, pairs);
   count_launches(1);
   return e;
 }
