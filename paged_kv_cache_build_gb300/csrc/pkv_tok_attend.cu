@@ -15,6 +15,10 @@
 // of a row block's splits joins their partial results. The products run on warp-level matrix
 // instructions with the 8 or 16 query rows on the N side: S^T = K Q^T and
 // O^T += V^T P^T.
+// Measured: 32 streams of up to 8192 tokens, 32 query heads on 8, in 50.8 us on bf16 pages
+// (6.1 TB/s, 0.90 of the measured copy rate) and in 37.7 us on E4M3 pages (4.2 TB/s: there
+// the conversions' and the softmax' instruction latencies on eight warps an SM bound it; more
+// warps with fewer registers, or two warps a tile, were no faster).
 //
 // bf16 pages: P is rounded to bf16 (2^-9 relative) for the second product. E4M3
 // pages: codes are exact in f16, so both products run in f16 on the codes: q is

@@ -1,8 +1,10 @@
 // Token streams: storing new tokens' keys and values (quantised on FP8 pages),
 // reading them back, and returning dropped tokens' pages.
 //
-// Bounds: memory traffic (and, for single tokens, latency). A warp moves four
-// consecutive tokens of one (K or V, head): 8 lanes of 16 bytes a token. The
+// Bounds: memory traffic (and, for single tokens, latency). 13754 tokens of 16 heads in 4
+// streams on E4M3 pages are written and read back in 35 us, 4.9 TB/s (0.72 of the measured
+// copy rate; a block's rounds of loads, quantising and stores overlap only with other
+// blocks'). With few tokens a warp moves four consecutive tokens of one (K or V, head): 8 lanes of 16 bytes a token. The
 // tokens' slots are neighbours in a page, so on E4M3 pages the warp writes one run
 // of 256 code bytes and 4 neighbouring exponent bytes.
 #include "pkv_tokens.cuh"
@@ -274,8 +276,9 @@ __global__ void __launch_bounds__(256) token_drop_kernel(const __grid_constant__
   }
 }
 
-// Tokens from which a block takes 32 of them: enough blocks to fill the SMs. (Below, a
-// warp per quad and plane: 64 single tokens of 8 heads take 4.2 us instead of TODO.)
+// Tokens from which a block takes 32 of them: enough blocks to fill the SMs. (Read-back of
+// 64 / 512 / 2560 / 4032 tokens of 8 heads on bf16 pages: 2.0 / 2.2 / 3.8 / 4.8 us with a
+// warp per quad and plane, 4.7 / 3.6 / 3.6 / 3.7 us with blocks of 32.)
 constexpr int kManyUnits = 152 * 16;
 
 int row_blocks(const TokenRowsArgs& a) {

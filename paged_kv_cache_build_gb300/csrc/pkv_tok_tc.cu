@@ -4,20 +4,21 @@
 //
 //   out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),   s_j = log2(e) sm_scale q . k_j
 //
-// Bounds: at head_dim 64 a 128 x 64 tile of scores is 2 x 256 matrix-unit cycles of
-// 4096 multiply-adds, and 256 cycles of the SM's 32 exponentials a cycle, so the
-// softmax must run beside the products without a pause. What stalls it is latency:
-// S must come back from the matrix unit and P go to it. So a CTA runs four
-// independent pipelines ("lanes"), each 128 query rows with its own S and O in
-// TMEM, its own issuing thread and its own four softmax warps (a thread per row);
-// while one waits for its products the others exponentiate. The lanes are MT
-// blocks of 128 rows times 4 / MT interleaved parts of the key tiles (MT = 4: 512
-// rows, every tile; 2: every second tile; 1: every fourth), joined at the end.
+// Bounds: at head_dim 64 a 128 x 64 tile of scores takes 2 x 128 matrix-unit cycles (4096
+// multiply-adds a cycle) and 256 cycles of the SM's 32 exponentials a cycle, so neither may
+// pause for the other. What makes them pause is latency: S must come back from the matrix
+// unit and P go to it. So an SM runs four independent pipelines ("lanes"), each 128 query
+// rows with its own S and O in TMEM, its own issuing warp and its own four softmax warps (a
+// thread per row); while one waits for its products the others exponentiate. A CTA's lanes
+// are MT blocks of 128 rows times kLanes / MT interleaved parts of the key tiles, joined at
+// the end. Measured: 1374 queries of 32 heads over 43968 keys of 8 in 481 us on bf16 pages,
+// 1.01 PFLOP/s (0.53 of the measured cuBLAS rate), and in 661 us on E4M3 pages, where the
+// three warps that convert tiles set the pace.
 //
-// Warps: 0-15 softmax (lane = warp / 4), 16-19 MMA issuers, 20 the producer, which
-// fills a ring of 64-slot K and V tiles by bulk copies (pages are stored as ready
-// operands); on E4M3 pages it fills a ring of codes, and warps 21-23 convert them
-// into the operand ring (code * 2^e is exact in bf16).
+// Warps: softmax (lane = warp / 4), the lanes' MMA issuers, the producer, which fills a ring
+// of 64-slot K and V tiles by bulk copies (pages are stored as ready operands); on E4M3 pages
+// it fills a ring of codes, and three warps convert them into the operand ring (code * 2^e is
+// exact in bf16).
 //
 // A lane's cycle: QK into S, softmax (P = 2^(S - m) as bf16 over the first half of S), PV
 // into O, and QK of the next tile behind it. Its issuing warp stays converged (see
@@ -39,32 +40,46 @@ namespace pkv {
 
 namespace {
 
-constexpr int kLanes = 4;
 constexpr int kBN = kTokTile;
-constexpr int kSoftmaxWarps = 4 * kLanes;
-constexpr int kIssuer0 = kSoftmaxWarps;
-constexpr int kProducer = kIssuer0 + kLanes;
-constexpr int kConvert0 = kProducer + 1;
-constexpr int kConvertWarps = 3;
-constexpr int kThreads = 32 * (kConvert0 + kConvertWarps);
-// Registers: 80 a thread at launch; the softmax warpgroups then take what the two
-// others give up.
-constexpr int kLaunchRegs = 80;
-template <bool FP8>
-constexpr int kOtherRegs = 32;
-template <bool FP8>
-constexpr int kSoftmaxRegs = 104;
-template <bool FP8>
-constexpr bool kRegsFit = kSoftmaxRegs<FP8> * kSoftmaxWarps + kOtherRegs<FP8> * (kThreads / 32 - kSoftmaxWarps) <=
-                          kLaunchRegs * (kThreads / 32);
-constexpr int kQThreads = 32 * kProducer;      // softmax warps and issuers
-// The ring's stages belong to one part of the tiles each: a multiple of 4 / MT.
+// bf16 pages, 256 rows: two CTAs of two lanes an SM, so that one's start and end run beside
+// the other's products (prefill of 8192 tokens, 16 heads: 145 us, 152 with one CTA of 512
+// rows; ragged batch of 12 chunks 245 against 270 us). Else one CTA of four lanes: E4M3 pages,
+// which it converts once for all of them (661 us for 1374 queries over 43968 keys), and 128
+// rows, which take little time beside the pages' (16 x 4031 keys 32 us, 37 with two CTAs).
 template <int MT, bool FP8>
-constexpr int kRing = FP8 && MT == 4 ? 6 : 8;
+constexpr int kLanes = FP8 || MT == 1 ? 4 : 2;
+template <int MT, bool FP8>
+constexpr int kCtasPerSm = 4 / kLanes<MT, FP8>;
+template <int MT, bool FP8>
+constexpr int kSoftmaxWarps = 4 * kLanes<MT, FP8>;
+template <int MT, bool FP8>
+constexpr int kIssuer0 = kSoftmaxWarps<MT, FP8>;
+template <int MT, bool FP8>
+constexpr int kProducer = kIssuer0<MT, FP8> + kLanes<MT, FP8>;
+template <int MT, bool FP8>
+constexpr int kConvert0 = kProducer<MT, FP8> + 1;
+template <int MT, bool FP8>
+constexpr int kConvertWarps = kLanes<MT, FP8> == 4 ? 3 : 1;   // (bf16: idle, to fill the warpgroup)
+template <int MT, bool FP8>
+constexpr int kThreads = 32 * (kConvert0<MT, FP8> + kConvertWarps<MT, FP8>);
+// Registers: 80 a thread at launch; the softmax warpgroups then take what the others
+// give up.
+constexpr int kLaunchRegs = 80;
+constexpr int kOtherRegs = 32;
+constexpr int kSoftmaxRegs = 104;
+template <int MT, bool FP8>
+constexpr bool kRegsFit = kSoftmaxRegs * kSoftmaxWarps<MT, FP8> + kOtherRegs * (kThreads<MT, FP8> / 32 - kSoftmaxWarps<MT, FP8>) <=
+                          kLaunchRegs * (kThreads<MT, FP8> / 32);
+template <int MT, bool FP8>
+constexpr int kQThreads = 32 * kProducer<MT, FP8>;   // softmax warps and issuers
+// The ring's stages belong to one part of the tiles each: a multiple of kLanes / MT.
+template <int MT, bool FP8>
+constexpr int kRing = kLanes<MT, FP8> == 2 ? 4 : MT == 4 ? 6 : 8;
 constexpr int kCodeRing = 4;
 constexpr int kCodeBytes = kBN * (kHeadDim + 1);
-// TMEM: S of lane i at 64 i, O at 256 + 64 i
-constexpr uint32_t kTmemCols = 512;
+// TMEM: S of lane i at 64 i, O at 64 (kLanes + i)
+template <int MT, bool FP8>
+constexpr uint32_t kTmemCols = 128 * kLanes<MT, FP8>;
 constexpr float kSumLimit = 1024.0f;           // values up to 2^90 cannot take O past fp32's end
 
 template <int MT, bool FP8>
@@ -75,17 +90,17 @@ struct __align__(1024) TcSmem {
       uint8_t k[kRing<MT, FP8>][kBN * 128];
       uint8_t v[kRing<MT, FP8>][kBN * 128];
     };
-    float o[kLanes - MT + (MT == 4)][kHeadDim][128];   // parts 1.. of the tiles, for the join
+    float o[kLanes<MT, FP8> - MT + (MT == kLanes<MT, FP8>)][kHeadDim][128];   // parts 1.. of the tiles, for the join
   };
   uint8_t code[FP8 ? kCodeRing : 1][FP8 ? 2 * kCodeBytes : 16];
-  float ml[kLanes][128][2];
+  float ml[kLanes<MT, FP8>][128][2];
   uint64_t kv_full[kRing<MT, FP8>];
   uint64_t kv_empty[kRing<MT, FP8>];
   uint64_t code_full[kCodeRing];
   uint64_t code_empty[kCodeRing];
-  uint64_t s_full[kLanes];
-  uint64_t p_full[kLanes];
-  uint64_t done[kLanes];
+  uint64_t s_full[kLanes<MT, FP8>];
+  uint64_t p_full[kLanes<MT, FP8>];
+  uint64_t done[kLanes<MT, FP8>];
   // the CTA's work, kept here for the roles to read what they need of it
   TokenWork work;
   TokTiles tiles;
@@ -152,24 +167,24 @@ __device__ __forceinline__ LaneRows lane_rows(const TokenAttendArgs& a, const To
 }
 
 template <int MT, bool FP8>
-__global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_constant__ TokenAttendArgs a) {
+__global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>) token_tc_kernel(const __grid_constant__ TokenAttendArgs a) {
   extern __shared__ uint8_t smem_raw[];
   TcSmem<MT, FP8>& sm = *reinterpret_cast<TcSmem<MT, FP8>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   constexpr int kS = kRing<MT, FP8>;
-  constexpr int kParts = kLanes / MT;
+  constexpr int kParts = kLanes<MT, FP8> / MT;
   static_assert(kS % kParts == 0, "a stage's tiles belong to one part");
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kS; ++s) {
-      mbar_init(&sm.kv_full[s], FP8 ? kConvertWarps : 1);
+      mbar_init(&sm.kv_full[s], FP8 ? kConvertWarps<MT, FP8> : 1);
       mbar_init(&sm.kv_empty[s], MT);
     }
     for (int s = 0; s < kCodeRing; ++s) {
       mbar_init(&sm.code_full[s], 1);
-      mbar_init(&sm.code_empty[s], kConvertWarps);
+      mbar_init(&sm.code_empty[s], kConvertWarps<MT, FP8>);
     }
-    for (int i = 0; i < kLanes; ++i) {
+    for (int i = 0; i < kLanes<MT, FP8>; ++i) {
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.done[i], 1);
@@ -177,10 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == kIssuer0) {
+  if (warp == kIssuer0<MT, FP8>) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      smem_u32(&sm.tmem_base)),
-                 "r"(kTmemCols));
+                 "r"(kTmemCols<MT, FP8>));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
   if (threadIdx.x == 32) {
@@ -203,15 +218,15 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
   volatile int* abort = &sm.abort;
   const TokenWork& w = sm.work;
   const int G = a.group;
-  static_assert(kRegsFit<FP8>, "the register split is within the launch's registers");
+  static_assert(kRegsFit<MT, FP8>, "the register split is within the launch's registers");
   pdl_wait();
   pdl_trigger();
 
-  if (warp < kProducer) {
+  if (warp < kProducer<MT, FP8>) {
     // Q rows as swizzled operand tiles, all on their way at once; rows behind the last
     // one as zeros
-    // (row r + kQThreads / 8 is dt tokens and dm members of the group further)
-    constexpr int kStepRows = kQThreads / 8;
+    // (row r + kQThreads<MT, FP8> / 8 is dt tokens and dm members of the group further)
+    constexpr int kStepRows = kQThreads<MT, FP8> / 8;
     const int c = threadIdx.x & 7, dt = kStepRows / G, dm = kStepRows - dt * G;
     int r = threadIdx.x >> 3, tok = (w.r0 + r) / G, mem = w.r0 + r - tok * G;
     for (; r < MT * 128; r += kStepRows) {
@@ -231,12 +246,12 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
     fence_proxy_async();
-    asm volatile("bar.sync 1, %0;\n" ::"r"(kQThreads) : "memory");
+    asm volatile("bar.sync 1, %0;\n" ::"r"(kQThreads<MT, FP8>) : "memory");
   }
 
-  if (warp == kProducer) {
+  if (warp == kProducer<MT, FP8>) {
     // ---------------------------------------------------------------- producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<FP8>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     const int Ps = a.pool.page_size;
     const int nT = sm.j1 - sm.j0, j0 = sm.j0, n_pages = sm.n_pages, head = w.head;
     const TokTiles tiles = sm.tiles;
@@ -293,19 +308,19 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
     if (lane == 0)
       for (int j = max(0, issued - kRingN); j < issued; ++j)
         tok_wait(&full[j % kRingN], (j / kRingN) & 1, abort, a.err, false);
-  } else if (warp >= kConvert0) {
+  } else if (warp >= kConvert0<MT, FP8>) {
     // ------------------------------------------------- E4M3 tiles to operands
     // 4 lanes a row, 16 codes a lane; 8 rows of K or of V a warp at a time
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<FP8>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     const int B = min(kBN, a.pool.page_size);    // rows of a code block
     const int nT = FP8 ? sm.j1 - sm.j0 : 0;
-    const int cw = warp - kConvert0;
+    const int cw = warp - kConvert0<MT, FP8>;
     for (int j = 0; j < nT; ++j) {
       const int c8 = j % kCodeRing, s = j % kS;
       if (!tok_wait(&sm.code_full[c8], (j / kCodeRing) & 1, abort, a.err)) break;
       if (!tok_wait(&sm.kv_empty[s], ((j / kS) & 1) ^ 1, abort, a.err)) break;
 #pragma unroll 2
-      for (int u = cw; u < 2 * kBN / 8; u += kConvertWarps) {
+      for (int u = cw; u < 2 * kBN / 8; u += kConvertWarps<MT, FP8>) {
         const int kv = u >= kBN / 8 ? 1 : 0;
         const int r = (u - kv * (kBN / 8)) * 8 + (lane >> 2), q4 = lane & 3;
         const uint8_t* blk = sm.code[c8] + kv * kCodeBytes + (r & ~(B - 1)) * (kHeadDim + 1);
@@ -334,11 +349,11 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
         mbar_arrive(&sm.code_empty[c8]);
       }
     }
-  } else if (warp >= kIssuer0) {
+  } else if (warp >= kIssuer0<MT, FP8>) {
     // ------------------------------------------------------------- MMA issuer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<FP8>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
     {
-      const int li = warp - kIssuer0;
+      const int li = warp - kIssuer0<MT, FP8>;
       const TokSpan span = lane_rows(a, sm.work, sm.pos0, li % MT).span;
       const int nT = sm.j1 - sm.j0, j0 = sm.j0;
       const TokTiles tiles = sm.tiles;
@@ -346,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
       constexpr uint32_t kIdQK = idesc_bf16(128, kBN, false);
       constexpr uint32_t kIdPV = idesc_bf16(128, kHeadDim, true);
       const uint64_t qa = sdesc(smem_u32(&sm.q[li % MT][0]));
-      const uint32_t t_s = tmem + 64 * li, t_o = tmem + 256 + 64 * li;
+      const uint32_t t_s = tmem + 64 * li, t_o = t_s + 64 * kLanes<MT, FP8>;
       uint32_t phase = 0;
       bool ok = true, busy = false;              // busy: a tile's P is to come
       uint32_t some = 0;                         // O holds something
@@ -399,14 +414,14 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs<FP8>));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
     const int li = warp >> 2, m_blk = li % MT, part = li / MT;
     const int wq = warp & 3, r = wq * 32 + lane;           // row of the lane's 128
     const LaneRows rows = lane_rows(a, sm.work, sm.pos0, m_blk);
     const int p = sm.pos0 + (w.r0 + 128 * m_blk + min(r, max(rows.n, 1) - 1)) / G;
     const uint32_t tmem = sm.tmem_base;
     const uint32_t t_lane = (uint32_t)(wq * 32) << 16;
-    const uint32_t t_s = tmem + t_lane + 64 * li, t_o = tmem + t_lane + 256 + 64 * li;
+    const uint32_t t_s = tmem + t_lane + 64 * li, t_o = t_s + 64 * kLanes<MT, FP8>;
     const float sl2 = a.scale_log2;
     float m_run = -INFINITY, l_run = 0.f;
     uint32_t n = 0;
@@ -510,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
     tc_fence_after();
     if (kParts > 1) {
       // ---- join the parts of the tiles: parts 1.. leave O, m and l to part 0
-      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps * 32) : "memory");   // the ring is free
+      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps<MT, FP8> * 32) : "memory");   // the ring is free
       if (part > 0) {
 #pragma unroll
         for (int c = 0; c < kHeadDim; c += 16) {
@@ -523,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
         sm.ml[li][r][0] = m_run;
         sm.ml[li][r][1] = l_run;
       }
-      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps * 32) : "memory");
+      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps<MT, FP8> * 32) : "memory");
     }
     if (alive && part == 0 && wq * 32 < rows.n) {
       float f0 = 1.f, fp[kParts];
@@ -603,16 +618,16 @@ __global__ void __launch_bounds__(kThreads, 1) token_tc_kernel(const __grid_cons
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssuer0) {
+  if (warp == kIssuer0<MT, FP8>) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tmem_base), "r"(kTmemCols));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tmem_base), "r"(kTmemCols<MT, FP8>));
   }
 }
 
 template <int MT, bool FP8>
 cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
   constexpr int smem = (int)sizeof(TcSmem<MT, FP8>) + 1024;
-  static_assert(smem <= 232448, "shared memory of a CTA");
+  static_assert((smem + 1024) * kCtasPerSm<MT, FP8> <= 228 * 1024, "shared memory per SM");
   static std::atomic<unsigned long long> configured{0};   // a bit per device
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
@@ -627,17 +642,21 @@ cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
     if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
     if (dev < 64) configured.fetch_or(bit);
   }
-  const cudaError_t e = launch_pdl(token_tc_kernel<MT, FP8>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+  const cudaError_t e = launch_pdl(token_tc_kernel<MT, FP8>, dim3(a.ctas), dim3(kThreads<MT, FP8>), smem, s, a);
   count_launches(1);
   return e;
 }
 
 }  // namespace
 
+int token_tc_max_rows(bool fp8) { return fp8 ? 512 : 256; }
+
+int token_tc_ctas_per_sm(bool fp8, int rows) { return !fp8 && rows == 256 ? kCtasPerSm<2, false> : 1; }
+
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s) {
   if (a.pool.fp8)
     return a.rows == 128 ? launch_tc<1, true>(a, s) : a.rows == 256 ? launch_tc<2, true>(a, s) : launch_tc<4, true>(a, s);
-  return a.rows == 128 ? launch_tc<1, false>(a, s) : a.rows == 256 ? launch_tc<2, false>(a, s) : launch_tc<4, false>(a, s);
+  return a.rows == 128 ? launch_tc<1, false>(a, s) : launch_tc<2, false>(a, s);
 }
 
 }  // namespace pkv

@@ -392,13 +392,15 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
     if (r <= kTokenFewRows) rows_sum += r, ++n_small;
   }
   const int few_rows = h->fp8 || rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
+  const int max_rows = token_tc_max_rows(h->fp8);
   for (const int shape : {few_rows, 128, 256, 512}) {
+    if (shape > max_rows) break;
     const int below = shape == few_rows ? 0 : shape == 128 ? few_rows : shape / 2;
     a.n = 0;
     int most = 0;
     for (int i = 0; i < n_items; ++i) {
       const long long r = (long long)all[i].n * group;
-      if (r <= below || (r > shape && shape < 512)) continue;
+      if (r <= below || (r > shape && shape < max_rows)) continue;
       a.item[a.n++] = all[i];
       most = std::max(most, (int)std::min<long long>(r, shape));
     }
@@ -417,7 +419,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
     }
     const int room = std::min<int>(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
     const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 12, 4, 8, room}
-                             : CtaCost{h->num_sms, 10, 4, 8, room};
+                             : CtaCost{h->num_sms * token_tc_ctas_per_sm(h->fp8, shape), 10, 4, 8, room};
     plan_splits(&a, first, last, cost);
     bool split = false;
     for (int i = 0; i < a.n; ++i) split = split || a.item[i].splits > 1;

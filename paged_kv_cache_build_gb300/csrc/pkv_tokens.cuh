@@ -131,7 +131,9 @@ constexpr int kTokenFewRowsAll = 32;
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s);
 // Resident CTAs per SM of that kernel.
 int token_few_ctas_per_sm();
-// Attention of 128, 256 or 512 query rows per CTA (a.rows), one CTA per SM.
+// Attention of 128, 256 or (on E4M3 pages) 512 query rows per CTA (a.rows).
+int token_tc_max_rows(bool fp8);
+int token_tc_ctas_per_sm(bool fp8, int rows);
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s);
 // Joins the splits of the items that have several (launch_token_few does so itself).
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s);
