@@ -459,7 +459,7 @@ pkv_status pkv_attend_noalloc(pkv_t h, const void* q, int n_q, int stream_id, in
  * once per handle, 64 MiB for split attention calls, which stay where they are until
  * pkv_destroy (pkv_scratch_info does not count them), so that no token call allocates.
  * Errors: INVALID (null argument, max_tokens outside 1 .. 2^28, negative window or
- * sinks, sinks above max_tokens or without a window), OOM (max_streams already
+ * sinks, sinks without a window), OOM (max_streams already
  * open), CUDA (the allocation failed). */
 pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks, int* stream_id);
 

@@ -152,15 +152,15 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
   if (!h || !stream_id) return fail(h, PKV_ERR_INVALID, "null argument");
   if (max_tokens < 1 || max_tokens > (1 << 28))
     return fail(h, PKV_ERR_INVALID, "max_tokens %d outside 1..2^28", max_tokens);
-  if (window < 0 || sinks < 0 || sinks > max_tokens || (window == 0 && sinks > 0))
-    return fail(h, PKV_ERR_INVALID, "window >= 0 and sinks in 0..max_tokens (0 without a window) required");
+  if (window < 0 || sinks < 0 || (window == 0 && sinks > 0))
+    return fail(h, PKV_ERR_INVALID, "window and sinks >= 0 required (no sinks without a window)");
   int sid = -1;
   for (int i = 0; i < h->max_streams && sid < 0; ++i)
     if (!h->streams[i].open) sid = i;
   if (sid < 0) return fail(h, PKV_ERR_OOM, "no free stream id");
   Stream st;
   st.cfg.mode = kModeTokens;
-  tok_open(&st.tok, h->Ps, max_tokens, window, sinks);
+  tok_open(&st.tok, h->Ps, max_tokens, window, std::min(sinks, max_tokens));
   // the page list, and the table buffers of pkv_export_state
   const size_t cap = (size_t)tok_pages(max_tokens, h->Ps);
   st.tbl_cap = (int)std::min<size_t>(cap, (size_t)h->P);

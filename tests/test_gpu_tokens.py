@@ -519,7 +519,7 @@ def test_refusals_change_nothing():
     refused("INVALID", lambda: cache.open_token_stream(0))
     refused("INVALID", lambda: cache.open_token_stream(10, window=-1))
     refused("INVALID", lambda: cache.open_token_stream(10, window=0, sinks=2))
-    refused("INVALID", lambda: cache.open_token_stream(10, window=3, sinks=11))
+    refused("INVALID", lambda: cache.open_token_stream(10, window=3, sinks=-1))
     refused("INVALID", lambda: cache.append_tokens(B([a, a], [1, 1]), x2, x2))
     refused("INVALID", lambda: cache.append_tokens(B([a, 7], [1, 1]), x2, x2))
     refused("INVALID", lambda: cache.append_tokens(B([2], [1]), x1, x1))
@@ -677,4 +677,19 @@ def test_drafts_on_either_side_of_the_row_blocks(fp8):
     p.check_attend(sids[4:], counts[4:], 4)
     for sid, n in zip(sids, counts):
         p.check_attend([sid], [n], 4, 100, 5)
+    p.cache.close()
+
+
+def test_a_stream_shorter_than_its_sinks():
+    """Sinks beyond a stream's largest length: nothing is ever evicted."""
+    p = Pool(20, 16, 2)
+    sid = p.cache.open_token_stream(90, window=5, sinks=100)
+    batch = p.cache.token_batch([sid], [90])
+    k, v, q = p.rows(90, 2), p.rows(90, 2), p.rows(90, 4)
+    p.cache.append_tokens(batch, k, v)
+    p.cache.evict_window(sid)
+    assert p.cache.token_info(sid) == (90, 0, 0)
+    out = p.cache.attend_tokens(batch, q, window=5, sinks=100)
+    assert torch.equal(out, p.cache.attend_tokens(batch, q))
+    p.cache.sync()
     p.cache.close()
