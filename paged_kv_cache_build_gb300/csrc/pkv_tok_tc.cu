@@ -12,13 +12,13 @@
 // thread per row); while one waits for its products the others exponentiate. A CTA's lanes
 // are MT blocks of 128 rows times kLanes / MT interleaved parts of the key tiles, joined at
 // the end. Measured: 1374 queries of 32 heads over 43968 keys of 8 in 481 us on bf16 pages,
-// 1.01 PFLOP/s (0.53 of the measured cuBLAS rate), and in 661 us on E4M3 pages, where the
-// three warps that convert tiles set the pace.
+// 1.01 PFLOP/s (0.53 of the measured cuBLAS rate), and in 627 us on E4M3 pages, where the
+// warps that convert tiles set the pace.
 //
 // Warps: softmax (lane = warp / 4), the lanes' MMA issuers, the producer, which fills a ring
 // of 64-slot K and V tiles by bulk copies (pages are stored as ready operands); on E4M3 pages
-// it fills a ring of codes, and three warps convert them into the operand ring (code * 2^e is
-// exact in bf16).
+// it fills a ring of codes, and three or seven warps convert them into the operand ring
+// (code * 2^e is exact in bf16).
 //
 // A lane's cycle: QK into S, softmax (P = 2^(S - m) as bf16 over the first half of S), PV
 // into O, and QK of the next tile behind it. Its issuing warp stays converged (see
@@ -44,8 +44,8 @@ constexpr int kBN = kTokTile;
 // bf16 pages, 256 rows: two CTAs of two lanes an SM, so that one's start and end run beside
 // the other's products (prefill of 8192 tokens, 16 heads: 145 us, 152 with one CTA of 512
 // rows; ragged batch of 12 chunks 245 against 270 us). Else one CTA of four lanes: E4M3 pages,
-// which it converts once for all of them (661 us for 1374 queries over 43968 keys), and 128
-// rows, which take little time beside the pages' (16 x 4031 keys 32 us, 37 with two CTAs).
+// which it converts once for all of them, and 128 rows, which take little time beside the
+// pages' (16 x 4031 keys: 32 us, 37 with two CTAs).
 template <int MT, bool FP8>
 constexpr int kLanes = FP8 || MT == 1 ? 4 : 2;
 template <int MT, bool FP8>
@@ -58,18 +58,25 @@ template <int MT, bool FP8>
 constexpr int kProducer = kIssuer0<MT, FP8> + kLanes<MT, FP8>;
 template <int MT, bool FP8>
 constexpr int kConvert0 = kProducer<MT, FP8> + 1;
+// The conversion sets E4M3 pages' pace: with one or two row blocks seven warps do it (16
+// streams of 8030 keys, 120 rows: 97 us, 160 with three), with four there are registers for
+// three only.
 template <int MT, bool FP8>
-constexpr int kConvertWarps = kLanes<MT, FP8> == 4 ? 3 : 1;   // (bf16: idle, to fill the warpgroup)
+constexpr int kConvertWarps = kLanes<MT, FP8> == 2 ? 1 : FP8 && MT < 4 ? 7 : 3;   // (bf16: idle, whole warpgroups)
 template <int MT, bool FP8>
 constexpr int kThreads = 32 * (kConvert0<MT, FP8> + kConvertWarps<MT, FP8>);
-// Registers: 80 a thread at launch; the softmax warpgroups then take what the others
-// give up.
-constexpr int kLaunchRegs = 80;
-constexpr int kOtherRegs = 32;
-constexpr int kSoftmaxRegs = 104;
+// Registers a thread at launch; the softmax warpgroups then take what the others give up.
 template <int MT, bool FP8>
-constexpr bool kRegsFit = kSoftmaxRegs * kSoftmaxWarps<MT, FP8> + kOtherRegs * (kThreads<MT, FP8> / 32 - kSoftmaxWarps<MT, FP8>) <=
-                          kLaunchRegs * (kThreads<MT, FP8> / 32);
+constexpr int kLaunchRegs = FP8 && MT < 4 ? 72 : 80;
+template <int MT, bool FP8>
+constexpr int kOtherRegs = FP8 && MT < 4 ? 40 : 32;
+template <int MT, bool FP8>
+constexpr int kSoftmaxRegs = FP8 && MT < 4 ? 96 : 104;
+template <int MT, bool FP8>
+constexpr bool kRegsFit =
+    kSoftmaxRegs<MT, FP8> * kSoftmaxWarps<MT, FP8> +
+        kOtherRegs<MT, FP8> * (kThreads<MT, FP8> / 32 - kSoftmaxWarps<MT, FP8>) <=
+    kLaunchRegs<MT, FP8> * (kThreads<MT, FP8> / 32);
 template <int MT, bool FP8>
 constexpr int kQThreads = 32 * kProducer<MT, FP8>;   // softmax warps and issuers
 // The ring's stages belong to one part of the tiles each: a multiple of kLanes / MT.
@@ -167,7 +174,8 @@ __device__ __forceinline__ LaneRows lane_rows(const TokenAttendArgs& a, const To
 }
 
 template <int MT, bool FP8>
-__global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>) token_tc_kernel(const __grid_constant__ TokenAttendArgs a) {
+__global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
+    token_tc_kernel(const __grid_constant__ TokenAttendArgs a) {
   extern __shared__ uint8_t smem_raw[];
   TcSmem<MT, FP8>& sm = *reinterpret_cast<TcSmem<MT, FP8>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>) token_
 
   if (warp == kProducer<MT, FP8>) {
     // ---------------------------------------------------------------- producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8>));
     const int Ps = a.pool.page_size;
     const int nT = sm.j1 - sm.j0, j0 = sm.j0, n_pages = sm.n_pages, head = w.head;
     const TokTiles tiles = sm.tiles;
@@ -311,16 +319,17 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>) token_
   } else if (warp >= kConvert0<MT, FP8>) {
     // ------------------------------------------------- E4M3 tiles to operands
     // 4 lanes a row, 16 codes a lane; 8 rows of K or of V a warp at a time
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8>));
     const int B = min(kBN, a.pool.page_size);    // rows of a code block
     const int nT = FP8 ? sm.j1 - sm.j0 : 0;
     const int cw = warp - kConvert0<MT, FP8>;
+    int u0 = cw;                                 // takes turns with the tile's larger shares
     for (int j = 0; j < nT; ++j) {
       const int c8 = j % kCodeRing, s = j % kS;
       if (!tok_wait(&sm.code_full[c8], (j / kCodeRing) & 1, abort, a.err)) break;
       if (!tok_wait(&sm.kv_empty[s], ((j / kS) & 1) ^ 1, abort, a.err)) break;
-#pragma unroll 2
-      for (int u = cw; u < 2 * kBN / 8; u += kConvertWarps<MT, FP8>) {
+#pragma unroll (MT == 4 ? 3 : 2)
+      for (int u = u0; u < 2 * kBN / 8; u += kConvertWarps<MT, FP8>) {
         const int kv = u >= kBN / 8 ? 1 : 0;
         const int r = (u - kv * (kBN / 8)) * 8 + (lane >> 2), q4 = lane & 3;
         const uint8_t* blk = sm.code[c8] + kv * kCodeBytes + (r & ~(B - 1)) * (kHeadDim + 1);
@@ -342,6 +351,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>) token_
         *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4 + 1) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
+      u0 = u0 + 1 < kConvertWarps<MT, FP8> ? u0 + 1 : 0;
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>) token_
     }
   } else if (warp >= kIssuer0<MT, FP8>) {
     // ------------------------------------------------------------- MMA issuer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8>));
     {
       const int li = warp - kIssuer0<MT, FP8>;
       const TokSpan span = lane_rows(a, sm.work, sm.pos0, li % MT).span;
@@ -414,7 +424,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>) token_
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs<MT, FP8>));
     const int li = warp >> 2, m_blk = li % MT, part = li / MT;
     const int wq = warp & 3, r = wq * 32 + lane;           // row of the lane's 128
     const LaneRows rows = lane_rows(a, sm.work, sm.pos0, m_blk);
@@ -620,7 +630,8 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>) token_
   __syncthreads();
   if (warp == kIssuer0<MT, FP8>) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tmem_base), "r"(kTmemCols<MT, FP8>));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tmem_base),
+                 "r"(kTmemCols<MT, FP8>));
   }
 }
 
@@ -639,7 +650,7 @@ cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
     // a warpgroup that asks for more registers than the launch brought would wait for ever
     cudaFuncAttributes attr;
     if (cudaError_t e2 = cudaFuncGetAttributes(&attr, token_tc_kernel<MT, FP8>)) return e2;
-    if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    if (attr.numRegs < kLaunchRegs<MT, FP8>) return cudaErrorInvalidConfiguration;
     if (dev < 64) configured.fetch_or(bit);
   }
   const cudaError_t e = launch_pdl(token_tc_kernel<MT, FP8>, dim3(a.ctas), dim3(kThreads<MT, FP8>), smem, s, a);
@@ -655,7 +666,9 @@ int token_tc_ctas_per_sm(bool fp8, int rows) { return !fp8 && rows == 256 ? kCta
 
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s) {
   if (a.pool.fp8)
-    return a.rows == 128 ? launch_tc<1, true>(a, s) : a.rows == 256 ? launch_tc<2, true>(a, s) : launch_tc<4, true>(a, s);
+    return a.rows == 128   ? launch_tc<1, true>(a, s)
+           : a.rows == 256 ? launch_tc<2, true>(a, s)
+                           : launch_tc<4, true>(a, s);
   return a.rows == 128 ? launch_tc<1, false>(a, s) : launch_tc<2, false>(a, s);
 }
 
