@@ -505,11 +505,11 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* stream_ids, const int* pos
  * stream's first `sinks` tokens stay visible beside it.
  * q: device bf16 [row_off[n]][q_heads][64], rows q_stride apart; out: the same,
  * contiguous. fp32 accumulation and softmax; the probabilities are rounded to bf16
- * for the second product, or, in streams with up to 64 rows x query heads per KV head
- * on E4M3 pages, to f16 (and q as well). sm_scale <= 0 means 1 / sqrt(64). Results depend on the batch only by
- * rounding (the split of the keys is chosen for the whole call) and are the same
- * bits for the same call. The handle's partial results are shared by its calls: order them
- * on one CUDA stream.
+ * for the second product, or, in streams with few rows x query heads per KV head
+ * (up to 64) on E4M3 pages, to f16 (and q as well). sm_scale <= 0 means 1 / sqrt(64).
+ * Results depend on the batch only by rounding (the kernel and the split of the keys
+ * are chosen for the whole call) and are the same bits for the same call. The
+ * handle's partial results are shared by its calls: order them on one CUDA stream.
  * Errors: INVALID (shape, stride, layer, q_heads, negative window or sinks, sinks
  * without a window, a null or unaligned pointer), STATE (not a token stream; more
  * rows than tokens; keys that the rows see are evicted). */

@@ -391,7 +391,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
     const long long r = (long long)all[i].n * group;
     if (r <= kTokenFewRows) rows_sum += r, ++n_small;
   }
-  const int few_rows = h->fp8 || rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
+  const int few_rows = rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
   const int max_rows = token_tc_max_rows(h->fp8);
   // one shape for all streams of the matrix-unit kernel, the largest's (a second launch costs
   // more than the lanes that stay idle: ragged drafts of 4 .. 34 tokens, 18 streams, 25.8

@@ -120,12 +120,13 @@ cudaError_t launch_token_read(const TokenRowsArgs& a, cudaStream_t s);
 cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s);
 
 // Attention in blocks of 8 or 16 query rows (a.rows). A stream of more rows reads its keys
-// once a block, from L2 but for the first, so this kernel takes at most kTokenFewRows of
-// them per KV head on E4M3 pages, which it does not convert, and where the streams are
-// smaller on the whole; else kTokenFewRowsAll. (16 streams of 4001 tokens, 8 KV heads, all
-// of them with 32 / 48 / 64 rows: 29.5 / 52.4 / 49.7 us on bf16 pages and 41 / 75 / 80 us
-// on E4M3 pages against 31.8 and 84 us in launch_token_tc's blocks of 128 rows; spread
-// over 4 .. 32 / 6 .. 48 / 8 .. 64 rows: 28.2 / 24.9 / 32.5 against 31.7 / 39.5 / 40.3 us.)
+// once a block, from L2 but for the first, so this kernel takes at most kTokenFewRowsAll of
+// them per KV head, or kTokenFewRows where the streams up to that size have no more than
+// kTokenFewRowsAll on average. (16 streams of 4001 tokens, 8 KV heads, all of them with
+// 32 / 48 / 64 rows: 29.5 / 52.4 / 49.7 us on bf16 pages and 41 / 75 / 80 us on E4M3 pages
+// against 31.8 and 53 us in launch_token_tc's blocks of 128 rows; spread over 4 .. 32 /
+// 6 .. 48 / 8 .. 64 rows: 28 / 25 / 33 against 32 / 40 / 40 us and 36 / 40 / 46 against
+// 46 / 54 / 55 us.)
 constexpr int kTokenFewRows = 64;
 constexpr int kTokenFewRowsAll = 32;
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s);
