@@ -93,8 +93,8 @@ __device__ __forceinline__ float max8(float x) {   // over the 8 lanes of a quer
 
 // Values d .. d + 3 of a row whose splits' partial results start at row pr0:
 // o = sum_s 2^(m_s - M) o_s, l = sum_s 2^(m_s - M) l_s, M = max_s m_s, in order.
-template <int kFold>
-__device__ __forceinline__ float4 join_splits(const TokenAttendArgs& a, long long pr0, int splits, int d,
+template <int kFold, typename Args>
+__device__ __forceinline__ float4 join_splits(const Args& a, long long pr0, int splits, int d,
                                               float* l_out) {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -128,8 +128,9 @@ __device__ __forceinline__ float4 join_splits(const TokenAttendArgs& a, long lon
   return o;
 }
 // Values d .. d + 3 of the CTA's row r, divided by the row's sum.
-__device__ __forceinline__ void write_row(const TokenAttendArgs& a, const TokenQuery& t, const TokenWork& w, int r,
-                                          int d, const float4& o, float l) {
+template <typename Args>
+__device__ __forceinline__ void write_row(const Args& a, const TokenQuery& t, const TokenWork& w, int r, int d,
+                                          const float4& o, float l) {
   const float inv = l > 0.f ? 1.f / l : 0.f;
   const int rr = w.r0 + r;
   uint16_t* dst = a.out + ((long long)(t.row0 + rr / a.group) * a.heads * a.group + w.head * a.group +
@@ -137,9 +138,8 @@ __device__ __forceinline__ void write_row(const TokenAttendArgs& a, const TokenQ
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
 }
 
-template <int NT, bool FP8>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    token_few_kernel(const __grid_constant__ TokenAttendArgs a) {
+template <int NT, bool FP8, typename Args>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) token_few_kernel(const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
   FewSmem<NT, FP8>& sm = *reinterpret_cast<FewSmem<NT, FP8>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -571,8 +571,8 @@ __global__ void __launch_bounds__(256, 4) token_combine_kernel(const __grid_cons
                  pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
 }
 
-template <int NT, bool FP8>
-cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
+template <int NT, bool FP8, typename Args>
+cudaError_t launch_few_args(const Args& a, cudaStream_t s) {
   constexpr int smem = (int)sizeof(FewSmem<NT, FP8>) + 1024;
   static_assert((smem + 1024) * kCtasPerSm <= 228 * 1024, "shared memory per SM");
   static std::atomic<unsigned long long> configured{0};   // a bit per device
@@ -580,14 +580,18 @@ cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (dev >= 64 || !(configured.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(token_few_kernel<NT, FP8>,
+    const cudaError_t e = cudaFuncSetAttribute(token_few_kernel<NT, FP8, Args>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) configured.fetch_or(bit);
   }
-  const cudaError_t e = launch_pdl(token_few_kernel<NT, FP8>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+  const cudaError_t e = launch_pdl(token_few_kernel<NT, FP8, Args>, dim3(a.ctas), dim3(kThreads), smem, s, a);
   count_launches(1);
   return e;
+}
+template <int NT, bool FP8>
+cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
+  return a.n <= kSmallTokenBatch ? launch_few_args<NT, FP8>(small_args(a), s) : launch_few_args<NT, FP8>(a, s);
 }
 
 }  // namespace

@@ -16,7 +16,8 @@ namespace {
 constexpr int kQuad = 4;             // tokens that a warp moves at a time
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ int page_of(const TokenRowsArgs& a, const TokenRows& it, int pi) {
+template <typename Args>
+__device__ __forceinline__ int page_of(const Args& a, const TokenRows& it, int pi) {
   const int page = a.is_meta && pi >= it.old_pages
                        ? a.free_stack[a.top - 1 - it.pop0 - (pi - it.old_pages)]
                        : it.pages[pi];
@@ -28,7 +29,8 @@ __device__ __forceinline__ int page_of(const TokenRowsArgs& a, const TokenRows& 
 }
 
 // Few rows: a warp per quad and plane.
-__global__ void __launch_bounds__(kWarps * 32) token_append_kernel(const __grid_constant__ TokenRowsArgs a) {
+template <typename Args>
+__global__ void __launch_bounds__(kWarps * 32) token_append_kernel(const __grid_constant__ Args a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, c = lane & 7;
@@ -81,7 +83,8 @@ __device__ __forceinline__ uint4 load_row_chunk(const PoolView& pv, int page, in
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kWarps * 32) token_read_kernel(const __grid_constant__ TokenRowsArgs a) {
+template <typename Args>
+__global__ void __launch_bounds__(kWarps * 32) token_read_kernel(const __grid_constant__ Args a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, c = lane & 7;
@@ -262,7 +265,8 @@ __global__ void __launch_bounds__(kWarps * 32) token_read_many_kernel(const __gr
   }
 }
 
-__global__ void __launch_bounds__(256) token_drop_kernel(const __grid_constant__ TokenDropArgs a) {
+template <typename Args>
+__global__ void __launch_bounds__(256) token_drop_kernel(const __grid_constant__ Args a) {
   pdl_wait();
   pdl_trigger();
   const TokenDropItem& it = a.item[blockIdx.x];
@@ -286,30 +290,47 @@ int row_blocks(const TokenRowsArgs& a) {
   return (int)((warps + kWarps - 1) / kWarps);
 }
 
+using SmallRowsArgs = TokenRowsArgsOf<kSmallTokenBatch>;
+using SmallDropArgs = TokenDropArgsOf<kSmallTokenBatch>;
+
 }  // namespace
 
 cudaError_t launch_token_append(const TokenRowsArgs& a, cudaStream_t s) {
-  const bool many = a.units >= kManyUnits;
-  const int blocks = many ? (a.units + kManyTokens - 1) / kManyTokens : row_blocks(a);
-  auto* const kernel = !many ? token_append_kernel
-                       : a.pool.fp8 ? token_append_many_kernel<true> : token_append_many_kernel<false>;
-  const cudaError_t e = launch_pdl(kernel, dim3(blocks), dim3(kWarps * 32), 0, s, a);
+  const dim3 threads(kWarps * 32);
+  cudaError_t e;
+  if (a.units >= kManyUnits) {
+    auto* const kernel = a.pool.fp8 ? token_append_many_kernel<true> : token_append_many_kernel<false>;
+    e = launch_pdl(kernel, dim3((a.units + kManyTokens - 1) / kManyTokens), threads, 0, s, a);
+  } else if (a.n <= kSmallTokenBatch) {
+    e = launch_pdl(token_append_kernel<SmallRowsArgs>, dim3(row_blocks(a)), threads, 0, s, small_args(a));
+  } else {
+    e = launch_pdl(token_append_kernel<TokenRowsArgs>, dim3(row_blocks(a)), threads, 0, s, a);
+  }
   count_launches(1);
   return e;
 }
 
 cudaError_t launch_token_read(const TokenRowsArgs& a, cudaStream_t s) {
-  const bool many = a.units >= kManyUnits;
-  const int blocks = many ? (a.units + kManyTokens - 1) / kManyTokens : row_blocks(a);
-  auto* const kernel = !many ? token_read_kernel
-                       : a.pool.fp8 ? token_read_many_kernel<true> : token_read_many_kernel<false>;
-  const cudaError_t e = launch_pdl(kernel, dim3(blocks), dim3(kWarps * 32), 0, s, a);
+  const dim3 threads(kWarps * 32);
+  cudaError_t e;
+  if (a.units >= kManyUnits) {
+    auto* const kernel = a.pool.fp8 ? token_read_many_kernel<true> : token_read_many_kernel<false>;
+    e = launch_pdl(kernel, dim3((a.units + kManyTokens - 1) / kManyTokens), threads, 0, s, a);
+  } else if (a.n <= kSmallTokenBatch) {
+    e = launch_pdl(token_read_kernel<SmallRowsArgs>, dim3(row_blocks(a)), threads, 0, s, small_args(a));
+  } else {
+    e = launch_pdl(token_read_kernel<TokenRowsArgs>, dim3(row_blocks(a)), threads, 0, s, a);
+  }
   count_launches(1);
   return e;
 }
 
 cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(token_drop_kernel, dim3(a.n), dim3(a.n > 4 ? 32 : 256), 0, s, a);
+  const dim3 threads(a.n > 4 ? 32 : 256);
+  const cudaError_t e =
+      a.n <= kSmallTokenBatch
+          ? launch_pdl(token_drop_kernel<SmallDropArgs>, dim3(a.n), threads, 0, s, small_args(a))
+          : launch_pdl(token_drop_kernel<TokenDropArgs>, dim3(a.n), threads, 0, s, a);
   count_launches(1);
   return e;
 }

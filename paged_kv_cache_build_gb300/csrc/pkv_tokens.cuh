@@ -1,12 +1,18 @@
 // Arguments and launchers of the token streams' kernels.
 #pragma once
 
+#include <cstddef>
+#include <cstring>
+
 #include "pkv_internal.cuh"
 #include "pkv_token_plan.h"
 
 namespace pkv {
 
 constexpr int kMaxTokenBatch = 256;   // streams of one token call
+// Kernels that single tokens go through exist for argument blocks of a few streams, too: a
+// launch's arguments are copied (10 KB for 256 streams; a call takes 0.5 us less without).
+constexpr int kSmallTokenBatch = 16;
 
 // One stream of an append or a read: rows row0 .. row0 + n - 1 of the packed
 // tensors are its positions pos0 .. pos0 + n - 1.
@@ -20,7 +26,8 @@ struct TokenRows {
   int pop0;                         // append: pages that the batch pops before this stream's
 };
 
-struct TokenRowsArgs {
+template <int kStreams>
+struct TokenRowsArgsOf {
   PoolView pool;
   uint16_t* k;                      // read: outputs, contiguous
   uint16_t* v;
@@ -31,8 +38,9 @@ struct TokenRowsArgs {
   int n;                            // streams
   int units;                        // row numbers in all
   int* err;
-  TokenRows item[kMaxTokenBatch];
+  TokenRows item[kStreams];
 };
+using TokenRowsArgs = TokenRowsArgsOf<kMaxTokenBatch>;
 
 // Page list entries start, start - 1, .. (count of them) go back on the free
 // stack from free[top + base] on.
@@ -40,14 +48,16 @@ struct TokenDropItem {
   const int32_t* pages;
   int start, count, base;
 };
-struct TokenDropArgs {
+template <int kStreams>
+struct TokenDropArgsOf {
   int32_t* free_stack;
   int top;
   int n;
   int pool_pages;
   int* err;
-  TokenDropItem item[kMaxTokenBatch];
+  TokenDropItem item[kStreams];
 };
+using TokenDropArgs = TokenDropArgsOf<kMaxTokenBatch>;
 
 // One stream of an attention call. Its query rows (token, head of the group) are
 // numbered token * group + member for each KV head and cut into blocks of the
@@ -61,7 +71,8 @@ struct TokenQuery {
   int blocks, splits;
 };
 
-struct TokenAttendArgs {
+template <int kStreams>
+struct TokenAttendArgsOf {
   const uint16_t* q;                // [rows][q_heads][64], rows q_stride elements apart
   uint16_t* out;                    // [rows][q_heads][64]
   long long q_stride;
@@ -76,8 +87,18 @@ struct TokenAttendArgs {
   int n;
   int ctas;
   int rows;                         // query rows per CTA
-  TokenQuery item[kMaxTokenBatch];
+  TokenQuery item[kStreams];
 };
+using TokenAttendArgs = TokenAttendArgsOf<kMaxTokenBatch>;
+
+// The arguments with their first streams only (the items come last).
+template <template <int> class Args>
+Args<kSmallTokenBatch> small_args(const Args<kMaxTokenBatch>& a) {
+  static_assert(offsetof(Args<kSmallTokenBatch>, item) == offsetof(Args<kMaxTokenBatch>, item), "a common start");
+  Args<kSmallTokenBatch> r;
+  std::memcpy(static_cast<void*>(&r), &a, sizeof(r));
+  return r;
+}
 
 // The item whose CTAs (units) the index falls into: the last one that starts at
 // or before it and is not empty. First entries grow with i.
@@ -98,7 +119,8 @@ struct TokenWork {
   int r0, rows;                     // its query rows in the (stream, head): first, count
   int p0, p1;                       // positions of the first and the last row
 };
-__device__ __forceinline__ TokenWork token_work(const TokenAttendArgs& a, int cta) {
+template <typename Args>
+__device__ __forceinline__ TokenWork token_work(const Args& a, int cta) {
   TokenWork w;
   w.item = find_item<TokenQuery, &TokenQuery::cta0>(a.item, a.n, cta);
   const TokenQuery& t = a.item[w.item];
