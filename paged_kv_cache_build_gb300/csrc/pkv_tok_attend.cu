@@ -10,10 +10,10 @@
 // Bounds: memory traffic; every visible K and V row is read once from HBM. One
 // producer warp keeps a ring of 64-slot tiles filled by bulk copies (the pages are
 // stored as ready operands, so a block of slots is one copy of K and one of V); each
-// of four warps takes every fourth tile whole, holds its own m, sum and O, and the
-// four are joined at the end. Long tables are split over CTAs; the one that ends last
+// of four (three) warps takes every fourth (third) tile whole, holds its own m, sum and O,
+// and they are joined at the end. Long tables are split over CTAs; the one that ends last
 // of a row block's splits joins their partial results. The products run on warp-level matrix
-// instructions with the 8 or 16 query rows on the N side: S^T = K Q^T and
+// instructions with the 8, 16 or 24 query rows on the N side: S^T = K Q^T and
 // O^T += V^T P^T.
 // Measured: 32 streams of up to 8192 tokens, 32 query heads on 8, in 50.8 us on bf16 pages
 // (6.1 TB/s, 0.90 of the measured copy rate) and in 37.7 us on E4M3 pages (4.2 TB/s: there
@@ -36,8 +36,14 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 4;                        // consumer warps
-constexpr int kThreads = (kWarps + 1) * 32;      // and the producer
+// Consumer warps (and one producer). Up to 16 rows: four, at 168 registers a thread. 24 rows:
+// three, so that two CTAs' warps have 255 (16 ragged streams of up to 4001 tokens, 20 rows:
+// 21.0 us; four warps that spill 21.9; two blocks of 16 rows 32.5. With 32 rows the block
+// takes longer than two of 16: 36 against 29 us, and 47 against 41 on E4M3 pages.)
+template <int NT>
+constexpr int kWarps = NT <= 2 ? 4 : 3;
+template <int NT>
+constexpr int kThreads = (kWarps<NT> + 1) * 32;
 
 template <bool FP8>
 constexpr int kTileBytes = FP8 ? kTokTile * (kHeadDim + 1) : kTokTile * kHeadDim * 2;   // K or V
@@ -54,9 +60,9 @@ struct __align__(1024) FewSmem {
       uint8_t k[kRing<FP8>][kTileBytes<FP8>];
       uint8_t v[kRing<FP8>][kTileBytes<FP8>];
     };
-    float o[kWarps][NT * 8][kHeadDim];           // after the last tile: the warps' O
+    float o[kWarps<NT>][NT * 8][kHeadDim];           // after the last tile: the warps' O
   };
-  float ml[kWarps][NT * 8][2];
+  float ml[kWarps<NT>][NT * 8][2];
   uint64_t full[kRing<FP8>];
   uint64_t empty[kRing<FP8>];
   int abort;
@@ -139,12 +145,12 @@ __device__ __forceinline__ void write_row(const Args& a, const TokenQuery& t, co
 }
 
 template <int NT, bool FP8, typename Args>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) token_few_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
   FewSmem<NT, FP8>& sm = *reinterpret_cast<FewSmem<NT, FP8>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   constexpr int kS = kRing<FP8>;
-  static_assert(kS > kWarps, "the order of the stages' releases");
+  static_assert(kS > kWarps<NT>, "the order of the stages' releases");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kS; ++s) {
@@ -166,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_few_kernel(const _
   pdl_wait();
   pdl_trigger();
 
-  if (warp == kWarps) {
+  if (warp == kWarps<NT>) {
     // ---------------------------------------------------------------- producer
     // The page blocks of the next 32 / per tiles, one per lane: their addresses are
     // worked out together, and a tile then costs a wait and its lanes' copies.
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_few_kernel(const _
 #pragma unroll
   for (int n = 0; n < NT; ++n) ref[n][0] = ref[n][1] = -INFINITY;
 
-  if (warp < kWarps) {
+  if (warp < kWarps<NT>) {
     // Q^T as B operands (query g of each 8), rows behind the last one as zeros.
     // E4M3: the K codes of a row are read 16 bytes a lane, so the d of (step kk,
     // lane tq, i) is 16 tq + 4 kk + i; bf16: the operand's own order.
@@ -281,12 +287,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_few_kernel(const _
       }
     }
 
-    for (int j = warp; j < nT; j += kWarps) {
+    for (int j = warp; j < nT; j += kWarps<NT>) {
       const int s = j % kS;
       // A stage passes between warps, and copies may land out of order: a parity
       // names the phase only once the one before it is over. The stage's last tile,
       // j - kS, is over when its warp has released it; the wait for that is exact,
-      // because tile j - kWarps, which this warp has used, was issued after tile
+      // because tile j - kWarps<NT>, which this warp has used, was issued after tile
       // j - kS, and so after tile j - 2 kS was released.
       if (j >= kS && !mbar_wait(&sm.empty[s], ((j / kS) & 1) ^ 1, abort, a.err)) break;
       if (!mbar_wait(&sm.full[s], (j / kS) & 1, abort, a.err)) break;
@@ -435,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_few_kernel(const _
   }
   __syncthreads();                               // every tile is used: the ring is free
 
-  // ---- join the four warps
-  if (warp < kWarps) {
+  // ---- join the warps
+  if (warp < kWarps<NT>) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -461,15 +467,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_few_kernel(const _
   }
   __syncthreads();
   // 16 lanes a row, 4 values a lane
-  for (int x = threadIdx.x; x < w.rows * 16; x += kThreads) {
+  for (int x = threadIdx.x; x < w.rows * 16; x += kThreads<NT>) {
     const int r = x >> 4, d = (x & 15) * 4;
     float mm = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) mm = fmaxf(mm, sm.ml[i][r][0]);
+    for (int i = 0; i < kWarps<NT>; ++i) mm = fmaxf(mm, sm.ml[i][r][0]);
     float ll = 0.f;
     float4 ov = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < kWarps<NT>; ++i) {
       const float f = mm == -INFINITY ? 0.f : fast_exp2(sm.ml[i][r][0] - mm);
       const float4 p = *reinterpret_cast<const float4*>(&sm.o[i][r][d]);
       ll += f * sm.ml[i][r][1];
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) token_few_kernel(const _
   __syncthreads();
   if (!sm.last) return;
   __threadfence();
-  for (int x = threadIdx.x; x < w.rows * 16; x += kThreads) {
+  for (int x = threadIdx.x; x < w.rows * 16; x += kThreads<NT>) {
     const int r = x >> 4, d = (x & 15) * 4;
     float l = 0.f;
     const float4 o = join_splits<12>(a, (long long)cta0 * a.rows + r, t.splits, d, &l);
@@ -585,7 +591,7 @@ cudaError_t launch_few_args(const Args& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) configured.fetch_or(bit);
   }
-  const cudaError_t e = launch_pdl(token_few_kernel<NT, FP8, Args>, dim3(a.ctas), dim3(kThreads), smem, s, a);
+  const cudaError_t e = launch_pdl(token_few_kernel<NT, FP8, Args>, dim3(a.ctas), dim3(kThreads<NT>), smem, s, a);
   count_launches(1);
   return e;
 }
@@ -599,8 +605,13 @@ cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
 int token_few_ctas_per_sm() { return kCtasPerSm; }
 
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s) {
-  if (a.pool.fp8) return a.rows == 8 ? launch_few<1, true>(a, s) : launch_few<2, true>(a, s);
-  return a.rows == 8 ? launch_few<1, false>(a, s) : launch_few<2, false>(a, s);
+  if (a.pool.fp8)
+    return a.rows == 8    ? launch_few<1, true>(a, s)
+           : a.rows == 16 ? launch_few<2, true>(a, s)
+                          : launch_few<3, true>(a, s);
+  return a.rows == 8    ? launch_few<1, false>(a, s)
+         : a.rows == 16 ? launch_few<2, false>(a, s)
+                        : launch_few<3, false>(a, s);
 }
 
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s) {

@@ -411,7 +411,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
     }
     if (a.n == 0) continue;
     const bool few = shape == few_rows;
-    a.rows = !few ? shape : most <= 8 ? 8 : 16;
+    a.rows = !few ? shape : most <= 8 ? 8 : most > 16 && most <= 24 ? 24 : 16;
     for (int i = 0; i < a.n; ++i) {
       TokenQuery& it = a.item[i];
       it.blocks = ceil_div((long long)it.n * group, a.rows);

@@ -141,7 +141,7 @@ cudaError_t launch_token_append(const TokenRowsArgs& a, cudaStream_t s);
 cudaError_t launch_token_read(const TokenRowsArgs& a, cudaStream_t s);
 cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s);
 
-// Attention in blocks of 8 or 16 query rows (a.rows). A stream of more rows reads its keys
+// Attention in blocks of 8, 16 or 24 query rows (a.rows). A stream of more rows reads its keys
 // once a block, from L2 but for the first, so this kernel takes at most kTokenFewRowsAll of
 // them per KV head, or kTokenFewRows where the streams up to that size have no more than
 // kTokenFewRowsAll on average. (16 streams of 4001 tokens, 8 KV heads, all of them with
