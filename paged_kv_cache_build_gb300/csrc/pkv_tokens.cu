@@ -394,7 +394,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   const int few_rows = rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
   const int max_rows = token_tc_max_rows(h->fp8);
   // one shape for all streams of the matrix-unit kernel, the largest's (a second launch costs
-  // more than the lanes that stay idle: ragged drafts of 4 .. 34 tokens, 18 streams, 25.8
+  // more than the lanes that stay idle: 2 .. 34 new tokens of 18 streams, 25.8
   // against 39.1 us)
   int tc_rows = 128;
   for (int i = 0; i < n_items; ++i)

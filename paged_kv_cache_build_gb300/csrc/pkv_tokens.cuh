@@ -146,9 +146,9 @@ cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s);
 // them per KV head, or kTokenFewRows where the streams up to that size have no more than
 // kTokenFewRowsAll on average. (16 streams of 4001 tokens, 8 KV heads, all of them with
 // 32 / 48 / 64 rows: 29.5 / 52.4 / 49.7 us on bf16 pages and 41 / 75 / 80 us on E4M3 pages
-// against 31.8 and 53 us in launch_token_tc's blocks of 128 rows; spread over 4 .. 32 /
-// 6 .. 48 / 8 .. 64 rows: 28 / 25 / 33 against 32 / 40 / 40 us and 36 / 40 / 46 against
-// 46 / 54 / 55 us.)
+// against 31.8 and 53 us in launch_token_tc's blocks of 128 rows. Streams of 500 .. 4001
+// tokens, with 32 / 4 .. 48 / 4 .. 64 rows: 28 / 25 / 33 against 32 / 40 / 40 us, and on
+// E4M3 pages 36 / 40 / 46 against 46 / 54 / 55 us.)
 constexpr int kTokenFewRows = 64;
 constexpr int kTokenFewRowsAll = 32;
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s);
