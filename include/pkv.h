@@ -458,6 +458,8 @@ pkv_status pkv_attend_noalloc(pkv_t h, const void* q, int n_q, int stream_id, in
  * keeps every token. Allocates the page list (4 bytes per page of max_tokens) and,
  * once per handle, 64 MiB for split attention calls, which stay where they are until
  * pkv_destroy (pkv_scratch_info does not count them), so that no token call allocates.
+ * The stream is ready when the call returns, for calls on any CUDA stream; it waits for
+ * no work that is queued.
  * Errors: INVALID (null argument, max_tokens outside 1 .. 2^28, negative window or
  * sinks, sinks without a window), OOM (max_streams already
  * open), CUDA (the allocation failed). */

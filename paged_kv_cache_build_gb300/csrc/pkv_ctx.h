@@ -92,6 +92,30 @@ inline uint16_t* layer_base(pkv_t h, int layer) {
                                      (long long)layer * h->P * h->page_bytes);
 }
 
+// What an entry point writes to the device before it returns, on a stream of its own
+// that it waits for: the caller's streams need not be ordered behind the default one,
+// which may be busy. Operations after a failed one do nothing; wait() returns the first
+// error.
+class SetupStream {
+ public:
+  SetupStream() : e_(cudaStreamCreateWithFlags(&s_, cudaStreamNonBlocking)) {}
+  ~SetupStream() {
+    if (s_) cudaStreamDestroy(s_);
+  }
+  SetupStream(const SetupStream&) = delete;
+  void fill(void* p, int byte, size_t bytes) {
+    if (e_ == cudaSuccess) e_ = cudaMemsetAsync(p, byte, bytes, s_);
+  }
+  cudaError_t wait() {
+    if (e_ == cudaSuccess) e_ = cudaStreamSynchronize(s_);
+    return e_;
+  }
+
+ private:
+  cudaStream_t s_ = nullptr;
+  cudaError_t e_;
+};
+
 // Records the message and returns the status.
 pkv_status fail(pkv_t h, pkv_status st, const char* fmt, ...);
 pkv_status cuda_fail(pkv_t h, cudaError_t e, const char* what);

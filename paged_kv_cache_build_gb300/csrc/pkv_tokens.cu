@@ -169,19 +169,16 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
   if (!h->d_joined) {
     unsigned* p = nullptr;
     PKV_CUDA(h, cudaMalloc(&p, kTokenJoins * sizeof(unsigned)));
-    if (cudaError_t e2 = cudaMemset(p, 0, kTokenJoins * sizeof(unsigned))) {
+    SetupStream setup;
+    setup.fill(p, 0, kTokenJoins * sizeof(unsigned));
+    if (cudaError_t e = setup.wait()) {
       cudaFree(p);
-      return cuda_fail(h, e2, "stream_open_tokens cudaMemset");
+      return cuda_fail(h, e, "stream_open_tokens: clearing the join counters");
     }
     h->d_joined = p;
   }
-  cudaError_t e = cudaMalloc(&st.d_mem, words * sizeof(int32_t));
-  if (e != cudaSuccess) return cuda_fail(h, e, "stream_open_tokens cudaMalloc");
-  e = cudaMemset(st.d_mem, 0, words * sizeof(int32_t));
-  if (e != cudaSuccess) {
-    cudaFree(st.d_mem);
-    return cuda_fail(h, e, "stream_open_tokens cudaMemset");
-  }
+  // (not cleared: an entry is written before any call reads it)
+  PKV_CUDA(h, cudaMalloc(&st.d_mem, words * sizeof(int32_t)));
   st.d_pages = st.d_mem;
   st.d_tbl_idx = st.d_mem + cap;
   st.d_tbl_len = st.d_tbl_idx + st.tbl_cap;

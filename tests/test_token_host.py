@@ -1,0 +1,57 @@
+"""Token streams' entry points without a GPU: the library's own host code, linked with a
+CUDA runtime that keeps books instead of driving a device (fake_cudart.cpp)."""
+
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+OK, INVALID = 0, 1
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    from paged_kv_cache_build_gb300 import build
+    from paged_kv_cache_build_gb300._lib import SIGNATURES
+    build.build()
+    so = str(tmp_path_factory.mktemp("host") / "host.so")
+    objs = [os.path.join(build.BUILD, os.path.basename(s)[:-3] + ".o") for s in build.sources()]
+    include = os.path.join(os.path.dirname(os.path.dirname(build.nvcc())), "include")
+    # -Bsymbolic: not the runtime that torch has loaded
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I", include,
+                    os.path.join(HERE, "fake_cudart.cpp")] + objs + ["-o", so], check=True)
+    L = ctypes.CDLL(so)
+    for name, (res, args) in SIGNATURES.items():
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = res, args
+    return L
+
+
+@pytest.fixture(params=[False, True], ids=["bf16", "e4m3"])
+def handle(lib, request):
+    lib.fake_set_device(0)
+    h = ctypes.c_void_p()
+    create = lib.pkv_create_fp8 if request.param else lib.pkv_create_ex
+    assert create(20, 16, 2, 64, 2, 8, ctypes.byref(h)) == OK
+    lib.cudaDeviceSynchronize()
+    yield h
+    lib.fake_set_device(0)
+    assert lib.pkv_destroy(h) == OK
+    assert lib.fake_allocs(0) == lib.fake_allocs(1) == 0 and lib.fake_streams() == 0
+
+
+def open_tokens(lib, h, *args):
+    sid = ctypes.c_int(-1)
+    return lib.pkv_stream_open_tokens(h, *args, ctypes.byref(sid)), sid.value
+
+
+def test_an_opened_stream_is_ready(lib, handle):
+    """Nothing that open has queued may still be to come when it returns: the caller's
+    streams are not ordered behind the one that it was queued on."""
+    for _ in range(2):                           # the first one lays out the handle's workspace, too
+        r, _ = open_tokens(lib, handle, 100, 0, 0)
+        assert r == OK
+        assert lib.fake_queued() == 0
