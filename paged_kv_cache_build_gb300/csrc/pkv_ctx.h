@@ -106,6 +106,9 @@ class SetupStream {
   void fill(void* p, int byte, size_t bytes) {
     if (e_ == cudaSuccess) e_ = cudaMemsetAsync(p, byte, bytes, s_);
   }
+  void copy_in(void* p, const void* host, size_t bytes) {
+    if (e_ == cudaSuccess) e_ = cudaMemcpyAsync(p, host, bytes, cudaMemcpyHostToDevice, s_);
+  }
   cudaError_t wait() {
     if (e_ == cudaSuccess) e_ = cudaStreamSynchronize(s_);
     return e_;

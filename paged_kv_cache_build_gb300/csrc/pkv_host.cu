@@ -250,30 +250,30 @@ static pkv_status create_cache(int pool_pages, int page_size, int heads, int hea
     h->noalloc_scratch = static_cast<float*>(p);
   }
   const size_t pool_bytes = (size_t)layers * pool_pages * h->page_bytes;
+  // page skipping's scratch (query means, estimates, kept list)
+  const size_t select_bytes = sizeof(float) * (kMaxHeads * kHeadDim + kMaxSampledEntries) +
+                              sizeof(uint16_t) * kMaxSampledEntries + sizeof(unsigned);
   if (e == cudaSuccess) e = cudaMalloc(&h->d_pool, pool_bytes);
-  if (e == cudaSuccess) e = cudaMemset(h->d_pool, 0, pool_bytes);
   if (e == cudaSuccess) e = cudaMalloc(&h->d_free, sizeof(int32_t) * pool_pages);
   if (e == cudaSuccess) e = cudaMalloc(&h->d_err, sizeof(int));
-  if (e == cudaSuccess) e = cudaMemset(h->d_err, 0, sizeof(int));
-  if (e == cudaSuccess) {
-    // page skipping's scratch (query means, estimates, kept list)
-    const size_t bytes = sizeof(float) * (kMaxHeads * kHeadDim + kMaxSampledEntries) +
-                         sizeof(uint16_t) * kMaxSampledEntries + sizeof(unsigned);
-    e = cudaMalloc(&h->d_select, bytes);
-    if (e == cudaSuccess) e = cudaMemset(h->d_select, 0, bytes);
-  }
+  if (e == cudaSuccess) e = cudaMalloc(&h->d_select, select_bytes);
   if (e == cudaSuccess && !fp8) {
-    // the mean-key cache of page skipping (1 / page_size of the pool's bytes),
-    // every tag -1 (nothing cached)
+    // the mean-key cache of page skipping (1 / page_size of the pool's bytes)
     e = cudaMalloc(&h->d_km, sizeof(float) * (size_t)layers * pool_pages * heads * head_dim);
     if (e == cudaSuccess) e = cudaMalloc(&h->d_km_len, sizeof(int) * (size_t)layers * pool_pages);
-    if (e == cudaSuccess) e = cudaMemset(h->d_km_len, 0xFF, sizeof(int) * (size_t)layers * pool_pages);
   }
   if (e == cudaSuccess) {
     // free stack bottom..top = P-1 .. 0, so pops hand out 0, 1, 2, ...
     std::vector<int32_t> init(pool_pages);
     for (int i = 0; i < pool_pages; ++i) init[i] = pool_pages - 1 - i;
-    e = cudaMemcpy(h->d_free, init.data(), sizeof(int32_t) * pool_pages, cudaMemcpyHostToDevice);
+    SetupStream setup;
+    setup.fill(h->d_pool, 0, pool_bytes);
+    setup.fill(h->d_err, 0, sizeof(int));
+    setup.fill(h->d_select, 0, select_bytes);
+    // every tag -1: nothing cached
+    if (!fp8) setup.fill(h->d_km_len, 0xFF, sizeof(int) * (size_t)layers * pool_pages);
+    setup.copy_in(h->d_free, init.data(), sizeof(int32_t) * pool_pages);
+    e = setup.wait();
   }
   if (e != cudaSuccess) {
     std::string msg = std::string("pkv_create: ") + cudaGetErrorString(e);
@@ -406,10 +406,11 @@ pkv_status pkv_stream_open(pkv_t h, const pkv_stream_cfg* cfg, int* stream_id) {
   if (pkv_status r = ensure_scratch(h, stream_scratch_need(h, c))) return r;
   cudaError_t e = cudaMalloc(&st.d_mem, words * sizeof(int32_t));
   if (e != cudaSuccess) return cuda_fail(h, e, "stream_open cudaMalloc");
-  e = cudaMemset(st.d_mem, 0, words * sizeof(int32_t));
-  if (e != cudaSuccess) {
+  SetupStream setup;
+  setup.fill(st.d_mem, 0, words * sizeof(int32_t));
+  if ((e = setup.wait()) != cudaSuccess) {
     cudaFree(st.d_mem);
-    return cuda_fail(h, e, "stream_open cudaMemset");
+    return cuda_fail(h, e, "stream_open: clearing the lists");
   }
   int32_t* p = st.d_mem;
   if (c.mode == PKV_MODE_FRAME) {

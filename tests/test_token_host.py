@@ -36,7 +36,6 @@ def handle(lib, request):
     h = ctypes.c_void_p()
     create = lib.pkv_create_fp8 if request.param else lib.pkv_create_ex
     assert create(20, 16, 2, 64, 2, 8, ctypes.byref(h)) == OK
-    lib.cudaDeviceSynchronize()
     yield h
     lib.fake_set_device(0)
     assert lib.pkv_destroy(h) == OK
@@ -48,10 +47,27 @@ def open_tokens(lib, h, *args):
     return lib.pkv_stream_open_tokens(h, *args, ctypes.byref(sid)), sid.value
 
 
+def test_a_new_handle_is_ready(lib, handle):
+    """Neither may anything that creating a handle has queued."""
+    assert lib.fake_queued() == 0
+
+
+@pytest.mark.parametrize("cfg", [dict(mode=0, num_scale=2, window=4, n_patch=16, n_special=6),
+                                 dict(mode=1, chunk_size=4, sliding_window_num=3, tokens_per_frame=22)],
+                         ids=["frames", "chunks"])
+def test_an_opened_frame_stream_is_ready(lib, handle, cfg):
+    from paged_kv_cache_build_gb300._lib import StreamCfg
+    sid = ctypes.c_int(-1)
+    lib.cudaDeviceSynchronize()
+    assert lib.pkv_stream_open(handle, ctypes.byref(StreamCfg(**cfg)), ctypes.byref(sid)) == OK
+    assert lib.fake_queued() == 0
+
+
 def test_an_opened_stream_is_ready(lib, handle):
     """Nothing that open has queued may still be to come when it returns: the caller's
     streams are not ordered behind the one that it was queued on."""
     for _ in range(2):                           # the first one lays out the handle's workspace, too
+        lib.cudaDeviceSynchronize()
         r, _ = open_tokens(lib, handle, 100, 0, 0)
         assert r == OK
         assert lib.fake_queued() == 0
