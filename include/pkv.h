@@ -448,8 +448,9 @@ pkv_status pkv_attend_noalloc(pkv_t h, const void* q, int n_q, int stream_id, in
  * token's row to the next one's (0: contiguous), multiples of 8, so that q, k and v
  * may be parts of one tensor. The other calls that take a stream (close, reset,
  * rollback, evict, visible page table, export) work on token streams; the frame
- * and chunk calls refuse them with STATE. Every call below refuses a current device
- * other than the handle's with INVALID. */
+ * and chunk calls refuse them with STATE. Every call on a token stream that uses the
+ * device, and pkv_stream_open_tokens, refuses a current device other than the handle's
+ * with INVALID. */
 
 /* Open a token stream of at most max_tokens tokens (dropped tokens not counted).
  * window > 0: pkv_evict_window frees the pages whose tokens no later query sees

@@ -124,6 +124,8 @@ pkv_status fail(pkv_t h, pkv_status st, const char* fmt, ...);
 pkv_status cuda_fail(pkv_t h, cudaError_t e, const char* what);
 PoolView pool_view(pkv_t h, int layer);
 pkv_status get_stream(pkv_t h, int sid, Stream** out);
+// Refuses a current device other than the handle's.
+pkv_status check_device(pkv_t h);
 pkv_status push_pages(pkv_t h, const PushSegment* segs, int n_seg, cudaStream_t s);
 PushSegment seg(const int32_t* src, int start, int count, int step = 1, int ring = 0);
 // Grows the handle's split-KV scratch (synchronises the device when it has to).

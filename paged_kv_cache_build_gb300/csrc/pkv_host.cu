@@ -74,9 +74,24 @@ pkv_status get_stream(pkv_t h, int sid, Stream** out) {
   return PKV_OK;
 }
 
+pkv_status check_device(pkv_t h) {
+  int dev = -1;
+  PKV_CUDA(h, cudaGetDevice(&dev));
+  if (dev != h->device)
+    return fail(h, PKV_ERR_INVALID, "the handle lives on device %d, the current device is %d", h->device, dev);
+  return PKV_OK;
+}
+
 }  // namespace pkv
 
 namespace {
+
+// get_stream for the calls that work on the device for every kind of stream: a token
+// stream's refuse another current device, as the token calls do.
+pkv_status get_device_stream(pkv_t h, int sid, Stream** out) {
+  if (pkv_status r = get_stream(h, sid, out)) return r;
+  return (*out)->cfg.mode == kModeTokens ? check_device(h) : PKV_OK;
+}
 
 // Visible table size from the counters.
 void visible_counts(const pkv_ctx* h, const Stream& st, int* n_pages, int* n_tokens, int* last) {
@@ -473,7 +488,7 @@ static void clear_counters(Stream* st) {
 
 pkv_status pkv_stream_close(pkv_t h, int sid, void* cuda_stream) {
   Stream* st = nullptr;
-  if (pkv_status r = get_stream(h, sid, &st)) return r;
+  if (pkv_status r = get_device_stream(h, sid, &st)) return r;
   if (pkv_status r = free_stream_pages(h, st, as_stream(cuda_stream))) return r;
   // the list memory may still be read by the push just launched
   PKV_CUDA(h, cudaStreamSynchronize(as_stream(cuda_stream)));
@@ -484,7 +499,7 @@ pkv_status pkv_stream_close(pkv_t h, int sid, void* cuda_stream) {
 
 pkv_status pkv_stream_reset(pkv_t h, int sid, void* cuda_stream) {
   Stream* st = nullptr;
-  if (pkv_status r = get_stream(h, sid, &st)) return r;
+  if (pkv_status r = get_device_stream(h, sid, &st)) return r;
   if (pkv_status r = free_stream_pages(h, st, as_stream(cuda_stream))) return r;
   clear_counters(st);
   return PKV_OK;
@@ -676,7 +691,7 @@ pkv_status pkv_append_frame(pkv_t h, int sid, int layer, const void* k, const vo
 
 pkv_status pkv_rollback_last_frame(pkv_t h, int sid, void* cuda_stream) {
   Stream* st = nullptr;
-  if (pkv_status r = get_stream(h, sid, &st)) return r;
+  if (pkv_status r = get_device_stream(h, sid, &st)) return r;
   cudaStream_t s = as_stream(cuda_stream);
   if (st->cfg.mode == kModeTokens) return token_rollback(h, st, s);
   if (!st->pending) return fail(h, PKV_ERR_STATE, "nothing to roll back");
@@ -772,7 +787,7 @@ static pkv_status window_reset(pkv_t h, Stream* st, cudaStream_t s) {
 
 pkv_status pkv_evict_window(pkv_t h, int sid, void* cuda_stream) {
   Stream* st = nullptr;
-  if (pkv_status r = get_stream(h, sid, &st)) return r;
+  if (pkv_status r = get_device_stream(h, sid, &st)) return r;
   cudaStream_t s = as_stream(cuda_stream);
   const pkv_stream_cfg& c = st->cfg;
   if (c.mode == kModeTokens) return token_evict(h, st, s);
@@ -816,7 +831,7 @@ pkv_status pkv_build_visible_page_table(pkv_t h, int sid, int32_t* d_idx, int32_
                                         int capacity, int32_t* d_n, int32_t* d_last_page_len,
                                         void* cuda_stream) {
   Stream* st = nullptr;
-  if (pkv_status r = get_stream(h, sid, &st)) return r;
+  if (pkv_status r = get_device_stream(h, sid, &st)) return r;
   int np, nt, last;
   visible_counts(h, *st, &np, &nt, &last);
   if (np > 0 && (!d_idx || !d_len)) return fail(h, PKV_ERR_INVALID, "null table buffers");
@@ -1320,7 +1335,7 @@ pkv_status pkv_free_pages(pkv_t h, int* n_free) {
 pkv_status pkv_export_state(pkv_t h, int sid, int32_t* host_buf, size_t cap_words,
                             size_t* used_words) {
   Stream* st = nullptr;
-  if (pkv_status r = get_stream(h, sid, &st)) return r;
+  if (pkv_status r = get_device_stream(h, sid, &st)) return r;
   if (!host_buf || !used_words) return fail(h, PKV_ERR_INVALID, "null argument");
   int np, nt, last;
   visible_counts(h, *st, &np, &nt, &last);

@@ -30,10 +30,7 @@ pkv_status check_batch(pkv_t h, int n, const int* sids, const int* row_off) {
   if (!h) return fail(h, PKV_ERR_INVALID, "null handle");
   if (n < 1 || n > kMaxTokenBatch || !sids)
     return fail(h, PKV_ERR_INVALID, "a batch names 1..%d streams", kMaxTokenBatch);
-  int dev = -1;
-  PKV_CUDA(h, cudaGetDevice(&dev));
-  if (dev != h->device)
-    return fail(h, PKV_ERR_INVALID, "the handle lives on device %d, the current device is %d", h->device, dev);
+  if (pkv_status r = check_device(h)) return r;
   const unsigned long long mark = ++h->batch_no;
   for (int i = 0; i < n; ++i) {
     Stream* st = nullptr;
@@ -154,6 +151,7 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
     return fail(h, PKV_ERR_INVALID, "max_tokens %d outside 1..2^28", max_tokens);
   if (window < 0 || sinks < 0 || (window == 0 && sinks > 0))
     return fail(h, PKV_ERR_INVALID, "window and sinks >= 0 required (no sinks without a window)");
+  if (pkv_status r = check_device(h)) return r;
   int sid = -1;
   for (int i = 0; i < h->max_streams && sid < 0; ++i)
     if (!h->streams[i].open) sid = i;

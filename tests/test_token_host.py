@@ -71,3 +71,50 @@ def test_an_opened_stream_is_ready(lib, handle):
         r, _ = open_tokens(lib, handle, 100, 0, 0)
         assert r == OK
         assert lib.fake_queued() == 0
+
+
+def test_another_device_is_refused(lib, handle):
+    """Nothing is allocated or launched for a handle of device 0 while device 1 is
+    current, and the state stays; on its own device the same calls work."""
+    r, sid = open_tokens(lib, handle, 100, 20, 0)
+    assert r == OK
+    ints = lambda *x: (ctypes.c_int * len(x))(*x)
+    rows = 2 * 64 * 2                            # bytes of a token's K or V
+    mem = ctypes.create_string_buffer(90 * rows + 16)
+    at = (ctypes.addressof(mem) + 15) // 16 * 16
+    n = ctypes.c_size_t()
+    words = (ctypes.c_int32 * 200)()
+    table = (ctypes.c_int32 * 50)()
+    table_at = ctypes.addressof(table)
+    append = lambda c: lib.pkv_append_tokens(handle, 1, ints(sid), ints(0, c), 0, at, at, 0, 0, None)
+    assert append(40) == OK
+    calls = {
+        "open": lambda: open_tokens(lib, handle, 100, 0, 0)[0],
+        "append": lambda: append(3),
+        "rollback": lambda: lib.pkv_rollback_last_frame(handle, sid, None),
+        "append again": lambda: append(50),
+        "read": lambda: lib.pkv_read_tokens(handle, 1, ints(sid), None, ints(0, 5), 0, at, at, None),
+        "attend": lambda: lib.pkv_attend_tokens(handle, at, 2, 0, ints(0, 1), ints(sid), 1, 0, at, 20, 0, 0.0, None),
+        "drop": lambda: lib.pkv_drop_tokens(handle, 1, ints(sid), ints(20), None),
+        "evict": lambda: lib.pkv_evict_window(handle, sid, None),
+        "table": lambda: lib.pkv_build_visible_page_table(handle, sid, table_at, table_at, 50, None, None, None),
+        "export": lambda: lib.pkv_export_state(handle, sid, words, 200, ctypes.byref(n)),
+        "reset": lambda: lib.pkv_stream_reset(handle, sid, None),
+        "close": lambda: lib.pkv_stream_close(handle, sid, None),
+    }
+
+    def state():
+        v = [ctypes.c_int() for _ in range(4)]
+        assert lib.pkv_token_info(handle, sid, *map(ctypes.byref, v[:3])) == OK
+        assert lib.pkv_free_pages(handle, ctypes.byref(v[3])) == OK
+        return [x.value for x in v] + [lib.fake_launches(), lib.fake_alloc_calls()]
+
+    for name, call in calls.items():
+        before = state()
+        lib.fake_set_device(1)
+        assert call() == INVALID, name
+        assert b"device" in lib.pkv_last_error(handle)
+        lib.fake_set_device(0)
+        assert state() == before, name
+        assert call() == OK, name
+    assert lib.fake_allocs(1) == 0
