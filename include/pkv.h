@@ -509,7 +509,8 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* stream_ids, const int* pos
  * q: device bf16 [row_off[n]][q_heads][64], rows q_stride apart; out: the same,
  * contiguous. fp32 accumulation and softmax; the probabilities are rounded to bf16
  * for the second product, or, in streams with few rows x query heads per KV head
- * (up to 64) on E4M3 pages, to f16 (and q as well). sm_scale <= 0 means 1 / sqrt(64).
+ * (up to 64) on E4M3 pages, to f16 (and q as well), which loses what is below 2^-39 of an
+ * output row's largest contribution. sm_scale <= 0 means 1 / sqrt(64).
  * Results depend on the batch only by rounding (the kernel and the split of the keys
  * are chosen for the whole call) and are the same bits for the same call. The
  * handle's partial results are shared by its calls: order them on one CUDA stream.

@@ -26,7 +26,9 @@
 // elements 2^-14 below the row's largest), the K row's exponent is added to the
 // score, and the V row's exponent is folded into P, which keeps a reference of its
 // own: w_j = 2^(s_j + e_j - R), R the running maximum of s_j + e_j minus 15 (so that f16
-// holds w from 2^15 down to 2^-24), O = 2^(R - m) sum_j w_j code_j.
+// holds w from 2^15 down to 2^-24), O = 2^(R - m) sum_j w_j code_j. Rows of zeros are left
+// out of R; any other row has a code of 224 or more (but for magnitudes near bf16's least),
+// so what f16 loses is 2^-39 of a row's largest contribution.
 #include "pkv_ptx.cuh"
 #include "pkv_tokens.cuh"
 
@@ -302,6 +304,7 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
       const int B = Ps >= kTokTile ? kTokTile : Ps;    // rows of an E4M3 block
       float sc[4][NT][4];                        // S^T: slot (16 sg +) g | g + 8, query 2 tq | + 1
       float ve[4][2];                            // E4M3: exponents of the V rows g, g + 8
+      float prod = 1.f;                          // E4M3: of the exponents; 0 if one of them is 0
 #pragma unroll
       for (int sg = 0; sg < 4; ++sg) {
 #pragma unroll
@@ -315,6 +318,7 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
             c[i] = *reinterpret_cast<const uint4*>(kt + blk + rb * kHeadDim + 16 * tq);
             ke[i] = __uint_as_float((uint32_t)(127 + (int8_t)kt[blk + B * kHeadDim + rb]) << 23);
             ve[sg][i] = (float)(int8_t)vt[blk + B * kHeadDim + rb];
+            prod *= ve[sg][i];
           }
           const uint32_t c0[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
           const uint32_t c1[4] = {c[1].x, c[1].y, c[1].z, c[1].w};
@@ -338,6 +342,27 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma_16816(sc[sg][n], ka, qb[n][kk][0], qb[n][kk][1]);
           }
+        }
+      }
+      if constexpr (FP8) {
+        // A row of zeros is stored with exponent 0 (others have it for magnitudes of 224 and
+        // more only). It brings nothing to O, so it must not raise R: its exponent is -inf.
+        // (Looking for it costs 1.5 to 2 % of a call of single tokens; a product of the
+        // exponents less than eight comparisons.)
+        if (__any_sync(0xffffffffu, prod == 0.f)) {
+          uint32_t zeros = 0;                    // bit 2 sg + i
+#pragma unroll 1
+          for (int u = 0; u < 8; ++u) {
+            const int r = 8 * u + g, rb = r & (B - 1);
+            const uint4 c = *reinterpret_cast<const uint4*>(vt + (r - rb) * (kHeadDim + 1) + rb * kHeadDim + 16 * tq);
+            uint32_t any = (c.x | c.y | c.z | c.w) & 0x7F7F7F7Fu;
+            any |= __shfl_xor_sync(0xffffffffu, any, 1);
+            any |= __shfl_xor_sync(0xffffffffu, any, 2);
+            if (any == 0u) zeros |= 1u << u;
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if ((zeros >> u) & 1u) ve[u >> 1][u & 1] = -INFINITY;
         }
       }
       const bool full = tok_tile_full(b, w.p0, w.p1, a.window, a.sinks);

@@ -46,3 +46,56 @@ def test_a_stream_opened_behind_a_busy_default_stream(fp8):
             torch.cuda.synchronize()
         p.cache.sync()
         p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 3, 7, 300])
+@pytest.mark.parametrize("ahead,size", [(0, 1e-10), (14, 1e-4), (20, 1e-3), (25, 1e-2), (30, 1.0), (-20, 1e-12)])
+def test_a_key_whose_value_is_zero(ahead, size, new, fp8):
+    """Rows of zeros among small values, their scores 2^ahead times the others': they
+    take weight and bring nothing, and the others' values keep their bits."""
+    p = Pool(200, 16, 2, fp8, seed=new)
+    n = 1500 + new
+    sid = p.open(n)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    k = torch.randn((n, 2, 64), generator=g, device="cuda")
+    v = torch.randn((n, 2, 64), generator=g, device="cuda") * size
+    q = torch.randn((new, 8, 64), generator=g, device="cuda")
+    q[..., 0] = 8.0
+    k[..., 0] = 0.0
+    zero = [0, 17, 700, 1499]                    # the sink's place, and others
+    k[zero] = 0.0
+    k[zero, :, 0] = ahead * float(np.log(2.0))   # times 8 and the scale of 1/8
+    v[zero] = 0.0
+    v[17] = -0.0
+    k, v, q = k.bfloat16(), v.bfloat16(), q.bfloat16()
+    p.cache.append_tokens(p.cache.token_batch([sid], [n]), k, v)
+    out = p.cache.attend_tokens(p.cache.token_batch([sid], [new]), q)
+    p.cache.sync()
+    kk, vv, qq = stored(k, fp8), stored(v, fp8), f64(q)
+    ref = causal_attend_fp64(qq, kk, vv, n - new, 0, 0, SCALE)
+    assert (np.abs(f64(out) - ref) / tolerance(qq, kk, vv, ref, n - new, 0, 0, SCALE)).max() <= 1
+    p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 5, 300])
+def test_values_that_are_all_zero(new, fp8):
+    """A stream of zeros, and zeros up to the last keys, which no other part of the table
+    knows of."""
+    p = Pool(300, 16, 2, fp8)
+    n = 1500 + new
+    k, q = p.rows(n, 2), p.rows(new, 4)
+    for tail in (0, 1, 70):
+        sid = p.open(n)
+        v = torch.zeros_like(k)
+        if tail:
+            v[n - tail:] = p.rows(tail, 2)
+        p.cache.append_tokens(p.cache.token_batch([sid], [n]), k, v)
+        out = p.cache.attend_tokens(p.cache.token_batch([sid], [new]), q)
+        kk, vv, qq = stored(k, fp8), stored(v, fp8), f64(q)
+        ref = causal_attend_fp64(qq, kk, vv, n - new, 0, 0, SCALE)
+        assert (np.abs(f64(out) - ref) <= tolerance(qq, kk, vv, ref, n - new, 0, 0, SCALE)).all()
+        p.cache.sync()
+        p.cache.close_stream(sid)
+    p.cache.close()
