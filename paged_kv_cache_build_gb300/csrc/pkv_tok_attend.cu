@@ -189,15 +189,13 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
       const uint8_t* src = nullptr;
       if (base + lane / per < nT) {
         const int f = tok_tile(tiles, j0 + base + lane / per) * kTokTile + (lane % per) * rows;
-        // blocks behind the last page repeat it: their slots are masked
-        const int e = f / Ps;
-        int page = t.pages[min(e, t.n_pages - 1)];
+        int page = t.pages[tok_block_entry(f, rows, w.p0, w.p1, a.window, a.sinks, Ps)];
         if (page < 0 || page >= a.pool.pool_pages) {
           atomicOr(a.err, kErrPageRange);
           page = 0;
         }
         src = reinterpret_cast<const uint8_t*>(a.pool.base) + (long long)page * a.pool.page_bytes +
-              w.head * plane + (f - e * Ps) * kRowBytes;
+              w.head * plane + (f % Ps) * kRowBytes;
       }
       const int end = min(nT, base + group);
       for (int j = base; j < end; ++j) {

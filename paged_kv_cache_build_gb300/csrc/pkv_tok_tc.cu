@@ -112,7 +112,7 @@ struct __align__(1024) TcSmem {
   TokenWork work;
   TokTiles tiles;
   int j0, j1;                    // its tiles
-  int row0, pos0, n_pages, splits;
+  int row0, pos0, splits;
   const int32_t* pages;
   uint32_t tmem_base;
   int abort;
@@ -216,7 +216,6 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     sm.j1 = (int)((long long)tiles.n * (w.split + 1) / t.splits);
     sm.row0 = t.row0;
     sm.pos0 = t.pos0;
-    sm.n_pages = t.n_pages;
     sm.splits = t.splits;
     sm.pages = t.pages;
   }
@@ -261,7 +260,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     // ---------------------------------------------------------------- producer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8>));
     const int Ps = a.pool.page_size;
-    const int nT = sm.j1 - sm.j0, j0 = sm.j0, n_pages = sm.n_pages, head = w.head;
+    const int nT = sm.j1 - sm.j0, j0 = sm.j0, p0 = w.p0, p1 = w.p1, head = w.head;
     const TokTiles tiles = sm.tiles;
     const int32_t* pages = sm.pages;
     // The page blocks of the next 32 / per tiles, one per lane: their addresses are
@@ -281,15 +280,13 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
       const uint8_t* src = nullptr;
       if (base + lane / per < nT) {
         const int f = tok_tile(tiles, j0 + base + lane / per) * kBN + (lane % per) * rows;
-        // blocks behind the last page repeat it: their slots are masked
-        const int e = f / Ps;
-        int page = pages[min(e, n_pages - 1)];
+        int page = pages[tok_block_entry(f, rows, p0, p1, a.window, a.sinks, Ps)];
         if (page < 0 || page >= a.pool.pool_pages) {
           atomicOr(a.err, kErrPageRange);
           page = 0;
         }
         src = reinterpret_cast<const uint8_t*>(a.pool.base) + (long long)page * a.pool.page_bytes +
-              head * plane + (f - e * Ps) * kRowBytes;
+              head * plane + (f % Ps) * kRowBytes;
       }
       const int end = min(nT, base + group);
       for (int j = base; j < end; ++j) {

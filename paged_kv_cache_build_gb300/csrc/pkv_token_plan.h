@@ -139,6 +139,15 @@ PKV_HD TokSpan tok_span(int p0, int p1, int window, int sinks) {
   s.f1 = (p0 + 1) / kTokTile;
   return s;
 }
+// The page list entry that slots f .. f + rows - 1 of a tile (rows of one page) are read
+// from for queries at positions p0 .. p1. Where none of them sees any of the slots, the
+// entry may be freed, its page another stream's by now, and what that holds may be no
+// number (0 * NaN is NaN in a product): such a block takes its masked rows from the page of
+// p1, which the stream holds.
+PKV_HD int tok_block_entry(int f, int rows, int p0, int p1, int window, int sinks, int page_size) {
+  const bool seen = f <= p1 && (f + rows > tok_window_lo(p0, window) || f < sinks);
+  return (seen ? f : p1) / page_size;
+}
 // Bit i: whether slot b + i is seen from position p.
 PKV_HD uint64_t tok_mask(int b, int p, int window, int sinks) {
   return tok_low_bits(p - b + 1) & (~tok_low_bits(tok_window_lo(p, window) - b) | tok_low_bits(sinks - b));

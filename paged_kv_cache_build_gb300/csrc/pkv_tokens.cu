@@ -373,7 +373,6 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
     it.row0 = row_off[i];
     it.n = rows;
     it.pos0 = t.len - rows;
-    it.n_pages = t.n_pages;
   }
   // one launch per kernel: the streams' rows per KV head decide
   cudaStream_t s = as_stream(cuda_stream);

@@ -66,7 +66,6 @@ struct TokenQuery {
   const int32_t* pages;
   int row0, n;                      // its token rows in q and out
   int pos0;                         // position of the first
-  int n_pages;
   int cta0;                         // its first CTA
   int blocks, splits;
 };

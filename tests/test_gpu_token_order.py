@@ -99,3 +99,30 @@ def test_values_that_are_all_zero(new, fp8):
         p.cache.sync()
         p.cache.close_stream(sid)
     p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("new", [1, 7, 40, 300])
+def test_another_streams_values_cannot_be_seen(new, page, fp8):
+    """Pages that left a window hold another stream's rows, none of them finite: the tiles at
+    the edges of the window and of the sinks, which cover such pages, bring nothing of them."""
+    window, sinks = 20, 3
+    p = Pool(64, page, 2, fp8, layers=2)
+    a, b = p.open(window=window, sinks=sinks), p.open()
+    for n in (403, 77):                          # two evictions: pages at the front and the back
+        p.append([a], [n])
+        p.cache.evict_window(a)
+        p.ora.evict(a)
+    p.append([a], [new])
+    free = p.cache.free_pages()
+    batch = p.cache.token_batch([b], [free * page])
+    bad = torch.full((free * page, 2, 64), float("nan"), device="cuda", dtype=torch.bfloat16)
+    bad[::3] = float("inf")
+    for layer in range(2):
+        p.cache.append_tokens(batch, bad, bad, layer=layer)
+    assert p.cache.free_pages() == 0
+    for layer in range(2):
+        p.check_attend([a], [new], 2, window, sinks, layer=layer)
+        p.check_attend([a], [min(new, 5)], 4, 2, 1, layer=layer)
+    p.cache.close()
