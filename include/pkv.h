@@ -443,7 +443,9 @@ pkv_status pkv_attend_noalloc(pkv_t h, const void* q, int n_q, int stream_id, in
  * are served by one call: a batch names n streams (1 .. 256, each once), and the
  * rows of all of them lie back to back in one tensor, rows row_off[i] ..
  * row_off[i + 1] - 1 being stream stream_ids[i]'s (n + 1 host ints that start at 0
- * and do not fall; a stream may have no row). Values must be finite.
+ * and do not fall; a stream may have no row). Values must be finite: what is not makes
+ * the outputs of its stream's rows meaningless (mostly NaN; on E4M3 pages they may be
+ * numbers), no other stream's.
  * Rows may be strided: k_stride, v_stride and q_stride are the elements from one
  * token's row to the next one's (0: contiguous), multiples of 8, so that q, k and v
  * may be parts of one tensor. The other calls that take a stream (close, reset,

@@ -121,7 +121,7 @@ __device__ __forceinline__ float4 join_splits(const Args& a, long long pr0, int 
     }
 #pragma unroll
     for (int k = 0; k < kFold; ++k) {
-      if (!(ml[k].y > 0.f)) continue;
+      if (ml[k].y == 0.f) continue;              // every key masked (a sum that is no number is kept)
       const float m_new = fmaxf(m, ml[k].x);
       const float c = fast_exp2(m - m_new), w = fast_exp2(ml[k].x - m_new);
       l = l * c + w * ml[k].y;

@@ -126,3 +126,29 @@ def test_another_streams_values_cannot_be_seen(new, page, fp8):
         p.check_attend([a], [new], 2, window, sinks, layer=layer)
         p.check_attend([a], [min(new, 5)], 4, 2, 1, layer=layer)
     p.cache.close()
+
+
+@pytest.mark.parametrize("new,fp8", [(1, False), (5, False), (40, False), (300, False), (1, True), (5, True)])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_a_value_that_is_no_number_shows(what, new, fp8):
+    """A visible key or value that is no number shows in every row that sees it, with the
+    keys split over CTAs or not, and in no other head (on E4M3 pages with few rows: the
+    matrix-unit kernel's conversion has no such code)."""
+    p = Pool(300, 16, 2, fp8, max_streams=64)
+    n = 3000 + new
+    k, v, q = p.rows(n, 2), p.rows(n, 2), p.rows(new, 4)
+    (k if what == "k" else v)[100, 1] = float("nan")
+    sid = p.open(n)
+    p.cache.append_tokens(p.cache.token_batch([sid], [n]), k, v)
+    short = [p.open(1) for _ in range(50)]       # streams that fill the card with one CTA a block
+    p.cache.append_tokens(p.cache.token_batch(short, [1] * 50), k[-50:], v[-50:])
+    for others in ([], short):
+        batch = p.cache.token_batch([sid] + others, [new] + [1] * len(others))
+        qq = torch.cat([q, p.rows(len(others), 4)])
+        out = p.cache.attend_tokens(batch, qq)
+        assert torch.isnan(out[:new, 2:]).all()
+        assert torch.isfinite(out[:new, :2]).all() and torch.isfinite(out[new:]).all()
+    # a window that begins behind it hides it
+    assert torch.isfinite(p.cache.attend_tokens(p.cache.token_batch([sid], [new]), q, window=2000)).all()
+    p.cache.sync()
+    p.cache.close()
