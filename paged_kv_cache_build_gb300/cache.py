@@ -40,6 +40,14 @@ def chunked_stream_cfg(chunk_size, sliding_window_num, tokens_per_frame):
                      tokens_per_frame)
 
 
+def _cut_short(*numbers):
+    """Whether C's int would hold another number."""
+    for x in numbers:                            # (any() takes five times as long)
+        if x >> 31 not in (0, -1):
+            return True
+    return False
+
+
 class TokenBatch:
     """The streams of a token call and how many rows each has, for every layer's calls
     of a step (PagedKVCache.token_batch)."""
@@ -50,7 +58,7 @@ class TokenBatch:
             raise ValueError("one count per stream")
         if any(c < 0 for c in counts):
             raise ValueError("counts must not be negative")
-        if any(s >> 31 not in (0, -1) for s in sids):
+        if _cut_short(*sids):
             raise ValueError("a stream id is no 32-bit number")
         n = len(sids)
         off = [0]
@@ -315,7 +323,7 @@ class PagedKVCache:
         """pkv_stream_open_tokens: a causal stream of up to max_tokens tokens; with a
         window, evict_window(sid) frees what no later query of such a window sees
         (the first `sinks` tokens' pages stay)."""
-        if any(x >> 31 not in (0, -1) for x in (max_tokens, window, sinks)):
+        if _cut_short(max_tokens, window, sinks):
             raise ValueError("max_tokens, window and sinks must be 32-bit numbers")
         sid = ctypes.c_int(-1)
         self._check(self.lib.pkv_stream_open_tokens(self.h, max_tokens, window, sinks, ctypes.byref(sid)))
@@ -349,6 +357,8 @@ class PagedKVCache:
     def append_tokens(self, batch, k, v, layer=0, stream=None):
         """pkv_append_tokens: k and v, [batch rows][heads][64], behind the batch's
         streams' tokens."""
+        if _cut_short(layer):
+            raise ValueError("layer must be a 32-bit number")
         kp, ks = self._rows(k, "k", batch, self.heads)
         vp, vs = self._rows(v, "v", batch, self.heads)
         self._check(self.lib.pkv_append_tokens(self.h, batch.n, batch.sids, batch.row_off, layer, kp, vp,
@@ -361,6 +371,8 @@ class PagedKVCache:
     def read_tokens(self, batch, pos0=None, layer=0, k_out=None, v_out=None, stream=None):
         """pkv_read_tokens: (k, v) of each stream's positions pos0[i] .. (its rows of
         the batch; pos0 None: its last ones), [batch rows][heads][64] bf16."""
+        if _cut_short(layer):
+            raise ValueError("layer must be a 32-bit number")
         shape = (batch.rows, self.heads, self.head_dim)
         outs = []
         for name, t in (("k_out", k_out), ("v_out", v_out)):
@@ -374,7 +386,7 @@ class PagedKVCache:
         if pos0 is not None:
             if len(pos0) != batch.n:
                 raise ValueError("one first position per stream")
-            if any(p >> 31 not in (0, -1) for p in pos0):
+            if _cut_short(*pos0):
                 raise ValueError("a position is no 32-bit number")
             first = (ctypes.c_int * batch.n)(*pos0)
         self._check(self.lib.pkv_read_tokens(self.h, batch.n, batch.sids, first, batch.row_off, layer,
@@ -385,8 +397,8 @@ class PagedKVCache:
         """pkv_attend_tokens: causal attention of the batch's rows (the last tokens of
         its streams) with q, [batch rows][q_heads][64]; q_heads is a multiple of the
         cache's heads. window, sinks: see pkv_attend_tokens."""
-        if window >> 31 not in (0, -1) or sinks >> 31 not in (0, -1):   # C would cut them short
-            raise ValueError("window and sinks must be 32-bit numbers (window 0: none)")
+        if _cut_short(layer, window, sinks):
+            raise ValueError("layer, window and sinks must be 32-bit numbers (window 0: none)")
         qp, qs = self._rows(q, "q", batch)
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -400,6 +412,8 @@ class PagedKVCache:
 
     def token_info(self, sid):
         """(tokens, first evicted position, first position behind them) of a token stream."""
+        if _cut_short(sid):
+            raise ValueError("a stream id is no 32-bit number")
         n, a, b = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
         self._check(self.lib.pkv_token_info(self.h, sid, ctypes.byref(n), ctypes.byref(a), ctypes.byref(b)))
         return n.value, a.value, b.value

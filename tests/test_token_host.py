@@ -118,3 +118,44 @@ def test_another_device_is_refused(lib, handle):
         assert state() == before, name
         assert call() == OK, name
     assert lib.fake_allocs(1) == 0
+
+
+@pytest.fixture
+def cache(lib, handle):
+    """The Python class over the same host code, its tensors in host memory."""
+    import torch
+    from paged_kv_cache_build_gb300 import PagedKVCache
+    c = PagedKVCache.__new__(PagedKVCache)
+    c.lib, c.h, c.device = lib, handle, torch.device("cpu")
+    c.pool_pages, c.page_size, c.heads, c.head_dim, c.layers = 20, 16, 2, 64, 2
+    yield c
+    c.h = None                                   # the handle is its fixture's
+
+
+class HostStream:
+    cuda_stream = 0
+
+
+def rows(n, heads):
+    import torch
+    mem = torch.zeros(n * heads * 64 + 8, dtype=torch.bfloat16)
+    at = (-mem.data_ptr() % 16) // 2
+    return mem[at:at + n * heads * 64].view(n, heads, 64)
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 1, -2 ** 31 - 1])
+def test_numbers_past_32_bits_are_refused(lib, cache, big):
+    """A layer or stream id that C would cut down to a valid one."""
+    sid = cache.open_token_stream(100)
+    b = cache.token_batch([sid], [3])
+    s = HostStream()
+    cache.append_tokens(b, rows(3, 2), rows(3, 2), stream=s)
+    launches = lib.fake_launches()
+    for call in (lambda: cache.append_tokens(b, rows(3, 2), rows(3, 2), layer=big, stream=s),
+                 lambda: cache.attend_tokens(b, rows(3, 4), layer=big, out=rows(3, 4), stream=s),
+                 lambda: cache.read_tokens(b, layer=big, k_out=rows(3, 2), v_out=rows(3, 2), stream=s),
+                 lambda: cache.token_info(big)):
+        with pytest.raises(ValueError):
+            call()
+    assert lib.fake_launches() == launches
+    assert cache.token_info(sid)[0] == 3
