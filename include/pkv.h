@@ -517,7 +517,8 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* stream_ids, const int* pos
  * are chosen for the whole call) and are the same bits for the same call. The
  * handle's partial results are shared by its calls: order them on one CUDA stream.
  * Errors: INVALID (shape, stride, layer, q_heads, negative window or sinks, sinks
- * without a window, a null or unaligned pointer), STATE (not a token stream; more
+ * without a window, a null or unaligned pointer, an sm_scale above 0 that is no normal
+ * fp32 number, also times log2(e), or NaN), STATE (not a token stream; more
  * rows than tokens; keys that the rows see are evicted). */
 pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
                              const int* stream_ids, int n, int layer, void* out, int window, int sinks,

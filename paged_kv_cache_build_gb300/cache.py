@@ -399,6 +399,8 @@ class PagedKVCache:
         cache's heads. window, sinks: see pkv_attend_tokens."""
         if _cut_short(layer, window, sinks):
             raise ValueError("layer, window and sinks must be 32-bit numbers (window 0: none)")
+        if 0 < sm_scale < 2 ** -126:             # C would take what rounds to 0 for the default
+            raise ValueError("sm_scale is too small for fp32")
         qp, qs = self._rows(q, "q", batch)
         if out is None:
             out = torch.empty_like(q, memory_format=torch.contiguous_format)

@@ -336,6 +336,10 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
     return fail(h, PKV_ERR_INVALID, "q_heads %d must be 1..%d times the cache's %d heads", q_heads, kMaxGroup, h->H);
   if (window < 0 || sinks < 0 || (window == 0 && sinks > 0))
     return fail(h, PKV_ERR_INVALID, "window and sinks >= 0 required (no sinks without a window)");
+  const float scale = sm_scale <= 0.f ? 1.0f / std::sqrt((float)h->D) : sm_scale;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isnormal(scale) || !std::isnormal(scale_log2))
+    return fail(h, PKV_ERR_INVALID, "sm_scale %g (times log2 e) is no normal fp32 number", sm_scale);
   const int group = q_heads / h->H, row = q_heads * kHeadDim;
   if (q_stride == 0) q_stride = row;
   if (pkv_status r = check_stride(h, "q_stride", q_stride, row)) return r;
@@ -354,8 +358,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   a.pool = pool_view(h, layer);
   a.window = window;
   a.sinks = sinks;
-  const float scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt((float)h->D);
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.err = h->d_err;
   a.joined = h->d_joined;
   int first[kMaxTokenBatch], last[kMaxTokenBatch];

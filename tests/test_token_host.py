@@ -159,3 +159,21 @@ def test_numbers_past_32_bits_are_refused(lib, cache, big):
             call()
     assert lib.fake_launches() == launches
     assert cache.token_info(sid)[0] == 3
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), 3e38, 1e39, 2.0 ** -127, 1e-45, 1e-50])
+def test_scales_that_fp32_does_not_hold_are_refused(lib, cache, scale):
+    """sm_scale (times log2 e) has to be a normal fp32 number, or 0 or less: the default."""
+    from paged_kv_cache_build_gb300 import PkvError
+    b = cache.token_batch([cache.open_token_stream(100)], [3])
+    s = HostStream()
+    cache.append_tokens(b, rows(3, 2), rows(3, 2), stream=s)
+    attend = lambda x: cache.attend_tokens(b, rows(3, 4), out=rows(3, 4), sm_scale=x, stream=s)
+    launches = lib.fake_launches()
+    with pytest.raises((PkvError, ValueError)) as e:
+        attend(scale)
+    assert getattr(e.value, "code", "INVALID") == "INVALID"
+    assert lib.fake_launches() == launches
+    for fine in (0.0, -0.0, -1.0, float("-inf"), 2.0 ** -126, 2.3e38, 0.3, 1):
+        attend(fine)
+    assert lib.fake_launches() > launches
