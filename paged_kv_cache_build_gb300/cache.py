@@ -336,6 +336,14 @@ class PagedKVCache:
     def _stream(self, stream):
         return _raw_stream(self.device.index) if stream is None else stream.cuda_stream
 
+    def _new(self, shape, stream):
+        """A bf16 tensor for a call on `stream`, from that stream's memory: a block of the
+        current one's may still be in use there."""
+        if stream is None:
+            return torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+
     def _rows(self, t, name, batch, heads=None):
         """(address, row stride) of a [rows][heads][64] bf16 tensor on the cache's
         device whose rows are contiguous and any multiple of 8 elements apart."""
@@ -377,7 +385,7 @@ class PagedKVCache:
         outs = []
         for name, t in (("k_out", k_out), ("v_out", v_out)):
             if t is None:
-                t = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+                t = self._new(shape, stream)
             elif tuple(t.shape) != shape or t.dtype != torch.bfloat16 or t.device != self.device or \
                     not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous bf16 tensor {list(shape)} on {self.device}")
@@ -403,7 +411,7 @@ class PagedKVCache:
             raise ValueError("sm_scale is too small for fp32")
         qp, qs = self._rows(q, "q", batch)
         if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = self._new(q.shape, stream)
         elif out.shape != q.shape or out.dtype != torch.bfloat16 or out.device != self.device or \
                 not out.is_contiguous():
             raise ValueError(f"out must be a contiguous bf16 tensor {list(q.shape)} on {self.device}")

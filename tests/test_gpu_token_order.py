@@ -152,3 +152,28 @@ def test_a_value_that_is_no_number_shows(what, new, fp8):
     assert torch.isfinite(p.cache.attend_tokens(p.cache.token_batch([sid], [new]), q, window=2000)).all()
     p.cache.sync()
     p.cache.close()
+
+
+def test_outputs_of_a_call_on_a_side_stream():
+    """What the current stream still has to do with memory that was freed there does not
+    reach the outputs of a call on another stream."""
+    p = Pool(40, 64, 2)
+    sid = p.open()
+    p.append([sid], [500])
+    batch = p.cache.token_batch([sid], [300])
+    q = p.rows(300, 4)
+    want = p.cache.attend_tokens(batch, q), *p.cache.read_tokens(batch)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    busy()
+    for shape in ((300, 4, 64), (300, 2, 64), (300, 2, 64)):
+        used = [torch.empty(shape, device="cuda", dtype=torch.bfloat16) for _ in range(3)]
+        for x in used:
+            x.fill_(7.0)                         # behind the busy work
+        del used, x
+    got = p.cache.attend_tokens(batch, q, stream=side), *p.cache.read_tokens(batch, stream=side)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    p.cache.sync()
+    p.cache.close()

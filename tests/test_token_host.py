@@ -177,3 +177,31 @@ def test_scales_that_fp32_does_not_hold_are_refused(lib, cache, scale):
     for fine in (0.0, -0.0, -1.0, float("-inf"), 2.0 ** -126, 2.3e38, 0.3, 1):
         attend(fine)
     assert lib.fake_launches() > launches
+
+
+def test_outputs_of_a_side_streams_call_are_allocated_for_it(lib, cache, monkeypatch):
+    """A block from the current stream's pool may still be in use there."""
+    import contextlib
+    import torch
+    sid = cache.open_token_stream(100)
+    b = cache.token_batch([sid], [3])
+    s = HostStream()
+    cache.append_tokens(b, rows(3, 2), rows(3, 2), stream=s)
+    on, made = [None], []
+
+    @contextlib.contextmanager
+    def stream(x):
+        on[0] = x
+        yield
+        on[0] = None
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    for f in ("empty", "empty_like"):
+        def alloc(like, **kw):
+            made.append(on[0])
+            return rows(*getattr(like, "shape", like)[:2])
+        monkeypatch.setattr(torch, f, alloc)
+    assert cache.attend_tokens(b, rows(3, 4), stream=s).shape == (3, 4, 64)
+    assert made == [s]
+    assert [x.shape for x in cache.read_tokens(b, stream=s)] == [(3, 2, 64)] * 2
+    assert made == [s, s, s]
