@@ -312,7 +312,7 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* sids, const int* pos0, con
       return fail(h, PKV_ERR_INVALID, "stream %d: positions %d.. (%d rows) of %d tokens", sids[i], p0, rows, t.len);
     // evicted: what lies between the sinks' pages and the first live one
     const long long gap0 = (long long)t.keep0 * h->Ps, gap1 = (long long)t.gap1 * h->Ps;
-    if (rows > 0 && p0 < gap1 && (long long)p0 + rows > gap0)
+    if (rows > 0 && gap1 > gap0 && p0 < gap1 && (long long)p0 + rows > gap0)
       return fail(h, PKV_ERR_STATE, "stream %d: positions %lld..%lld are evicted", sids[i], gap0, gap1 - 1);
     TokenRows& it = a.item[i];
     it.pages = st.d_pages;

@@ -205,3 +205,27 @@ def test_outputs_of_a_side_streams_call_are_allocated_for_it(lib, cache, monkeyp
     assert made == [s]
     assert [x.shape for x in cache.read_tokens(b, stream=s)] == [(3, 2, 64)] * 2
     assert made == [s, s, s]
+
+
+@pytest.mark.parametrize("sinks", [0, 1, 16, 20])
+def test_reads_across_the_sinks_end(lib, cache, sinks):
+    """A range that begins in the sinks' pages and ends behind them can be read as long as
+    nothing between them is evicted."""
+    from paged_kv_cache_build_gb300 import PkvError
+    s = HostStream()
+    sid = cache.open_token_stream(200, window=50, sinks=sinks)
+    cache.append_tokens(cache.token_batch([sid], [100]), rows(100, 2), rows(100, 2), stream=s)
+    read = lambda pos0, n: cache.read_tokens(cache.token_batch([sid], [n]), [pos0], k_out=rows(n, 2), v_out=rows(n, 2),
+                                             stream=s)
+    for pos0, n in ((0, 100), (15, 2), (16, 1), (31, 2), (0, 33)):
+        read(pos0, n)
+    lib.pkv_evict_window(cache.h, sid, None)
+    _, a, b = cache.token_info(sid)
+    assert (a, b) == (-(-sinks // 16) * 16, 48)  # the next token sees from position 51 on
+    read(b, 100 - b)
+    if a:
+        read(0, a)
+    for pos0, n in ((a, 1), (b - 1, 1), (b - 1, 2), (a, b - a), (0, 100)):
+        with pytest.raises(PkvError) as e:
+            read(pos0, n)
+        assert e.value.code == "STATE"
