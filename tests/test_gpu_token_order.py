@@ -177,3 +177,65 @@ def test_outputs_of_a_call_on_a_side_stream():
         assert torch.equal(x, y)
     p.cache.sync()
     p.cache.close()
+
+
+@pytest.mark.parametrize("copies", [1, 40], ids=["few rows", "many rows"])
+def test_ties_go_to_the_even_code(copies):
+    """Every value half way between two codes, in rows of many exponents: the read-back is
+    the even code's value (and the oracle's)."""
+    code = np.arange(127)
+    value = np.where(code < 8, code / 8 * 2.0 ** -6, (1 + code % 8 / 8) * 2.0 ** (code // 8 - 7.0))
+    middle = (value[1:] + value[:-1]) / 2
+    even = value[(np.arange(126) + 1) // 2 * 2]
+    rows, want = [], []
+    for e in list(range(-12, 13)) + [-110, -64, 63, 110]:
+        for part in (slice(0, 63), slice(63, 126)):
+            for sign in (1.0, -1.0):
+                rows.append(np.concatenate([[448.0], sign * middle[part]]) * 2.0 ** e)
+                want.append(np.concatenate([[448.0], sign * even[part]]) * 2.0 ** e)
+    n = len(rows)
+    x = torch.tensor(np.stack(rows)[:, None].repeat(2, 1), dtype=torch.float32).bfloat16().cuda()
+    np.testing.assert_array_equal(f64(x)[:, 0], np.stack(rows))      # bf16 holds the middles
+    x = x.repeat(copies, 1, 1)
+    p = Pool(-(-copies * n // 64), 64, 2, True)
+    sid = p.open()
+    batch = p.cache.token_batch([sid], [copies * n])
+    p.cache.append_tokens(batch, x, x)
+    for got in p.cache.read_tokens(batch):
+        np.testing.assert_array_equal(f64(got), np.stack(want * copies)[:, None].repeat(2, 1))
+        np.testing.assert_array_equal(f64(got), stored(x, True))
+    p.cache.sync()
+    p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_no_call_on_a_token_stream_allocates(fp8):
+    """Every call between a stream's opening and its end, few rows and many, on both layers:
+    the device's free memory stays, and so does the frame calls' scratch."""
+    for attempt in ("the kernels are loaded", "what is looked at"):
+        p = Pool(700, 16, 2, fp8, layers=2)
+        a, b = p.cache.open_token_stream(9000, 500, 20), p.cache.open_token_stream(9000)
+        B = p.cache.token_batch
+        x = {n: (p.rows(n, 2), p.rows(n, 2), p.rows(n, 8)) for n in (6000, 300, 9, 2)}
+        outs = {n: tuple(torch.empty_like(t) for t in v) for n, v in x.items()}
+        batches = {6000: B([a, b], [5000, 1000]), 300: B([b], [300]), 9: B([a, b], [5, 4]), 2: B([a, b], [1, 1])}
+        scratch = p.cache.scratch_info()
+        torch.cuda.synchronize()
+        free = torch.cuda.mem_get_info()[0]
+        for n, batch in batches.items():
+            k, v, q = x[n]
+            for layer in range(2):
+                p.cache.append_tokens(batch, k, v, layer=layer)
+                p.cache.attend_tokens(batch, q, layer=layer, window=400, sinks=20, out=outs[n][2])
+                p.cache.read_tokens(batch, layer=layer, k_out=outs[n][0], v_out=outs[n][1])
+            if n == 9:
+                p.cache.drop_tokens(batch)
+            if n == 2:
+                p.cache.rollback_last_frame(b)
+            p.cache.evict_window(a)
+        p.cache.reset_stream(b)
+        torch.cuda.synchronize()
+        assert p.cache.scratch_info() == scratch
+        after = torch.cuda.mem_get_info()[0]
+        p.cache.close()
+    assert after == free
