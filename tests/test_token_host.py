@@ -229,3 +229,88 @@ def test_reads_across_the_sinks_end(lib, cache, sinks):
         with pytest.raises(PkvError) as e:
             read(pos0, n)
         assert e.value.code == "STATE"
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_calls_are_accepted_as_the_page_state_allows(lib, cache, seed):
+    """Random calls on streams with and without windows: each is accepted or refused, with
+    its code, as the oracle's pages say, and the counters follow."""
+    import random
+    from oracle.tokens import TokenError, TokenStreamsOracle, visible
+    from paged_kv_cache_build_gb300 import PkvError
+    rng = random.Random(seed)
+    S, s = 16, HostStream()
+    ora = TokenStreamsOracle(20, S)
+    kinds = [(0, 0), (1, 0), (rng.randrange(1, 60), rng.choice([0, 1, 16, 17, 40])), (33, 5)]
+    sids = []
+    for window, sinks in kinds:
+        sids.append(cache.open_token_stream(200, window, sinks))
+        ora.open(sids[-1], 200, window, sinks)
+
+    def outcome(f):
+        try:
+            f()
+        except (PkvError, TokenError) as e:
+            return e.code
+        return "OK"
+
+    def live(sid, positions):
+        if not all(p // S in ora.streams[sid]["pages"] for p in positions):
+            raise TokenError("STATE")
+
+    def sees(sid, n, window, sinks):
+        length = ora.streams[sid]["len"]
+        if n > length:
+            raise TokenError("STATE")
+        for p in range(length - n, length):
+            live(sid, [j for j, v in enumerate(visible(p, length, window, sinks)) if v])
+
+    for _ in range(300):
+        op = rng.choice(["append", "append", "drop", "rollback", "evict", "read", "attend", "attend", "reset"])
+        some = rng.sample(sids, rng.randrange(1, 4))
+        counts = [rng.choice([0, 1, 2, 15, 16, 17, rng.randrange(1, 70)]) for _ in some]
+        sid, n = some[0], counts[0]
+        length = ora.streams[sid]["len"]
+        batch = cache.token_batch(some, counts)
+        if op == "append":
+            x = rows(batch.rows, 2)
+            got = outcome(lambda: cache.append_tokens(batch, x, x, stream=s))
+            want = outcome(lambda: ora.append(some, counts))
+        elif op == "drop":
+            got = outcome(lambda: cache.drop_tokens(batch, stream=s))
+            want = outcome(lambda: ora.drop(some, counts))
+        elif op == "rollback":
+            got = outcome(lambda: lib.pkv_rollback_last_frame(cache.h, sid, None) and cache._check(3))
+            want = outcome(lambda: ora.rollback(sid))
+        elif op == "evict":
+            got, want = outcome(lambda: cache._check(lib.pkv_evict_window(cache.h, sid, None))), outcome(lambda: ora.evict(sid))
+        elif op == "reset":
+            if rng.random() < 0.7:
+                continue
+            got, want = outcome(lambda: cache._check(lib.pkv_stream_reset(cache.h, sid, None))), "OK"
+            ora.release(sid)
+        elif op == "read":
+            n = min(n, length)
+            pos0 = rng.randrange(0, length - n + 1)
+            out = rows(n, 2)
+            got = outcome(lambda: cache.read_tokens(cache.token_batch([sid], [n]), [pos0], k_out=out, v_out=out, stream=s))
+            want = outcome(lambda: live(sid, range(pos0, pos0 + n)))
+        else:
+            window = rng.choice([0, 1, 2, 33, rng.randrange(1, 80)])
+            sinks = rng.choice([0, 1, 16, 17, 45, 300]) if window else 0
+            q = rows(n, 4)
+            got = outcome(lambda: cache.attend_tokens(cache.token_batch([sid], [n]), q, window=window, sinks=sinks,
+                                                      out=q, stream=s))
+            want = outcome(lambda: sees(sid, n, window, sinks))
+        if op == "drop" and got != "OK":         # which of a batch's faults is named is open
+            assert want != "OK"
+        else:
+            assert got == want, (op, some, counts, ora.streams)
+        for i in sids:
+            st = ora.streams[i]
+            free = ctypes.c_int()
+            lib.pkv_free_pages(cache.h, ctypes.byref(free))
+            assert (cache.token_info(i)[0], free.value) == (st["len"], len(ora.free))
+            pages, tokens = ctypes.c_int(), ctypes.c_int()
+            lib.pkv_visible_count(cache.h, i, ctypes.byref(pages), ctypes.byref(tokens))
+            assert (pages.value, tokens.value) == (len(st["pages"]), sum(ora.table(i)[1]))
