@@ -128,8 +128,6 @@ pkv_status get_stream(pkv_t h, int sid, Stream** out);
 pkv_status check_device(pkv_t h);
 pkv_status push_pages(pkv_t h, const PushSegment* segs, int n_seg, cudaStream_t s);
 PushSegment seg(const int32_t* src, int start, int count, int step = 1, int ring = 0);
-// Grows the handle's split-KV scratch (synchronises the device when it has to).
-pkv_status ensure_scratch(pkv_t h, size_t bytes);
 
 // Token streams (pkv_tokens.cu).
 pkv_status token_rollback(pkv_t h, Stream* st, cudaStream_t s);

@@ -333,8 +333,9 @@ pkv_status pkv_destroy(pkv_t h) {
 
 }  // extern "C"
 
-namespace pkv {
+namespace {
 
+// Grows the handle's split-KV scratch (synchronises the device when it has to).
 pkv_status ensure_scratch(pkv_t h, size_t bytes) {
   if (bytes <= h->scratch_bytes) return PKV_OK;
   PKV_CUDA(h, cudaDeviceSynchronize());
@@ -346,10 +347,6 @@ pkv_status ensure_scratch(pkv_t h, size_t bytes) {
   h->scratch_allocs++;
   return PKV_OK;
 }
-
-}  // namespace pkv
-
-namespace {
 
 // Split-KV scratch that the attention calls of a stream with this configuration
 // need at their natural query count (a frame's n_patch + n_special rows, or a
