@@ -239,3 +239,107 @@ def test_no_call_on_a_token_stream_allocates(fp8):
         after = torch.cuda.mem_get_info()[0]
         p.cache.close()
     assert after == free
+
+
+def poison(cache):
+    """Every free page's rows, on every layer, become NaN and infinities; the free stack stays."""
+    n = cache.free_pages() * cache.page_size
+    sid = cache.open_token_stream(n)
+    batch = cache.token_batch([sid], [n])
+    bad = torch.full((n, cache.heads, 64), float("nan"), device="cuda", dtype=torch.bfloat16)
+    bad[::3] = float("inf")
+    for layer in range(cache.layers):
+        cache.append_tokens(batch, bad, bad, layer=layer)
+    cache.drop_tokens(batch)                     # (closing alone would turn the free stack over)
+    cache.close_stream(sid)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64, 192])
+def test_a_served_run_on_used_pages(page, fp8):
+    """Steps of three streams on two layers where every free page holds values that are not
+    finite, again before each step: appends over page ends, drops, rollbacks, evictions."""
+    p = Pool(4000 // page, page, 2, fp8, layers=2, seed=page)
+    poison(p.cache)
+    W, K = 70, 21
+    a, b, c = p.open(), p.open(window=W, sinks=K), p.open(window=W)
+    sids = [a, b, c]
+    for step, n in enumerate([(1, 130, 300), (64, 1, 1), (5, 7, 3), (1, 1, 1), (200, 90, 1), (1, 1, 1), (2, 3, 260), (1, 1, 1)]):
+        poison(p.cache)
+        batch = p.append(sids, n)
+        for layer in range(2):
+            p.check_attend(sids, n, 2, W, 0, layer=layer, batch=batch)
+            p.check_attend([a, b], n[:2], 4, W, K, layer=layer)
+            p.check_attend([a], n[:1], 1, layer=layer)
+        if step % 3 == 2:
+            p.drop(sids, [min(2, x) for x in n])
+            p.check_attend([a], [1], 2, layer=1)
+        if step % 3 == 1:
+            p.cache.rollback_last_frame(a)
+            p.ora.rollback(a)
+            for layer in p.kv[a]:
+                layer[:] = [x[:len(x) - n[0]] for x in layer]
+        for s in (b, c):
+            p.cache.evict_window(s)
+            p.ora.evict(s)
+        p.check_state(sids)
+    p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_frames_on_pages_that_a_token_stream_used(fp8):
+    """A frame stream and a chunked one give the same bits on pages that a token stream left
+    values in that are not finite."""
+    from paged_kv_cache_build_gb300 import PagedKVCache, chunked_stream_cfg, frame_stream_cfg
+    g = torch.Generator(device="cuda").manual_seed(8)
+    frames = [[torch.randn((22, 4, 64), generator=g, device="cuda").bfloat16() for _ in range(3)] for _ in range(9)]
+    results = []
+    for used in (False, True):
+        cache = PagedKVCache(64, 16, 4, layers=2, fp8=fp8)
+        if used:
+            poison(cache)
+        f, c = cache.open_stream(frame_stream_cfg(2, 4, 16, 6)), cache.open_stream(chunked_stream_cfg(3, 2, 22))
+        outs = []
+        for i, (q, k, v) in enumerate(frames):
+            for layer in range(2):
+                cache.append_frame(f, k, v, layer=layer)
+                outs.append(cache.attend(q, f, layer=layer))
+                cache.append_frame(c, k, v, layer=layer)
+                whole = torch.cat([x[0] for x in frames[i // 3 * 3:i + 1]])
+                outs.append(cache.attend_chunked(whole, c, layer=layer))
+            if i % 3 == 1:
+                cache.rollback_last_frame(f)
+            else:
+                cache.evict_window(f)
+            if i % 3 == 2:
+                cache.evict_window(c)
+            if used:
+                poison(cache)
+        results.append(torch.cat(outs))
+        cache.sync()
+        cache.close()
+    assert torch.isfinite(results[1]).all()
+    assert torch.equal(results[0], results[1])
+
+
+@pytest.mark.parametrize("new", [1, 5, 200])
+def test_two_handles_on_two_streams(new):
+    """Calls of two handles that run at the same time: each one's split results are its own."""
+    pools = [Pool(400, 16, 2, bool(i), seed=i) for i in range(2)]
+    work = []
+    for p in pools:
+        sids = [p.open(), p.open()]
+        p.append(sids, [2500 + new, 900 + new])
+        batch = p.cache.token_batch(sids, [new, new])
+        q = p.rows(2 * new, 4)
+        work.append((p, batch, q, p.cache.attend_tokens(batch, q), [torch.empty_like(q) for _ in range(30)]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in pools]
+    for i in range(30):
+        for s, (p, batch, q, _, outs) in zip(streams, work):
+            p.cache.attend_tokens(batch, q, out=outs[i], stream=s)
+    torch.cuda.synchronize()
+    for p, _, _, want, outs in work:
+        assert all(torch.equal(x, want) for x in outs)
+        p.cache.sync()
+        p.cache.close()
