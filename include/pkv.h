@@ -443,9 +443,11 @@ pkv_status pkv_attend_noalloc(pkv_t h, const void* q, int n_q, int stream_id, in
  * are served by one call: a batch names n streams (1 .. 256, each once), and the
  * rows of all of them lie back to back in one tensor, rows row_off[i] ..
  * row_off[i + 1] - 1 being stream stream_ids[i]'s (n + 1 host ints that start at 0
- * and do not fall; a stream may have no row). Values must be finite: what is not makes
- * the outputs of its stream's rows meaningless (mostly NaN; on E4M3 pages they may be
- * numbers), no other stream's.
+ * and do not fall; a stream may have no row; 2^24 rows at most). Values must be finite:
+ * what is not makes the outputs of its stream's rows meaningless (mostly NaN; on E4M3 pages
+ * they may be numbers), no other stream's. Sums are held in fp32, so v must stay below 2^90
+ * in magnitude; and a weight is off by about 2^-23 |score|, relatively, so that scores
+ * sm_scale * q . k of 2^20 and more have little meaning.
  * Rows may be strided: k_stride, v_stride and q_stride are the elements from one
  * token's row to the next one's (0: contiguous), multiples of 8, so that q, k and v
  * may be parts of one tensor. The other calls that take a stream (close, reset,
@@ -471,7 +473,8 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
 /* Append each stream's rows of k and v (device bf16 [row_off[n]][heads][64], rows
  * strided) behind its tokens. layer 0 pops the pages that they need, in the order
  * of the batch, and counts the tokens; layer > 0 writes the same slots of that
- * layer's page set and must bring the rows of the stream's last append on layer 0.
+ * layer's page set and must bring the rows of the stream's last append on layer 0, before
+ * the next one there (rows that a layer was not given hold what the page held before).
  * On an E4M3 cache rows are quantised as pkv_create_fp8 says. Slots behind the
  * last token of a page that the call opens are zeroed; a dropped token's row stays
  * until its slot is written again.
@@ -509,8 +512,9 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* stream_ids, const int* pos
  * so a window holds the query's own token and the window - 1 before it, and the
  * stream's first `sinks` tokens stay visible beside it.
  * q: device bf16 [row_off[n]][q_heads][64], rows q_stride apart; out: the same,
- * contiguous. fp32 accumulation and softmax; the probabilities are rounded to bf16
- * for the second product, or, in streams with few rows x query heads per KV head
+ * contiguous. A call takes fewer than 2^27 rows x q_heads. fp32 accumulation and softmax;
+ * the probabilities are rounded to bf16 for the second product, or, in streams with few
+ * rows x query heads per KV head
  * (up to 64) on E4M3 pages, to f16 (and q as well), which loses what is below 2^-39 of an
  * output row's largest contribution. sm_scale <= 0 means 1 / sqrt(64).
  * Results depend on the batch only by rounding (the kernel and the split of the keys

@@ -15,8 +15,8 @@
 // of a row block's splits joins their partial results. The products run on warp-level matrix
 // instructions with the 8, 16 or 24 query rows on the N side: S^T = K Q^T and
 // O^T += V^T P^T.
-// Measured: 32 streams of up to 8192 tokens, 32 query heads on 8, in 50.8 us on bf16 pages
-// (6.1 TB/s, 0.90 of the measured copy rate) and in 37.7 us on E4M3 pages (4.2 TB/s: there
+// Measured: 32 streams of up to 8192 tokens, 32 query heads on 8, in 51.2 us on bf16 pages
+// (6.0 TB/s, 0.89 of the measured copy rate) and in 38.2 us on E4M3 pages (4.1 TB/s: there
 // the conversions' and the softmax' instruction latencies on eight warps an SM bound it; more
 // warps with fewer registers, or two warps a tile, were no faster).
 //
@@ -39,9 +39,11 @@ namespace pkv {
 namespace {
 
 // Consumer warps (and one producer). Up to 16 rows: four, at 168 registers a thread. 24 rows:
-// three, so that two CTAs' warps have 255 (16 ragged streams of up to 4001 tokens, 20 rows:
-// 21.0 us; four warps that spill 21.9; two blocks of 16 rows 32.5. With 32 rows the block
-// takes longer than two of 16: 36 against 29 us, and 47 against 41 on E4M3 pages.)
+// three, so that two CTAs' warps have 255 (a fourth warp makes them spill: 4 % slower). A
+// block of 24 against two of 16, 16 streams of 4001 tokens with 17, 20, 21 or 24 rows, which
+// take the same: 29.8 against 36.9 us, of 500 .. 4001 tokens 22.6 against 31.6 us, on E4M3
+// pages 35.4 against 43.6 and 26.1 against 37.4 us. With 32 rows the block takes longer than
+// two of 16: 36 against 29 us, and 47 against 41 on E4M3 pages.
 template <int NT>
 constexpr int kWarps = NT <= 2 ? 4 : 3;
 template <int NT>

@@ -282,7 +282,12 @@ __global__ void __launch_bounds__(256) token_drop_kernel(const __grid_constant__
 
 // Tokens from which a block takes 32 of them: enough blocks to fill the SMs. (Read-back of
 // 64 / 512 / 2560 / 4032 tokens of 8 heads on bf16 pages: 2.0 / 2.2 / 3.8 / 4.8 us with a
-// warp per quad and plane, 4.7 / 3.6 / 3.6 / 3.7 us with blocks of 32.)
+// warp per quad and plane, 4.7 / 3.6 / 3.6 / 3.7 us with blocks of 32. The rule asks for
+// neither heads nor direction, and is off for some. From cold memory, each with a drop's
+// launch of some 5 us in the appends, 2432 / 9728 tokens, quads against blocks: 8 heads, bf16
+// append 10 / 17 against 18 / 20 us, read 10 / 14 against 11 / 13; E4M3 11 / 20 against
+// 13 / 18 and 9 / 18 against 9 / 13; 32 heads, bf16 17 / 38 against 42 / 52 and 16 / 36
+// against 18 / 34; E4M3 20 / 50 against 28 / 36 and 18 / 42 against 18 / 28 us.)
 constexpr int kManyUnits = 152 * 16;
 
 int row_blocks(const TokenRowsArgs& a) {

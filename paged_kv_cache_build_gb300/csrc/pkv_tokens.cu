@@ -390,9 +390,11 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
   }
   const int few_rows = rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
   const int max_rows = token_tc_max_rows(h->fp8);
-  // one shape for all streams of the matrix-unit kernel, the largest's (a second launch costs
-  // more than the lanes that stay idle: 2 .. 34 new tokens of 18 streams, 25.8
-  // against 39.1 us)
+  // one shape for all streams of the matrix-unit kernel, the largest's. On bf16 pages a second
+  // launch costs more than the lanes that stay idle: 2 .. 34 new tokens of 18 streams, 25.8
+  // against 39.1 us; a chunk of 1500 tokens beside 11 drafts of 20, group 4, 99 against 122 us.
+  // On E4M3 pages it depends: the first batch 36.6 against 56.6 us, the second 165 against 155
+  // us (there the 512-row shape leaves three of a draft's four lanes without rows).
   int tc_rows = 128;
   for (int i = 0; i < n_items; ++i)
     while (tc_rows < max_rows && (long long)all[i].n * group > tc_rows) tc_rows *= 2;
