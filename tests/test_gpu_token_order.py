@@ -21,8 +21,8 @@ def busy(seconds=0.05):
 def test_a_stream_opened_behind_a_busy_default_stream(fp8):
     """Opened while the default stream has work to do, and used on a side stream at once:
     the pages and the joined splits are right before and after that work ends."""
-    side, done = torch.cuda.Stream(), torch.cuda.Event()
-    for waits in (0.0, 0.1):                     # the first turn loads the kernels
+    side, done, behind = torch.cuda.Stream(), torch.cuda.Event(), []
+    for waits in (0.0, 0.4):                     # the first turn loads the kernels
         p = Pool(400, 16, 2, fp8)
         torch.cuda.synchronize()
         for _ in range(2):                       # a handle's first open lays out its workspace, too
@@ -36,7 +36,7 @@ def test_a_stream_opened_behind_a_busy_default_stream(fp8):
                 p.cache.append_tokens(batch, k, v)
                 out = p.cache.attend_tokens(p.cache.token_batch([sid], [1]), q)
                 early = out.cpu()
-            assert waits == 0 or not done.query(), "the default stream was to be busy meanwhile"
+            behind.append(not done.query())      # (not where the host was held up)
             kk, vv, qq = stored(k, fp8), stored(v, fp8), f64(q)
             ref = causal_attend_fp64(qq, kk, vv, 1999, 0, 0, SCALE)
             assert (np.abs(f64(early) - ref) <= tolerance(qq, kk, vv, ref, 1999, 0, 0, SCALE)).all()
@@ -46,6 +46,7 @@ def test_a_stream_opened_behind_a_busy_default_stream(fp8):
             torch.cuda.synchronize()
         p.cache.sync()
         p.cache.close()
+    assert any(behind[2:]), "the default stream was to be busy meanwhile"
 
 
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
