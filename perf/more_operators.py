@@ -8,6 +8,8 @@ every layer, keep some of them, read those back and drop them. Where `own` is fa
 are computed in elementary torch operations on plain tensors (pages, tables, codes), where it is true
 through the package's public calls."""
 
+import functools
+
 import torch
 
 own = False
@@ -316,14 +318,25 @@ def prepare(c, seed):
     return state
 
 
+@functools.lru_cache(None)
+def _powers(dtype, device):
+    return torch.tensor([2.0 ** i for i in range(-149, 128)], dtype=dtype, device=device)
+
+
+def _power(e, like):
+    """2^e, from a list: a power taken on the device may be an ulp off, which a value midway between
+    two codes would show."""
+    return _powers(like.dtype, like.device)[e.long() + 149]
+
+
 def _quantise(x):
     """E4M3 codes (as their values) and the exponent of each row of 64."""
     big = x.abs().amax(-1)
     m, ex = torch.frexp(big)
     e = torch.where(big > 0, (ex - 9 + (m > E4M3_MAX / 512).int()).clamp(-126, 126), torch.zeros_like(ex))
-    y = torch.ldexp(x, -e[..., None])
+    y = x * _power(-e[..., None], x)
     _, ey = torch.frexp(y)
-    step = torch.ldexp(torch.ones_like(y), (ey - 1).clamp(min=-6) - 3)
+    step = _power((ey - 1).clamp(min=-6) - 3, y)
     return (torch.round(y / step) * step).float(), e
 
 
@@ -340,7 +353,8 @@ def _load(store, slot):
     if len(store) == 1:
         return store[0][slot].float()
     codes = store[0].view(torch.uint8)[slot].view(torch.float8_e4m3fn)
-    return torch.ldexp(codes.float(), store[1][slot][..., None].int())
+    codes = codes.float()
+    return codes * _power(store[1][slot][..., None], codes)
 
 
 def _turn(x, cos, sin, distance):
@@ -436,18 +450,19 @@ def _nearest_e4m3(x):
     """Rows of 64 in doubles to what their 8-bit form stands for: the nearest of the format's values
     (ties to the even code), scaled by the smallest power of two that holds the row."""
     code = torch.arange(127, device=x.device)
-    value = torch.where(code < 8, (code % 8) / 8.0 * 2.0 ** -6, (1 + (code % 8) / 8.0) * 2.0 ** (code // 8 - 7.0)).double()
+    value = torch.where(code < 8, (code % 8).double() / 8 * 2.0 ** -6,
+                        (1 + (code % 8).double() / 8) * _power(code // 8 - 7, x))
     big = x.abs().amax(-1, keepdim=True)
-    e = torch.ceil(torch.log2(torch.where(big > 0, big, torch.ones_like(big)) / E4M3_MAX))
-    e = e + (big > E4M3_MAX * 2.0 ** e) - (big <= E4M3_MAX * 2.0 ** (e - 1)).double()
+    e = torch.ceil(torch.log2(torch.where(big > 0, big, torch.ones_like(big)) / E4M3_MAX)).long().clamp(-148, 126)
+    e = e + (big > E4M3_MAX * _power(e, x)).long() - (big <= E4M3_MAX * _power(e - 1, x)).long()
     e = torch.where(big > 0, e.clamp(-126, 126), torch.zeros_like(e))
-    y = (x / 2.0 ** e)
+    y = x / _power(e, x)
     middle = (value[1:] + value[:-1]) / 2
     a = y.abs().contiguous()
     low = torch.bucketize(a, middle)                 # middles below a
     up = torch.bucketize(a, middle, right=True)      # and those equal to it
     i = torch.where(low % 2 == 0, low, up)
-    return torch.sign(y) * value[i] * 2.0 ** e
+    return torch.sign(y) * value[i] * _power(e, x)
 
 
 def _stored(c, x):
