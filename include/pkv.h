@@ -485,6 +485,39 @@ pkv_status pkv_append_tokens(pkv_t h, int n, const int* stream_ids, const int* r
                              const void* k, const void* v, long long k_stride, long long v_stride,
                              void* cuda_stream);
 
+/* A rotation of rows of 64 values by positions: 32 pairs of elements pair_distance apart
+ * (pair i: elements a = i / d * 2 d + i % d and a + d, d = pair_distance), each turned by the
+ * angle freq[i] x (the position on axis[i]):
+ *   y[a] = x[a] cos - x[a + d] sin,   y[a + d] = x[a] sin + x[a + d] cos.
+ * d = 32 pairs a row's halves, d = 1 neighbours, d = 16 the halves of each half. Text has one
+ * axis, or several with equal positions; images and video have time, row and column. */
+typedef struct {
+  int axes;          /* numbers of a token's position: 1 .. 4                     */
+  int pair_distance; /* 1, 2, 4, 8, 16 or 32                                     */
+  double freq[32];   /* radians per unit of position, at most 2^20 in magnitude    */
+  int axis[32];      /* 0 .. axes - 1                                            */
+} pkv_rotary;
+
+/* pkv_append_tokens with rotary positions: k's rows are turned as `rotary` says before they
+ * are stored (v's are not), and so are q's, into q_out. positions: device int32
+ * [row_off[n]][axes], any values; which position a token has is the caller's, for the cache
+ * orders tokens by slots alone (drafted tokens of a tree share positions, pkv_attend_tree).
+ * q: device bf16 [row_off[n]][q_heads][64], rows q_stride apart (0: contiguous); q_out: the
+ * same, contiguous; it may be q itself where that is contiguous, and overlaps nothing else.
+ * q_heads = 0: no q (q and q_out are not used). freq / 2 pi is kept to 2^-65 of a turn, and whole
+ * turns are taken off exactly; sines, cosines and sums are fp32, and what is stored is rounded
+ * once: to bf16, or, on an E4M3 cache, to the codes and exponent of the row as turned (those of
+ * the exact values, but where these lie within |position| 2^-62 + 2^-48 of a border of two codes,
+ * relatively). Slots, pages, layers and the rest are as in pkv_append_tokens; k must stay below
+ * 2^125 in magnitude.
+ * Errors: as pkv_append_tokens; INVALID for a null rotary or one outside its limits, q_heads
+ * outside 0 .. 128 x heads, a q_stride that is no multiple of 8 or below a row, positions, q or
+ * q_out null or unaligned (4 bytes, 16 bytes), q_out = q with a stride. */
+pkv_status pkv_append_tokens_rotary(pkv_t h, int n, const int* stream_ids, const int* row_off, int layer,
+                                    const void* k, const void* v, long long k_stride, long long v_stride,
+                                    const void* q, int q_heads, long long q_stride, void* q_out,
+                                    const void* positions, const pkv_rotary* rotary, void* cuda_stream);
+
 /* Drop each stream's last counts[i] tokens (host ints; drafted tokens that were
  * not accepted). Pages left empty go back on the free stack, the last stream's
  * first, so that dropping a whole append restores the stack.
@@ -493,6 +526,21 @@ pkv_status pkv_append_tokens(pkv_t h, int n, const int* stream_ids, const int* r
  * (not a token stream; what the stream's window would see from before the dropped
  * tokens is evicted). */
 pkv_status pkv_drop_tokens(pkv_t h, int n, const int* stream_ids, const int* counts, void* cuda_stream);
+
+/* Keep some of each stream's last tokens and drop the others (the accepted nodes of a tree of
+ * drafted tokens). Of stream i's last row_off[i + 1] - row_off[i] tokens, numbered from 0,
+ * those numbered kept[keep_off[i]] .. kept[keep_off[i + 1] - 1] stay: in every layer their K and
+ * V rows move, as they are stored, to the first of these tokens' slots, and the stream is that
+ * much shorter. keep_off: n + 1 host ints that start at 0; kept: device int32, rising strictly
+ * within a stream (NULL where nothing stays). Pages left empty go back on the free stack, the last stream's first. The next append on layer > 0
+ * needs one on layer 0 first, as after a drop.
+ * A kept number out of its range or order is noted (pkv_sync: DEVICE) and leaves the
+ * rows of its stream undefined; no other memory is touched.
+ * Errors: INVALID (offsets, more to keep than tokens, more tokens than the stream has, a
+ * stream twice, kept null or not 4-byte aligned), STATE (not a token stream; tokens that
+ * would stay, or what the stream's window sees from behind them, are evicted). */
+pkv_status pkv_keep_tokens(pkv_t h, int n, const int* stream_ids, const int* row_off, const int* keep_off,
+                           const void* kept, void* cuda_stream);
 
 /* Read rows back: stream i's positions pos0[i] .. (row_off[i + 1] - row_off[i] of
  * them; pos0 NULL: its last ones) into k_out and v_out, device bf16
@@ -527,6 +575,22 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* stream_ids, const int* pos
 pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
                              const int* stream_ids, int n, int layer, void* out, int window, int sinks,
                              float sm_scale, void* cuda_stream);
+
+/* Attention of trees of drafted tokens. Stream i's rows, its last tokens (up to 256), are the
+ * nodes of a tree: parents[r] (device int32 [row_off[n]]) is the number, from 0 within the
+ * stream's rows, of row r's parent, which comes before it, or -1: a child of the token before the
+ * tree (several may be). With P the stream's tokens before the tree, a node's position is
+ * P + depth (depth 0 where the parent is -1), and it sees the P tokens before the tree, its ancestors and itself,
+ * with a window only those whose position is above its own - window or below sinks:
+ *   out[r][g] = softmax over those j of (sm_scale * q[r][g] . k[j]) v[j].
+ * A tree without branches gives pkv_attend_tokens' results but for rounding. Everything else is
+ * as in pkv_attend_tokens. A parent that does not come before its node is taken for -1, and noted
+ * (pkv_sync: DEVICE).
+ * Errors: as pkv_attend_tokens; INVALID for more than 256 rows of a stream, and for parents
+ * null or not 4-byte aligned. */
+pkv_status pkv_attend_tree(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
+                           const int* stream_ids, int n, int layer, const void* parents, void* out,
+                           int window, int sinks, float sm_scale, void* cuda_stream);
 
 /* A token stream's tokens, and its evicted positions evicted_from ..
  * evicted_to - 1 (0, 0: none); each pointer may be NULL.

@@ -6,10 +6,13 @@ position: a stack of free pages (popped from its end), each stream's dict of pag
 index -> page id. With a retention window, evict() frees every page none of whose
 positions a later query can see (a query at p sees j > p - window, and j < sinks);
 a page is freed as a whole. causal_attend_fp64 is softmax attention with the
-visible set spelled out per query.
+visible set spelled out per query; tree_attend_fp64 the same for trees of drafted tokens, whose
+nodes' paths are walked; rotate_fp64 the rotation of rows by positions.
 """
 
 import numpy as np
+
+TWO_PI = "6.2831853071795864769252867665590057683943387987502"
 
 
 class TokenError(Exception):
@@ -71,6 +74,20 @@ class TokenStreamsOracle:
             st["len"] = end
             st["last"] = None
 
+    def keep(self, sids, counts, kept):
+        """Of each stream's last counts[i] tokens kept[i] (a number) stay."""
+        S = self.page_size
+        for sid, n, m in zip(sids, counts, kept):
+            st = self.streams[sid]
+            if not 0 <= m <= n or n > st["len"]:
+                raise TokenError("INVALID")
+            if any(p // S not in st["pages"] for p in range(st["len"] - n, st["len"])):
+                raise TokenError("STATE")
+        self.drop(sids, [n - m for n, m in zip(counts, kept)])
+        for sid, n in zip(sids, counts):
+            if n:
+                self.streams[sid]["last"] = None
+
     def rollback(self, sid):
         st = self.streams[sid]
         if st["last"] is None:
@@ -117,4 +134,57 @@ def causal_attend_fp64(q, k, v, pos0, window, sinks, sm_scale):
         s = np.where(seen, s, -np.inf)
         p = np.exp(s - s.max(axis=1, keepdims=True))
         out[:, g] = (p @ v[:, g // group]) / p.sum(axis=1, keepdims=True)
+    return out
+
+
+def tree_paths(parents):
+    """Each node's path, itself first, walked from node to node."""
+    paths = []
+    for i, p in enumerate(parents):
+        assert -1 <= p < i
+        paths.append([i] + (paths[p] if p >= 0 else []))
+    return paths
+
+
+def tree_visible(parents, before, window, sinks):
+    """[nodes][before + nodes]: what each node of a tree behind `before` tokens sees."""
+    paths = tree_paths(parents)
+    place = np.concatenate([np.arange(before), [before + len(p) - 1 for p in paths]]).astype(np.int64)
+    seen = np.zeros((len(parents), before + len(parents)), dtype=bool)
+    for i, path in enumerate(paths):
+        seen[i, :before] = True
+        seen[i, [before + a for a in path]] = True
+        if window:
+            seen[i] &= (place > before + len(path) - 1 - window) | (place < sinks)
+    return seen
+
+
+def tree_attend_fp64(q, k, v, parents, window, sinks, sm_scale):
+    """q [nodes][q_heads][64], k and v [before + nodes][heads][64], float64."""
+    seen = tree_visible(parents, len(k) - len(q), window, sinks)
+    group = q.shape[1] // k.shape[1]
+    out = np.empty_like(q)
+    for g in range(q.shape[1]):
+        s = np.where(seen, sm_scale * (q[:, g] @ k[:, g // group].T), -np.inf)
+        p = np.exp(s - s.max(axis=1, keepdims=True))
+        out[:, g] = (p @ v[:, g // group]) / p.sum(axis=1, keepdims=True)
+    return out
+
+
+def rotate_fp64(x, positions, freq, axis, pair_distance):
+    """Rows [rows][heads][64], positions [rows][axes]: each pair times e^(i freq position). The
+    angle's whole turns are taken off in exact arithmetic (a double as a fraction)."""
+    from fractions import Fraction
+    out = np.empty_like(x, dtype=np.float64)
+    tau = Fraction(TWO_PI)
+    d = pair_distance
+    for i in range(32):
+        a = i // d * 2 * d + i % d
+        angle = []
+        for p in positions[:, axis[i]]:
+            t = Fraction(float(freq[i])) * int(p)
+            angle.append(float(t - round(t / tau) * tau))
+        turn = np.exp(1j * np.array(angle))[:, None]
+        z = (x[..., a] + 1j * x[..., a + d]) * turn
+        out[..., a], out[..., a + d] = z.real, z.imag
     return out

@@ -12,7 +12,7 @@ from ._lib import LIB_PATH, PkvError, load  # noqa: F401
 def __getattr__(name):
     # the torch-facing binding is imported lazily so that loading the library
     # (symbol checks) works without a GPU
-    if name in ("PagedKVCache", "TokenBatch", "frame_stream_cfg", "chunked_stream_cfg", "synth_fill",
+    if name in ("PagedKVCache", "TokenBatch", "Rotary", "frame_stream_cfg", "chunked_stream_cfg", "synth_fill",
                 "kernel_launches", "MODE_FRAME", "MODE_CHUNKED"):
         from . import cache
         return getattr(cache, name)

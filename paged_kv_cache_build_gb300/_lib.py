@@ -19,6 +19,10 @@ class StreamCfg(ctypes.Structure):
                 ("chunk_size", c_int), ("sliding_window_num", c_int), ("tokens_per_frame", c_int)]
 
 
+class RotaryCfg(ctypes.Structure):
+    _fields_ = [("axes", c_int), ("pair_distance", c_int), ("freq", ctypes.c_double * 32), ("axis", c_int * 32)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "pkv_create": (c_int, [c_int, c_int, c_int, c_int, ctypes.POINTER(c_void_p)]),
@@ -65,11 +69,17 @@ SIGNATURES = {
     "pkv_stream_open_tokens": (c_int, [c_void_p, c_int, c_int, c_int, ctypes.POINTER(c_int)]),
     "pkv_append_tokens": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
                                   ctypes.c_longlong, ctypes.c_longlong, c_void_p]),
+    "pkv_append_tokens_rotary": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                         ctypes.c_longlong, ctypes.c_longlong, c_void_p, c_int,
+                                         ctypes.c_longlong, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "pkv_keep_tokens": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "pkv_drop_tokens": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
     "pkv_read_tokens": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p,
                                 c_void_p, c_void_p]),
     "pkv_attend_tokens": (c_int, [c_void_p, c_void_p, c_int, ctypes.c_longlong, c_void_p, c_void_p,
                                   c_int, c_int, c_void_p, c_int, c_int, c_float, c_void_p]),
+    "pkv_attend_tree": (c_int, [c_void_p, c_void_p, c_int, ctypes.c_longlong, c_void_p, c_void_p,
+                                c_int, c_int, c_void_p, c_void_p, c_int, c_int, c_float, c_void_p]),
     "pkv_token_info": (c_int, [c_void_p, c_int, ctypes.POINTER(c_int), ctypes.POINTER(c_int),
                                ctypes.POINTER(c_int)]),
     "pkv_sync": (c_int, [c_void_p, c_void_p]),

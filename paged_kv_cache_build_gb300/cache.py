@@ -9,7 +9,7 @@ import ctypes
 
 import torch
 
-from ._lib import PkvError, StreamCfg, check, load
+from ._lib import PkvError, RotaryCfg, StreamCfg, check, load
 
 MODE_FRAME = 0
 MODE_CHUNKED = 1
@@ -66,11 +66,41 @@ class TokenBatch:
             off.append(off[-1] + c)
         if off[-1] >= 2 ** 31:
             raise ValueError("too many rows")
-        self.n, self.rows = n, off[-1]
+        self.n, self.rows, self.ids = n, off[-1], sids
         # host arrays that the calls read (kept alive with the batch), and their addresses
         self._ids, self._counts, self._off = (ctypes.c_int * n)(*sids), (ctypes.c_int * n)(*counts), \
             (ctypes.c_int * (n + 1))(*off)
         self.sids, self.counts, self.row_off = map(ctypes.addressof, (self._ids, self._counts, self._off))
+
+
+class Rotary:
+    """How positions turn q and k (pkv_rotary): pair i of a row's 32, its elements pair_distance
+    apart, by freq[i] radians per unit of the position on axis[i]. Positions have `axes` numbers
+    (default: as many as the pairs use)."""
+
+    def __init__(self, freq, axis=(0,) * 32, pair_distance=32, axes=None):
+        freq, axis = [float(f) for f in freq], [int(a) for a in axis]
+        if len(freq) != 32 or len(axis) != 32:
+            raise ValueError("one frequency and one axis for each of the 32 pairs")
+        axes = max(axis) + 1 if axes is None else axes
+        if _cut_short(pair_distance, axes, *axis):
+            raise ValueError("pair_distance, axes and each axis must be 32-bit numbers")
+        self.axes, self.pair_distance = axes, pair_distance
+        self._cfg = RotaryCfg(axes, pair_distance, (ctypes.c_double * 32)(*freq), (ctypes.c_int * 32)(*axis))
+        self.cfg = ctypes.addressof(self._cfg)
+
+    @classmethod
+    def sections(cls, pairs, base=10000.0, pair_distance=32, restart=False):
+        """Axis j turns the next pairs[j] pairs (32 in all): frequencies base ** (-i / 32) of pair i, or,
+        with `restart`, base ** (-i / pairs[j]) of each axis' own pair i."""
+        if sum(pairs) != 32 or min(pairs) < 1:
+            raise ValueError("the sections share 32 pairs")
+        freq, axis = [], []
+        for j, n in enumerate(pairs):
+            for i in range(n):
+                freq.append(base ** (-i / n) if restart else base ** (-len(freq) / 32))
+                axis.append(j)
+        return cls(freq, axis, pair_distance)
 
 
 class PagedKVCache:
@@ -372,6 +402,52 @@ class PagedKVCache:
         self._check(self.lib.pkv_append_tokens(self.h, batch.n, batch.sids, batch.row_off, layer, kp, vp,
                                                ks, vs, self._stream(stream)))
 
+    def _ints(self, t, name, shape):
+        """The address of a contiguous int32 tensor on the cache's device."""
+        if t.dtype != torch.int32 or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def _bf16_out(self, t, name, shape, stream):
+        if t is None:
+            return self._new(shape, stream)
+        if tuple(t.shape) != tuple(shape) or t.dtype != torch.bfloat16 or t.device != self.device or \
+                not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 tensor {list(shape)} on {self.device}")
+        return t
+
+    def append_tokens_rotary(self, batch, k, v, positions, rotary, q=None, layer=0, q_out=None, stream=None):
+        """pkv_append_tokens_rotary: append_tokens with k turned by `rotary` (a Rotary) at positions, int32
+        [batch rows][axes] (one axis: [batch rows], too); returns q, [batch rows][q_heads][64],
+        turned likewise (None without q)."""
+        if _cut_short(layer):
+            raise ValueError("layer must be a 32-bit number")
+        kp, ks = self._rows(k, "k", batch, self.heads)
+        vp, vs = self._rows(v, "v", batch, self.heads)
+        flat = rotary.axes == 1 and positions.dim() == 1
+        at = self._ints(positions, "positions", (batch.rows,) if flat else (batch.rows, rotary.axes))
+        qp = qs = out = q_heads = 0
+        if q is not None:
+            qp, qs = self._rows(q, "q", batch)
+            q_heads = q.shape[1]
+            q_out = self._bf16_out(q_out, "q_out", q.shape, stream)
+            out = q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        self._check(self.lib.pkv_append_tokens_rotary(self.h, batch.n, batch.sids, batch.row_off, layer, kp, vp,
+                                                      ks, vs, qp, q_heads, qs, out, at, rotary.cfg,
+                                                      self._stream(stream)))
+        return q_out
+
+    def keep_tokens(self, batch, kept, accepted, stream=None):
+        """pkv_keep_tokens: of the batch's rows, the last ones of its streams, those numbered in `kept` stay
+        (int32, each stream's numbers from 0, rising, one behind the other), the others go. `accepted`: a
+        token_batch of the same streams with how many of each stay; behind the call it names those."""
+        if accepted.n != batch.n or accepted.ids != batch.ids:
+            raise ValueError("accepted must be of the batch's streams")
+        self._check(self.lib.pkv_keep_tokens(self.h, batch.n, batch.sids, batch.row_off, accepted.row_off,
+                                             self._ints(kept, "kept", (accepted.rows,)), self._stream(stream)))
+
     def drop_tokens(self, batch, stream=None):
         """pkv_drop_tokens: the batch's rows, the last ones of its streams, go."""
         self._check(self.lib.pkv_drop_tokens(self.h, batch.n, batch.sids, batch.counts, self._stream(stream)))
@@ -418,6 +494,21 @@ class PagedKVCache:
         self._check(self.lib.pkv_attend_tokens(self.h, qp, q.shape[1], qs, batch.row_off, batch.sids, batch.n,
                                                layer, out.data_ptr(), window, sinks, sm_scale,
                                                self._stream(stream)))
+        return out
+
+    def attend_tree(self, batch, q, parents, layer=0, window=0, sinks=0, out=None, sm_scale=0.0, stream=None):
+        """pkv_attend_tree: attention of the batch's rows (the last tokens of its streams, up to 256 each) as
+        trees of drafted tokens: parents, int32 [batch rows], numbers each row's parent within its
+        stream's rows, or -1. q, window, sinks, out, sm_scale: as in attend_tokens."""
+        if _cut_short(layer, window, sinks):
+            raise ValueError("layer, window and sinks must be 32-bit numbers (window 0: none)")
+        if 0 < sm_scale < 2 ** -126:             # C would take what rounds to 0 for the default
+            raise ValueError("sm_scale is too small for fp32")
+        qp, qs = self._rows(q, "q", batch)
+        at = self._ints(parents, "parents", (batch.rows,))
+        out = self._bf16_out(out, "out", q.shape, stream)
+        self._check(self.lib.pkv_attend_tree(self.h, qp, q.shape[1], qs, batch.row_off, batch.sids, batch.n, layer,
+                                             at, out.data_ptr(), window, sinks, sm_scale, self._stream(stream)))
         return out
 
     def token_info(self, sid):
@@ -497,6 +588,6 @@ def synth_fill(out, seed, workload, stream_id, layer, frame0, tensor, token0=0, 
     return out
 
 
-__all__ = ["PagedKVCache", "TokenBatch", "PkvError", "frame_stream_cfg", "chunked_stream_cfg", "synth_fill",
+__all__ = ["PagedKVCache", "TokenBatch", "Rotary", "PkvError", "frame_stream_cfg", "chunked_stream_cfg", "synth_fill",
            "kernel_launches",
            "MODE_FRAME", "MODE_CHUNKED"]

@@ -1309,7 +1309,9 @@ pkv_status pkv_sync(pkv_t h, void* cuda_stream) {
   int err = 0;
   PKV_CUDA(h, cudaMemcpy(&err, h->d_err, sizeof(int), cudaMemcpyDeviceToHost));
   if (err & kErrTimeout) return fail(h, PKV_ERR_TIMEOUT, "a bounded device wait gave up (0x%x)", err);
-  if (err) return fail(h, PKV_ERR_DEVICE, "device error word 0x%x (page id outside the pool)", err);
+  if (err & kErrPageRange) return fail(h, PKV_ERR_DEVICE, "device error word 0x%x (page id outside the pool)", err);
+  if (err)
+    return fail(h, PKV_ERR_DEVICE, "device error word 0x%x (a tree's parents or kept nodes out of order)", err);
   return PKV_OK;
 }
 

@@ -21,6 +21,7 @@ constexpr int kMaxCarry = 64;       // overlap keyframes carried by a window res
 enum : int {
   kErrPageRange = 1,   // a page id outside [0, pool_pages) was read from the metadata
   kErrTimeout = 2,     // a bounded wait gave up
+  kErrTree = 4,        // a tree's parent does not come before its node, or kept nodes are out of order
 };
 
 // 128-byte-swizzled storage: logical 16-byte chunk c of slot s sits at c ^ (s & 7).

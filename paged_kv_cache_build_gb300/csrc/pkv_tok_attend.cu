@@ -33,6 +33,7 @@
 #include "pkv_tokens.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace pkv {
 
@@ -57,7 +58,9 @@ constexpr int kCtasPerSm = 2;
 template <bool FP8>
 constexpr int kRing = FP8 ? 11 : 6;
 
-template <int NT, bool FP8>
+struct NoTree {};
+
+template <int NT, bool FP8, bool TREE>
 struct __align__(1024) FewSmem {
   union {
     struct {
@@ -69,6 +72,7 @@ struct __align__(1024) FewSmem {
   float ml[kWarps<NT>][NT * 8][2];
   uint64_t full[kRing<FP8>];
   uint64_t empty[kRing<FP8>];
+  std::conditional_t<TREE, TreeSmem<NT * 8>, NoTree> tree;
   int abort;
   int last;
 };
@@ -148,10 +152,10 @@ __device__ __forceinline__ void write_row(const Args& a, const TokenQuery& t, co
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
 }
 
-template <int NT, bool FP8, typename Args>
+template <int NT, bool FP8, bool TREE, typename Args>
 __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
-  FewSmem<NT, FP8>& sm = *reinterpret_cast<FewSmem<NT, FP8>*>(
+  FewSmem<NT, FP8, TREE>& sm = *reinterpret_cast<FewSmem<NT, FP8, TREE>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   constexpr int kS = kRing<FP8>;
   static_assert(kS > kWarps<NT>, "the order of the stages' releases");
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   __syncthreads();
-  const TokenWork w = token_work(a, blockIdx.x);
+  const TokenWork w = token_work<TREE>(a, blockIdx.x);
   const TokenQuery& t = a.item[w.item];
   const TokTiles tiles = tok_tiles(w.p0, w.p1, a.window, a.sinks);
   const int j0 = (int)((long long)tiles.n * w.split / t.splits);
@@ -243,7 +247,19 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
     // lane tq, i) is 16 tq + 4 kk + i; bf16: the operand's own order.
     uint32_t qb[NT][4][2];
     float sl2[NT][2];                            // score scale of queries 2 tq, 2 tq + 1
-    int pos[NT][2];
+    int pos[NT][2];                              // trees: the row in the block instead
+    if constexpr (TREE) {
+      // what the rows see of the tree, if the CTA has a tile that some of them do not see whole
+      if (a.window > 0 || (nT > 0 && tok_tile(tiles, j1 - 1) * kTokTile + kTokTile > t.pos0)) {
+        load_parents(sm.tree, a.parents + t.row0, t.n, threadIdx.x, kWarps<NT> * 32, a.err);
+        __syncwarp();
+        asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps<NT> * 32) : "memory");
+        if (threadIdx.x < w.rows)
+          walk_tree(sm.tree, threadIdx.x, (w.r0 + threadIdx.x) / a.group, t.pos0, a.window, a.sinks);
+        __syncwarp();
+        asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps<NT> * 32) : "memory");
+      }
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = n * 8 + g;
@@ -284,8 +300,8 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
       for (int i = 0; i < 2; ++i) {
         const int er = __shfl_sync(0xffffffffu, e, (2 * tq + i) * 4);
         sl2[n][i] = a.scale_log2 * __uint_as_float((uint32_t)(127 + er) << 23);
-        const int rq = min(w.r0 + n * 8 + 2 * tq + i, w.r0 + w.rows - 1);
-        pos[n][i] = t.pos0 + rq / a.group;
+        const int rq = min(n * 8 + 2 * tq + i, w.rows - 1);
+        pos[n][i] = TREE ? rq : t.pos0 + (w.r0 + rq) / a.group;
       }
     }
 
@@ -365,7 +381,8 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
             if ((zeros >> u) & 1u) ve[u >> 1][u & 1] = -INFINITY;
         }
       }
-      const bool full = tok_tile_full(b, w.p0, w.p1, a.window, a.sinks);
+      const bool full = TREE ? tree_tile_full(b, t.pos0, t.n, a.window, a.sinks)
+                             : tok_tile_full(b, w.p0, w.p1, a.window, a.sinks);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -376,7 +393,11 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
             sc[sg][n][2 + i] *= sl2[n][i];
           }
           if (!full) {
-            const uint64_t bits = tok_mask(b, pos[n][i], a.window, a.sinks);
+            uint64_t bits;
+            if constexpr (TREE)
+              bits = tree_mask(b, t.pos0, sm.tree.depth[pos[n][i]], sm.tree.words[pos[n][i]], a.window, a.sinks);
+            else
+              bits = tok_mask(b, pos[n][i], a.window, a.sinks);
 #pragma unroll
             for (int sg = 0; sg < 4; ++sg)
 #pragma unroll
@@ -602,27 +623,34 @@ __global__ void __launch_bounds__(256, 4) token_combine_kernel(const __grid_cons
                  pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
 }
 
-template <int NT, bool FP8, typename Args>
+template <int NT, bool FP8, bool TREE, typename Args>
 cudaError_t launch_few_args(const Args& a, cudaStream_t s) {
-  constexpr int smem = (int)sizeof(FewSmem<NT, FP8>) + 1024;
+  constexpr int smem = (int)sizeof(FewSmem<NT, FP8, TREE>) + 1024;
   static_assert((smem + 1024) * kCtasPerSm <= 228 * 1024, "shared memory per SM");
   static std::atomic<unsigned long long> configured{0};   // a bit per device
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (dev >= 64 || !(configured.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(token_few_kernel<NT, FP8, Args>,
+    const cudaError_t e = cudaFuncSetAttribute(token_few_kernel<NT, FP8, TREE, Args>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) configured.fetch_or(bit);
   }
-  const cudaError_t e = launch_pdl(token_few_kernel<NT, FP8, Args>, dim3(a.ctas), dim3(kThreads<NT>), smem, s, a);
+  const cudaError_t e = launch_pdl(token_few_kernel<NT, FP8, TREE, Args>, dim3(a.ctas), dim3(kThreads<NT>), smem, s, a);
   count_launches(1);
   return e;
 }
-template <int NT, bool FP8>
+template <int NT, bool FP8, bool TREE>
 cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
-  return a.n <= kSmallTokenBatch ? launch_few_args<NT, FP8>(small_args(a), s) : launch_few_args<NT, FP8>(a, s);
+  return a.n <= kSmallTokenBatch ? launch_few_args<NT, FP8, TREE>(small_args(a), s)
+                                 : launch_few_args<NT, FP8, TREE>(a, s);
+}
+template <bool FP8, bool TREE>
+cudaError_t launch_few_rows(const TokenAttendArgs& a, cudaStream_t s) {
+  return a.rows == 8    ? launch_few<1, FP8, TREE>(a, s)
+         : a.rows == 16 ? launch_few<2, FP8, TREE>(a, s)
+                        : launch_few<3, FP8, TREE>(a, s);
 }
 
 }  // namespace
@@ -630,13 +658,8 @@ cudaError_t launch_few(const TokenAttendArgs& a, cudaStream_t s) {
 int token_few_ctas_per_sm() { return kCtasPerSm; }
 
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s) {
-  if (a.pool.fp8)
-    return a.rows == 8    ? launch_few<1, true>(a, s)
-           : a.rows == 16 ? launch_few<2, true>(a, s)
-                          : launch_few<3, true>(a, s);
-  return a.rows == 8    ? launch_few<1, false>(a, s)
-         : a.rows == 16 ? launch_few<2, false>(a, s)
-                        : launch_few<3, false>(a, s);
+  if (a.parents) return a.pool.fp8 ? launch_few_rows<true, true>(a, s) : launch_few_rows<false, true>(a, s);
+  return a.pool.fp8 ? launch_few_rows<true, false>(a, s) : launch_few_rows<false, false>(a, s);
 }
 
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s) {

@@ -16,18 +16,6 @@ namespace {
 constexpr int kQuad = 4;             // tokens that a warp moves at a time
 constexpr int kWarps = 8;
 
-template <typename Args>
-__device__ __forceinline__ int page_of(const Args& a, const TokenRows& it, int pi) {
-  const int page = a.is_meta && pi >= it.old_pages
-                       ? a.free_stack[a.top - 1 - it.pop0 - (pi - it.old_pages)]
-                       : it.pages[pi];
-  if (page < 0 || page >= a.pool.pool_pages) {
-    atomicOr(a.err, kErrPageRange);
-    return -1;
-  }
-  return page;
-}
-
 // Few rows: a warp per quad and plane.
 template <typename Args>
 __global__ void __launch_bounds__(kWarps * 32) token_append_kernel(const __grid_constant__ Args a) {
@@ -280,6 +268,88 @@ __global__ void __launch_bounds__(256) token_drop_kernel(const __grid_constant__
   }
 }
 
+// Accepted drafts move to the front of their tree's slots, in every layer; a warp takes one
+// (stream, layer, K or V, head), 32 rows at a time, read before any of them is written. A row's
+// destination is never behind its source, so what later rounds read is not overwritten. The
+// blocks behind those return the dropped pages.
+constexpr int kKeepRows = 8;         // rows a lane has on their way
+template <typename Args>
+__global__ void __launch_bounds__(kWarps * 32) token_keep_kernel(const __grid_constant__ Args a, int move_blocks) {
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x >= move_blocks) {
+    const TokenKeepItem& it = a.item[blockIdx.x - move_blocks];
+    for (int i = threadIdx.x; i < it.count; i += blockDim.x) {
+      const int p = it.pages[it.start - i];
+      if (p < 0 || p >= a.pool.pool_pages) atomicOr(a.err, kErrPageRange);
+      else a.free_stack[a.top + it.base + i] = p;
+    }
+    return;
+  }
+  const int lane = threadIdx.x & 31, c = lane & 7, t0 = lane >> 3;
+  const int H2 = 2 * a.pool.heads, Ps = a.pool.page_size;
+  const int w = blockIdx.x * kWarps + (threadIdx.x >> 5), planes = a.layers * H2;
+  if (w >= a.n * planes) return;
+  const TokenKeepItem& it = a.item[w / planes];
+  const int layer = w % planes / H2, hh = w % H2, kv = hh >= a.pool.heads ? 1 : 0, h = hh - kv * a.pool.heads;
+  uint8_t* const base = reinterpret_cast<uint8_t*>(a.pool.base) + layer * a.layer_bytes;
+  const int32_t* const kept = a.kept + it.kept0;
+  const auto page_at = [&](int pos) {
+    const int page = it.pages[pos / Ps];
+    if (page >= 0 && page < a.pool.pool_pages) return page;
+    atomicOr(a.err, kErrPageRange);
+    return -1;
+  };
+  for (int r0 = 0; r0 < it.m; r0 += kQuad * kKeepRows) {
+    uint4 val[kKeepRows];
+    int exp[kKeepRows];
+    uint32_t moves = 0;
+#pragma unroll
+    for (int u = 0; u < kKeepRows; ++u) {
+      const int i = r0 + u * kQuad + t0;
+      exp[u] = 0;
+      val[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (i >= it.m) continue;
+      const int x = kept[i];
+      if (x < i || x >= it.n || (i > 0 && kept[i - 1] >= x)) {
+        if (hh == 0 && layer == 0 && c == 0) atomicOr(a.err, kErrTree);
+        if (x < i || x >= it.n) continue;
+      }
+      if (x == i) continue;
+      const int pos = it.pos0 + x, page = page_at(pos), slot = pos % Ps;
+      if (page < 0) continue;
+      const uint8_t* const p = base + (long long)page * a.pool.page_bytes;
+      if (a.pool.fp8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p + fp8_code_off(a.pool.heads, Ps, kv, h, slot) + 8 * c);
+        val[u].x = v.x;
+        val[u].y = v.y;
+        if (c == 0) exp[u] = p[fp8_exp_off(a.pool.heads, Ps, kv, h, slot)];
+      } else {
+        val[u] = *reinterpret_cast<const uint4*>(
+            p + (((long long)hh * Ps + slot) * kHeadDim + swizzle_chunk(slot, c) * 8) * 2);
+      }
+      moves |= 1u << u;
+    }
+    __syncwarp();                                // read before written
+#pragma unroll
+    for (int u = 0; u < kKeepRows; ++u) {
+      if (!((moves >> u) & 1u)) continue;
+      const int pos = it.pos0 + r0 + u * kQuad + t0, page = page_at(pos), slot = pos % Ps;
+      if (page < 0) continue;
+      uint8_t* const p = base + (long long)page * a.pool.page_bytes;
+      if (a.pool.fp8) {
+        *reinterpret_cast<uint2*>(p + fp8_code_off(a.pool.heads, Ps, kv, h, slot) + 8 * c) =
+            make_uint2(val[u].x, val[u].y);
+        if (c == 0) p[fp8_exp_off(a.pool.heads, Ps, kv, h, slot)] = (uint8_t)exp[u];
+      } else {
+        *reinterpret_cast<uint4*>(p + (((long long)hh * Ps + slot) * kHeadDim + swizzle_chunk(slot, c) * 8) * 2) =
+            val[u];
+      }
+    }
+    __syncwarp();
+  }
+}
+
 // Tokens from which a block takes 32 of them: enough blocks to fill the SMs. (Read-back of
 // 64 / 512 / 2560 / 4032 tokens of 8 heads on bf16 pages: 2.0 / 2.2 / 3.8 / 4.8 us with a
 // warp per quad and plane, 4.7 / 3.6 / 3.6 / 3.7 us with blocks of 32. The rule asks for
@@ -297,6 +367,7 @@ int row_blocks(const TokenRowsArgs& a) {
 
 using SmallRowsArgs = TokenRowsArgsOf<kSmallTokenBatch>;
 using SmallDropArgs = TokenDropArgsOf<kSmallTokenBatch>;
+using SmallKeepArgs = TokenKeepArgsOf<kSmallTokenBatch>;
 
 }  // namespace
 
@@ -336,6 +407,17 @@ cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s) {
       a.n <= kSmallTokenBatch
           ? launch_pdl(token_drop_kernel<SmallDropArgs>, dim3(a.n), threads, 0, s, small_args(a))
           : launch_pdl(token_drop_kernel<TokenDropArgs>, dim3(a.n), threads, 0, s, a);
+  count_launches(1);
+  return e;
+}
+
+cudaError_t launch_token_keep(const TokenKeepArgs& a, cudaStream_t s) {
+  const int blocks = (a.n * a.layers * 2 * a.pool.heads + kWarps - 1) / kWarps;
+  const dim3 grid(blocks + a.n), threads(kWarps * 32);
+  const cudaError_t e =
+      a.n <= kSmallTokenBatch
+          ? launch_pdl(token_keep_kernel<SmallKeepArgs>, grid, threads, 0, s, small_args(a), blocks)
+          : launch_pdl(token_keep_kernel<TokenKeepArgs>, grid, threads, 0, s, a, blocks);
   count_launches(1);
   return e;
 }

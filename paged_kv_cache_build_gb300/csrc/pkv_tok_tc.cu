@@ -89,7 +89,9 @@ template <int MT, bool FP8>
 constexpr uint32_t kTmemCols = 128 * kLanes<MT, FP8>;
 constexpr float kSumLimit = 1024.0f;           // values up to 2^90 cannot take O past fp32's end
 
-template <int MT, bool FP8>
+struct NoTree {};
+
+template <int MT, bool FP8, bool TREE>
 struct __align__(1024) TcSmem {
   uint8_t q[MT][128 * 128];
   union {
@@ -116,6 +118,7 @@ struct __align__(1024) TcSmem {
   const int32_t* pages;
   uint32_t tmem_base;
   int abort;
+  std::conditional_t<TREE, TreeSmem<kTreeNodes>, NoTree> tree;   // by node
 };
 
 __device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float s, float c) {
@@ -164,20 +167,22 @@ struct LaneRows {
   int n;
   TokSpan span;
 };
+template <bool TREE>
 __device__ __forceinline__ LaneRows lane_rows(const TokenAttendArgs& a, const TokenWork& w, int pos0, int m) {
   LaneRows l;
   l.n = min(128, w.rows - 128 * m);
   const int r0 = w.r0 + 128 * m;
-  l.span = tok_span(pos0 + r0 / a.group, pos0 + (r0 + l.n - 1) / a.group, a.window, a.sinks);
+  if constexpr (TREE) l.span = tree_span(pos0, w.p1 - pos0 + 1, a.window, a.sinks);
+  else l.span = tok_span(pos0 + r0 / a.group, pos0 + (r0 + l.n - 1) / a.group, a.window, a.sinks);
   if (l.n <= 0) l.span.hi = -1;
   return l;
 }
 
-template <int MT, bool FP8>
+template <int MT, bool FP8, bool TREE>
 __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     token_tc_kernel(const __grid_constant__ TokenAttendArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  TcSmem<MT, FP8>& sm = *reinterpret_cast<TcSmem<MT, FP8>*>(
+  TcSmem<MT, FP8, TREE>& sm = *reinterpret_cast<TcSmem<MT, FP8, TREE>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   constexpr int kS = kRing<MT, FP8>;
   constexpr int kParts = kLanes<MT, FP8> / MT;
@@ -207,7 +212,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
   if (threadIdx.x == 32) {
-    const TokenWork w = token_work(a, blockIdx.x);
+    const TokenWork w = token_work<TREE>(a, blockIdx.x);
     const TokenQuery& t = a.item[w.item];
     const TokTiles tiles = tok_tiles(w.p0, w.p1, a.window, a.sinks);
     sm.work = w;
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8>));
     {
       const int li = warp - kIssuer0<MT, FP8>;
-      const TokSpan span = lane_rows(a, sm.work, sm.pos0, li % MT).span;
+      const TokSpan span = lane_rows<TREE>(a, sm.work, sm.pos0, li % MT).span;
       const int nT = sm.j1 - sm.j0, j0 = sm.j0;
       const TokTiles tiles = sm.tiles;
       const uint32_t tmem = sm.tmem_base;
@@ -424,8 +429,28 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs<MT, FP8>));
     const int li = warp >> 2, m_blk = li % MT, part = li / MT;
     const int wq = warp & 3, r = wq * 32 + lane;           // row of the lane's 128
-    const LaneRows rows = lane_rows(a, sm.work, sm.pos0, m_blk);
-    const int p = sm.pos0 + (w.r0 + 128 * m_blk + min(r, max(rows.n, 1) - 1)) / G;
+    const LaneRows rows = lane_rows<TREE>(a, sm.work, sm.pos0, m_blk);
+    const int node = (w.r0 + 128 * m_blk + min(r, max(rows.n, 1) - 1)) / G;
+    const int p = sm.pos0 + node;
+    if constexpr (TREE) {
+      // what the nodes see of the tree, if the CTA has a tile that some of them do not see whole
+      if (a.window > 0 || (sm.j1 > sm.j0 && tok_tile(sm.tiles, sm.j1 - 1) * kBN + kBN > sm.pos0)) {
+        constexpr int kMen = kSoftmaxWarps<MT, FP8> * 32;
+        const int nodes = w.p1 - sm.pos0 + 1;
+        load_parents(sm.tree, a.parents + sm.row0, nodes, threadIdx.x, kMen, a.err);
+        __syncwarp();
+        asm volatile("bar.sync 2, %0;\n" ::"n"(kMen) : "memory");
+        for (int i = threadIdx.x; i < nodes; i += kMen) walk_tree(sm.tree, i, i, sm.pos0, a.window, a.sinks);
+        __syncwarp();
+        asm volatile("bar.sync 2, %0;\n" ::"n"(kMen) : "memory");
+      }
+    }
+    const auto row_bits = [&](int tile) -> uint64_t {
+      if constexpr (TREE)
+        return tree_mask(tile * kBN, sm.pos0, sm.tree.depth[node], sm.tree.words[node], a.window, a.sinks);
+      else
+        return tok_mask(tile * kBN, p, a.window, a.sinks);
+    };
     const uint32_t tmem = sm.tmem_base;
     const uint32_t t_lane = (uint32_t)(wq * 32) << 16;
     const uint32_t t_s = tmem + t_lane + 64 * li, t_o = t_s + 64 * kLanes<MT, FP8>;
@@ -451,7 +476,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
       const auto exponentiate = [&](auto masked) {
         const float m_ref = m_run == -INFINITY ? 0.f : m_run;
         uint64_t bits = 0;
-        if constexpr (masked) bits = tok_mask(tile * kBN, p, a.window, a.sinks);
+        if constexpr (masked) bits = row_bits(tile);
         sum0 = sum1 = 0.f;
         float v[2][16];
         PKV_TMEM_LD16(t_s, reinterpret_cast<uint32_t*>(v[0]));
@@ -485,7 +510,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
         const bool redo = m_run == -INFINITY || !(sum0 + sum1 <= kSumLimit);
         if (pass == 1 || !__any_sync(0xffffffffu, redo)) break;
         // the row's maximum becomes its reference (S is still in TMEM)
-        const uint64_t bits = tok_mask(tile * kBN, p, a.window, a.sinks);
+        const uint64_t bits = TREE && whole ? ~0ull : row_bits(tile);
         float mx = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < kBN; c += 16) {
@@ -632,27 +657,36 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
   }
 }
 
-template <int MT, bool FP8>
+template <int MT, bool FP8, bool TREE>
 cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
-  constexpr int smem = (int)sizeof(TcSmem<MT, FP8>) + 1024;
+  constexpr int smem = (int)sizeof(TcSmem<MT, FP8, TREE>) + 1024;
   static_assert((smem + 1024) * kCtasPerSm<MT, FP8> <= 228 * 1024, "shared memory per SM");
   static std::atomic<unsigned long long> configured{0};   // a bit per device
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (dev >= 64 || !(configured.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(token_tc_kernel<MT, FP8>,
+    const cudaError_t e = cudaFuncSetAttribute(token_tc_kernel<MT, FP8, TREE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // a warpgroup that asks for more registers than the launch brought would wait for ever
     cudaFuncAttributes attr;
-    if (cudaError_t e2 = cudaFuncGetAttributes(&attr, token_tc_kernel<MT, FP8>)) return e2;
+    if (cudaError_t e2 = cudaFuncGetAttributes(&attr, token_tc_kernel<MT, FP8, TREE>)) return e2;
     if (attr.numRegs < kLaunchRegs<MT, FP8>) return cudaErrorInvalidConfiguration;
     if (dev < 64) configured.fetch_or(bit);
   }
-  const cudaError_t e = launch_pdl(token_tc_kernel<MT, FP8>, dim3(a.ctas), dim3(kThreads<MT, FP8>), smem, s, a);
+  const cudaError_t e = launch_pdl(token_tc_kernel<MT, FP8, TREE>, dim3(a.ctas), dim3(kThreads<MT, FP8>), smem, s, a);
   count_launches(1);
   return e;
+}
+
+template <bool TREE>
+cudaError_t launch_tc_rows(const TokenAttendArgs& a, cudaStream_t s) {
+  if (a.pool.fp8)
+    return a.rows == 128   ? launch_tc<1, true, TREE>(a, s)
+           : a.rows == 256 ? launch_tc<2, true, TREE>(a, s)
+                           : launch_tc<4, true, TREE>(a, s);
+  return a.rows == 128 ? launch_tc<1, false, TREE>(a, s) : launch_tc<2, false, TREE>(a, s);
 }
 
 }  // namespace
@@ -662,11 +696,7 @@ int token_tc_max_rows(bool fp8) { return fp8 ? 512 : 256; }
 int token_tc_ctas_per_sm(bool fp8, int rows) { return !fp8 && rows == 256 ? kCtasPerSm<2, false> : 1; }
 
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s) {
-  if (a.pool.fp8)
-    return a.rows == 128   ? launch_tc<1, true>(a, s)
-           : a.rows == 256 ? launch_tc<2, true>(a, s)
-                           : launch_tc<4, true>(a, s);
-  return a.rows == 128 ? launch_tc<1, false>(a, s) : launch_tc<2, false>(a, s);
+  return a.parents ? launch_tc_rows<true>(a, s) : launch_tc_rows<false>(a, s);
 }
 
 }  // namespace pkv

@@ -72,6 +72,10 @@ inline bool tok_can_drop(const TokenCounts& t, int n) {
   if (n < 0 || n > t.len) return false;
   return t.gap1 == t.keep0 || tok_window_lo(t.len - n, t.window) >= t.gap1 * t.page_size;
 }
+// Whether the last n tokens are held.
+inline bool tok_has_last(const TokenCounts& t, int n) {
+  return n == 0 || t.gap1 == t.keep0 || t.len - n >= t.gap1 * t.page_size;
+}
 // Pages that the drop frees: the list's last ones.
 inline int tok_drop_pages(const TokenCounts& t, int n) { return t.n_pages - tok_pages(t.len - n, t.page_size); }
 inline void tok_drop(TokenCounts* t, int n) {
@@ -151,6 +155,47 @@ PKV_HD int tok_block_entry(int f, int rows, int p0, int p1, int window, int sink
 // Bit i: whether slot b + i is seen from position p.
 PKV_HD uint64_t tok_mask(int b, int p, int window, int sinks) {
   return tok_low_bits(p - b + 1) & (~tok_low_bits(tok_window_lo(p, window) - b) | tok_low_bits(sinks - b));
+}
+
+
+// ---------------------------------------------------------- trees of drafted tokens
+// A stream's last n tokens, slots pos0 .. pos0 + n - 1, are the nodes of a tree: node i's
+// parent is a node before it, or -1. Its position is pos0 + depth. It sees the slots
+// before pos0, its ancestors and itself; a window and sinks go by positions.
+constexpr int kTreeNodes = 256;                          // of one stream
+constexpr int kTreeWords = kTreeNodes / kTokTile + 1;    // tiles that the nodes' slots may touch
+
+// A parent as read; -2 where it does not come before its node.
+PKV_HD int tree_parent(int i, int p) { return p >= -1 && p < i ? p : -2; }
+
+// The tiles that the tree's nodes see something of, and those that all of them see whole.
+PKV_HD TokSpan tree_span(int pos0, int n, int window, int sinks) {
+  TokSpan s = tok_span(pos0, pos0 + n - 1, window, sinks);
+  s.f1 = pos0 / kTokTile;
+  return s;
+}
+PKV_HD bool tree_tile_full(int b, int pos0, int n, int window, int sinks) {
+  return tok_tile_full(b, pos0 - 1, pos0 + n - 1, window, sinks);
+}
+// Node i's depth, and the tree's slots that it sees: bit x % 64 of words[x / 64], x counted
+// from the start of pos0's tile (words: zeros before).
+template <typename Parent>
+PKV_HD int tree_walk(const Parent* parent, int i, int pos0, int window, int sinks, uint64_t* words) {
+  int depth = -1;
+  for (int a = i; a >= 0; a = parent[a]) ++depth;
+  int k = 0;
+  for (int a = i; a >= 0; a = parent[a], ++k)
+    if (window == 0 || k < window || pos0 + depth - k < sinks) {
+      const int x = pos0 % kTokTile + a;
+      words[x / kTokTile] |= 1ull << (x % kTokTile);
+    }
+  return depth;
+}
+// Bit i: whether slot b + i is seen by a node at that depth with those words.
+PKV_HD uint64_t tree_mask(int b, int pos0, int depth, const uint64_t* words, int window, int sinks) {
+  const uint64_t before = tok_mask(b, pos0 + depth, window, sinks) & tok_low_bits(pos0 - b);
+  const int t = b / kTokTile - pos0 / kTokTile;
+  return before | (t >= 0 && t < kTreeWords ? words[t] : 0ull);
 }
 
 }  // namespace pkv

@@ -21,6 +21,7 @@ constexpr int kMaxGroup = 128;       // query heads per KV head
 constexpr size_t kTokenScratchBytes = size_t(64) << 20;
 
 constexpr int kTokenJoins = 16384;   // counters of the splits' joins
+constexpr double kMaxFreq = 1048576.0;   // radians per unit of position
 
 bool misaligned(const void* p) { return !p || !aligned16(p); }
 
@@ -115,6 +116,219 @@ void plan_splits(TokenAttendArgs* a, const int* first, const int* last, const Ct
   a->ctas = cta;
 }
 
+// The rotation as the kernel takes it: whole turns do not matter for whole positions, so a
+// pair's angle is position x turn in 64-bit arithmetic that wraps, 2^64 to the turn, exact for
+// every 32-bit position. freq / 2 pi is taken with twice a double's digits.
+pkv_status rotary_args(pkv_t h, const pkv_rotary* r, RotaryArgs* a) {
+  if (!r) return fail(h, PKV_ERR_INVALID, "null rotary");
+  if (r->axes < 1 || r->axes > kMaxAxes)
+    return fail(h, PKV_ERR_INVALID, "%d position axes, not 1..%d", r->axes, kMaxAxes);
+  const int d = r->pair_distance;
+  if (d < 1 || d > kHeadDim / 2 || (d & (d - 1)) != 0)
+    return fail(h, PKV_ERR_INVALID, "pair_distance %d is no power of two in 1..%d", d, kHeadDim / 2);
+  std::memset(a, 0, sizeof(*a));
+  a->axes = r->axes;
+  a->distance = d;
+  for (int i = 0; i < kHeadDim / 2; ++i) {
+    if (r->axis[i] < 0 || r->axis[i] >= r->axes)
+      return fail(h, PKV_ERR_INVALID, "pair %d: axis %d of %d", i, r->axis[i], r->axes);
+    if (!(std::fabs(r->freq[i]) <= kMaxFreq))
+      return fail(h, PKV_ERR_INVALID, "pair %d: a frequency of %g (at most %g in magnitude)", i, r->freq[i], kMaxFreq);
+    const double inv = 0.15915494309189535, inv_low = -9.839338337591243e-18;   // 1 / 2 pi
+    const double t = r->freq[i] * inv;
+    const double low = std::fma(r->freq[i], inv, -t) + r->freq[i] * inv_low;
+    const double part = t - std::rint(t);        // exact, within half a turn
+    const double two64 = 18446744073709551616.0;
+    a->turn[i] = (part == 0.5 ? 1ull << 63 : (unsigned long long)std::llrint(part * two64)) +
+                 (unsigned long long)std::llrint(low * two64);
+    a->axis[i] = (uint8_t)r->axis[i];
+  }
+  return PKV_OK;
+}
+
+// An append, with or without rotation.
+pkv_status append_rows(pkv_t h, int n, const int* sids, const int* row_off, int layer, const void* k,
+                       const void* v, long long k_stride, long long v_stride, const RotaryArgs* rotary,
+                       void* cuda_stream) {
+  if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
+  if (!row_off) return fail(h, PKV_ERR_INVALID, "null row_off");
+  if (pkv_status r = check_layer(h, layer)) return r;
+  const int row = h->H * kHeadDim;
+  if (k_stride == 0) k_stride = row;
+  if (v_stride == 0) v_stride = row;
+  if (pkv_status r = check_stride(h, "k_stride", k_stride, row)) return r;
+  if (pkv_status r = check_stride(h, "v_stride", v_stride, row)) return r;
+  if (row_off[n] > 0 && (misaligned(k) || misaligned(v)))
+    return fail(h, PKV_ERR_INVALID, "k/v must be 16-byte aligned device pointers");
+  TokenRowsArgs a;
+  rows_args(h, layer, &a);
+  a.k = const_cast<uint16_t*>(static_cast<const uint16_t*>(k));
+  a.v = const_cast<uint16_t*>(static_cast<const uint16_t*>(v));
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.is_meta = layer == 0 ? 1 : 0;
+  a.n = n;
+  long long need = 0, units = 0;
+  for (int i = 0; i < n; ++i) {
+    Stream& st = h->streams[sids[i]];
+    const TokenCounts& t = st.tok;
+    const int rows = row_off[i + 1] - row_off[i];
+    TokenRows& it = a.item[i];
+    it.pages = st.d_pages;
+    it.unit0 = (int)units;
+    it.row0 = row_off[i];
+    it.n = rows;
+    it.pop0 = (int)need;
+    if (layer == 0) {
+      if (rows > t.max_tokens - t.len)
+        return fail(h, PKV_ERR_INVALID, "stream %d: %d + %d tokens exceed its %d", sids[i], t.len, rows,
+                    t.max_tokens);
+      it.pos0 = t.len;
+      it.old_pages = t.n_pages;
+      need += tok_append_need(t, rows);
+    } else {
+      if (rows == 0) {
+        it.pos0 = t.len;
+        it.old_pages = t.n_pages;
+      } else {
+        if (!t.pending) return fail(h, PKV_ERR_STATE, "stream %d: layer > 0 append without one on layer 0", sids[i]);
+        if (rows != t.len - t.u_pos0)
+          return fail(h, PKV_ERR_INVALID, "stream %d: %d rows, the append on layer 0 had %d", sids[i], rows,
+                      t.len - t.u_pos0);
+        it.pos0 = t.u_pos0;
+        it.old_pages = t.u_old_pages;
+      }
+    }
+    units += rows + tok_zero_slots(t, it.pos0, rows, it.old_pages);
+  }
+  if (need > h->free_top)
+    return fail(h, PKV_ERR_OOM, "free list exhausted (%lld pages needed, %d free)", need, h->free_top);
+  if (units == 0) return PKV_OK;
+  a.units = (int)units;
+  cudaStream_t s = as_stream(cuda_stream);
+  PKV_CUDA(h, rotary ? launch_token_append_rotary(a, *rotary, s) : launch_token_append(a, s));
+  if (layer == 0) {
+    h->free_top -= (int)need;
+    for (int i = 0; i < n; ++i)
+      if (a.item[i].n > 0) tok_append(&h->streams[sids[i]].tok, a.item[i].n);
+  }
+  return PKV_OK;
+}
+
+// Attention of the streams' last tokens: in a row, or (parents) as trees.
+pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
+                       const int* sids, int n, int layer, const int32_t* parents, void* out, int window,
+                       int sinks, float sm_scale, void* cuda_stream) {
+  if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
+  if (!row_off) return fail(h, PKV_ERR_INVALID, "null row_off");
+  if (pkv_status r = check_layer(h, layer)) return r;
+  if (q_heads < 1 || q_heads % h->H != 0 || q_heads / h->H > kMaxGroup)
+    return fail(h, PKV_ERR_INVALID, "q_heads %d must be 1..%d times the cache's %d heads", q_heads, kMaxGroup, h->H);
+  if (window < 0 || sinks < 0 || (window == 0 && sinks > 0))
+    return fail(h, PKV_ERR_INVALID, "window and sinks >= 0 required (no sinks without a window)");
+  const float scale = sm_scale <= 0.f ? 1.0f / std::sqrt((float)h->D) : sm_scale;
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isnormal(scale) || !std::isnormal(scale_log2))
+    return fail(h, PKV_ERR_INVALID, "sm_scale %g (times log2 e) is no normal fp32 number", sm_scale);
+  const int group = q_heads / h->H, row = q_heads * kHeadDim;
+  if (q_stride == 0) q_stride = row;
+  if (pkv_status r = check_stride(h, "q_stride", q_stride, row)) return r;
+  if (row_off[n] == 0) return PKV_OK;
+  if ((long long)row_off[n] * q_heads > INT_MAX / 16)
+    return fail(h, PKV_ERR_INVALID, "%d rows of %d heads are too many for one call", row_off[n], q_heads);
+  if (misaligned(q) || misaligned(out))
+    return fail(h, PKV_ERR_INVALID, "q/out must be 16-byte aligned device pointers");
+  TokenAttendArgs a;
+  std::memset(&a, 0, offsetof(TokenAttendArgs, item));
+  a.q = static_cast<const uint16_t*>(q);
+  a.out = static_cast<uint16_t*>(out);
+  a.parents = parents;
+  a.q_stride = q_stride;
+  a.heads = h->H;
+  a.group = group;
+  a.pool = pool_view(h, layer);
+  a.window = window;
+  a.sinks = sinks;
+  a.scale_log2 = scale_log2;
+  a.err = h->d_err;
+  a.joined = h->d_joined;
+  int first[kMaxTokenBatch], last[kMaxTokenBatch];
+  for (int i = 0; i < n; ++i) {
+    const Stream& st = h->streams[sids[i]];
+    const TokenCounts& t = st.tok;
+    const int rows = row_off[i + 1] - row_off[i];
+    if (rows > t.len)
+      return fail(h, PKV_ERR_STATE, "stream %d: %d query rows, but only %d tokens", sids[i], rows, t.len);
+    if (rows == 0) continue;
+    if (!tok_holds(t, tok_window_lo(t.len - rows, window), sinks))
+      return fail(h, PKV_ERR_STATE, "stream %d: keys that its queries see are evicted", sids[i]);
+    TokenQuery& it = a.item[a.n++];
+    it.pages = st.d_pages;
+    it.row0 = row_off[i];
+    it.n = rows;
+    it.pos0 = t.len - rows;
+  }
+  // one launch per kernel: the streams' rows per KV head decide
+  cudaStream_t s = as_stream(cuda_stream);
+  const int n_items = a.n;
+  TokenQuery all[kMaxTokenBatch];
+  std::copy(a.item, a.item + n_items, all);
+  long long rows_sum = 0;
+  int n_small = 0;
+  for (int i = 0; i < n_items; ++i) {
+    const long long r = (long long)all[i].n * group;
+    if (r <= kTokenFewRows) rows_sum += r, ++n_small;
+  }
+  const int few_rows = rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
+  const int max_rows = token_tc_max_rows(h->fp8);
+  // one shape for all streams of the matrix-unit kernel, the largest's. On bf16 pages a second
+  // launch costs more than the lanes that stay idle: 2 .. 34 new tokens of 18 streams, 25.8
+  // against 39.1 us; a chunk of 1500 tokens beside 11 drafts of 20, group 4, 99 against 122 us.
+  // On E4M3 pages it depends: the first batch 36.6 against 56.6 us, the second 165 against 155
+  // us (there the 512-row shape leaves three of a draft's four lanes without rows).
+  int tc_rows = 128;
+  for (int i = 0; i < n_items; ++i)
+    while (tc_rows < max_rows && (long long)all[i].n * group > tc_rows) tc_rows *= 2;
+  for (const int shape : {few_rows, tc_rows}) {
+    const int below = shape == few_rows ? 0 : few_rows;
+    a.n = 0;
+    int most = 0;
+    for (int i = 0; i < n_items; ++i) {
+      const long long r = (long long)all[i].n * group;
+      if (r <= below || (r > shape && shape == few_rows)) continue;
+      a.item[a.n++] = all[i];
+      most = std::max(most, (int)std::min<long long>(r, shape));
+    }
+    if (a.n == 0) continue;
+    const bool few = shape == few_rows;
+    a.rows = !few ? shape : most <= 8 ? 8 : most > 16 && most <= 24 ? 24 : 16;
+    for (int i = 0; i < a.n; ++i) {
+      TokenQuery& it = a.item[i];
+      it.blocks = ceil_div((long long)it.n * group, a.rows);
+      const auto block_tiles = [&](int b) {
+        if (parents) return tok_tiles(it.pos0, it.pos0 + it.n - 1, window, sinks).n;
+        const int r0 = b * a.rows, r1 = std::min(r0 + a.rows, it.n * group) - 1;
+        return tok_tiles(it.pos0 + r0 / group, it.pos0 + r1 / group, window, sinks).n;
+      };
+      first[i] = block_tiles(0);
+      last[i] = block_tiles(it.blocks - 1);
+    }
+    const int room = std::min<int>(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
+    const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 12, 4, 8, room}
+                             : CtaCost{h->num_sms * token_tc_ctas_per_sm(h->fp8, shape), 10, 4, 8, room};
+    plan_splits(&a, first, last, cost);
+    bool split = false;
+    for (int i = 0; i < a.n; ++i) split = split || a.item[i].splits > 1;
+    if (split) {
+      a.part_o = h->d_token_part;
+      a.part_ml = h->d_token_part + (size_t)a.ctas * a.rows * kHeadDim;
+    }
+    PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, s));
+    if (split && !few) PKV_CUDA(h, launch_token_combine(a, s));
+  }
+  return PKV_OK;
+}
+
 }  // namespace
 
 namespace pkv {
@@ -189,68 +403,36 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
 pkv_status pkv_append_tokens(pkv_t h, int n, const int* sids, const int* row_off, int layer,
                              const void* k, const void* v, long long k_stride, long long v_stride,
                              void* cuda_stream) {
+  return append_rows(h, n, sids, row_off, layer, k, v, k_stride, v_stride, nullptr, cuda_stream);
+}
+
+pkv_status pkv_append_tokens_rotary(pkv_t h, int n, const int* sids, const int* row_off, int layer,
+                                    const void* k, const void* v, long long k_stride, long long v_stride,
+                                    const void* q, int q_heads, long long q_stride, void* q_out,
+                                    const void* positions, const pkv_rotary* rotary, void* cuda_stream) {
   if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
   if (!row_off) return fail(h, PKV_ERR_INVALID, "null row_off");
-  if (pkv_status r = check_layer(h, layer)) return r;
-  const int row = h->H * kHeadDim;
-  if (k_stride == 0) k_stride = row;
-  if (v_stride == 0) v_stride = row;
-  if (pkv_status r = check_stride(h, "k_stride", k_stride, row)) return r;
-  if (pkv_status r = check_stride(h, "v_stride", v_stride, row)) return r;
-  if (row_off[n] > 0 && (misaligned(k) || misaligned(v)))
-    return fail(h, PKV_ERR_INVALID, "k/v must be 16-byte aligned device pointers");
-  TokenRowsArgs a;
-  rows_args(h, layer, &a);
-  a.k = const_cast<uint16_t*>(static_cast<const uint16_t*>(k));
-  a.v = const_cast<uint16_t*>(static_cast<const uint16_t*>(v));
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.is_meta = layer == 0 ? 1 : 0;
-  a.n = n;
-  long long need = 0, units = 0;
-  for (int i = 0; i < n; ++i) {
-    Stream& st = h->streams[sids[i]];
-    const TokenCounts& t = st.tok;
-    const int rows = row_off[i + 1] - row_off[i];
-    TokenRows& it = a.item[i];
-    it.pages = st.d_pages;
-    it.unit0 = (int)units;
-    it.row0 = row_off[i];
-    it.n = rows;
-    it.pop0 = (int)need;
-    if (layer == 0) {
-      if (rows > t.max_tokens - t.len)
-        return fail(h, PKV_ERR_INVALID, "stream %d: %d + %d tokens exceed its %d", sids[i], t.len, rows,
-                    t.max_tokens);
-      it.pos0 = t.len;
-      it.old_pages = t.n_pages;
-      need += tok_append_need(t, rows);
-    } else {
-      if (rows == 0) {
-        it.pos0 = t.len;
-        it.old_pages = t.n_pages;
-      } else {
-        if (!t.pending) return fail(h, PKV_ERR_STATE, "stream %d: layer > 0 append without one on layer 0", sids[i]);
-        if (rows != t.len - t.u_pos0)
-          return fail(h, PKV_ERR_INVALID, "stream %d: %d rows, the append on layer 0 had %d", sids[i], rows,
-                      t.len - t.u_pos0);
-        it.pos0 = t.u_pos0;
-        it.old_pages = t.u_old_pages;
-      }
-    }
-    units += rows + tok_zero_slots(t, it.pos0, rows, it.old_pages);
+  RotaryArgs a;
+  if (pkv_status r = rotary_args(h, rotary, &a)) return r;
+  if (q_heads < 0 || q_heads > kMaxGroup * h->H)
+    return fail(h, PKV_ERR_INVALID, "q_heads %d outside 0..%d", q_heads, kMaxGroup * h->H);
+  const int row = q_heads * kHeadDim;
+  if (q_stride == 0) q_stride = row;
+  if (pkv_status r = check_stride(h, "q_stride", q_stride, row)) return r;
+  if (row_off[n] > 0) {
+    if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
+      return fail(h, PKV_ERR_INVALID, "positions must be a 4-byte aligned device pointer");
+    if (q_heads > 0 && (misaligned(q) || misaligned(q_out)))
+      return fail(h, PKV_ERR_INVALID, "q/q_out must be 16-byte aligned device pointers");
+    if (q_heads > 0 && q == q_out && q_stride != row)
+      return fail(h, PKV_ERR_INVALID, "q_out may be q only where q is contiguous");
   }
-  if (need > h->free_top)
-    return fail(h, PKV_ERR_OOM, "free list exhausted (%lld pages needed, %d free)", need, h->free_top);
-  if (units == 0) return PKV_OK;
-  a.units = (int)units;
-  PKV_CUDA(h, launch_token_append(a, as_stream(cuda_stream)));
-  if (layer == 0) {
-    h->free_top -= (int)need;
-    for (int i = 0; i < n; ++i)
-      if (a.item[i].n > 0) tok_append(&h->streams[sids[i]].tok, a.item[i].n);
-  }
-  return PKV_OK;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_stride = q_stride;
+  a.q_heads = q_heads;
+  a.positions = static_cast<const int32_t*>(positions);
+  return append_rows(h, n, sids, row_off, layer, k, v, k_stride, v_stride, &a, cuda_stream);
 }
 
 pkv_status pkv_drop_tokens(pkv_t h, int n, const int* sids, const int* counts, void* cuda_stream) {
@@ -286,6 +468,57 @@ pkv_status pkv_drop_tokens(pkv_t h, int n, const int* sids, const int* counts, v
   h->free_top += base;
   for (int i = 0; i < n; ++i)
     if (counts[i] > 0) tok_drop(&h->streams[sids[i]].tok, counts[i]);
+  return PKV_OK;
+}
+
+pkv_status pkv_keep_tokens(pkv_t h, int n, const int* sids, const int* row_off, const int* keep_off,
+                           const void* kept, void* cuda_stream) {
+  if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
+  if (!row_off || !keep_off) return fail(h, PKV_ERR_INVALID, "null offsets");
+  if (keep_off[0] != 0) return fail(h, PKV_ERR_INVALID, "keep_off[0] must be 0");
+  TokenKeepArgs a;
+  std::memset(static_cast<void*>(&a), 0, offsetof(TokenKeepArgs, item));
+  a.pool = pool_view(h, 0);
+  a.layer_bytes = (long long)h->P * h->page_bytes;
+  a.layers = h->L;
+  a.kept = static_cast<const int32_t*>(kept);
+  a.free_stack = h->d_free;
+  a.top = h->free_top;
+  a.err = h->d_err;
+  int base = 0;
+  // the last stream's pages first, as where they are dropped
+  for (int i = n - 1; i >= 0; --i) {
+    const Stream& st = h->streams[sids[i]];
+    const TokenCounts& t = st.tok;
+    const int rows = row_off[i + 1] - row_off[i];
+    const long long m = (long long)keep_off[i + 1] - keep_off[i];
+    if (m < 0 || m > rows)
+      return fail(h, PKV_ERR_INVALID, "stream %d: %lld of %d tokens to keep", sids[i], m, rows);
+    if (rows > t.len)
+      return fail(h, PKV_ERR_INVALID, "stream %d: the last %d of its %d tokens", sids[i], rows, t.len);
+    if (rows == 0) continue;
+    if (!tok_can_drop(t, rows - (int)m) || !tok_has_last(t, rows))
+      return fail(h, PKV_ERR_STATE, "stream %d: tokens that would stay or be seen are evicted", sids[i]);
+    TokenKeepItem& it = a.item[a.n++];
+    it.pages = st.d_pages;
+    it.pos0 = t.len - rows;
+    it.n = rows;
+    it.m = (int)m;
+    it.kept0 = keep_off[i];
+    it.start = t.n_pages - 1;
+    it.count = tok_drop_pages(t, rows - (int)m);
+    it.base = base;
+    base += it.count;
+  }
+  if (keep_off[n] > 0 && (!kept || (reinterpret_cast<uintptr_t>(kept) & 3u) != 0))
+    return fail(h, PKV_ERR_INVALID, "kept must be a 4-byte aligned device pointer");
+  if (h->free_top + base > h->P) return fail(h, PKV_ERR_STATE, "free stack overflow");
+  if (keep_off[n] > 0 || base > 0) PKV_CUDA(h, launch_token_keep(a, as_stream(cuda_stream)));
+  h->free_top += base;
+  for (int i = 0; i < n; ++i) {
+    const int rows = row_off[i + 1] - row_off[i];
+    if (rows > 0) tok_drop(&h->streams[sids[i]].tok, rows - (keep_off[i + 1] - keep_off[i]));
+  }
   return PKV_OK;
 }
 
@@ -329,112 +562,23 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* sids, const int* pos0, con
 pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
                              const int* sids, int n, int layer, void* out, int window, int sinks,
                              float sm_scale, void* cuda_stream) {
+  return attend_rows(h, q, q_heads, q_stride, row_off, sids, n, layer, nullptr, out, window, sinks, sm_scale,
+                     cuda_stream);
+}
+
+pkv_status pkv_attend_tree(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
+                           const int* sids, int n, int layer, const void* parents, void* out, int window,
+                           int sinks, float sm_scale, void* cuda_stream) {
   if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
   if (!row_off) return fail(h, PKV_ERR_INVALID, "null row_off");
-  if (pkv_status r = check_layer(h, layer)) return r;
-  if (q_heads < 1 || q_heads % h->H != 0 || q_heads / h->H > kMaxGroup)
-    return fail(h, PKV_ERR_INVALID, "q_heads %d must be 1..%d times the cache's %d heads", q_heads, kMaxGroup, h->H);
-  if (window < 0 || sinks < 0 || (window == 0 && sinks > 0))
-    return fail(h, PKV_ERR_INVALID, "window and sinks >= 0 required (no sinks without a window)");
-  const float scale = sm_scale <= 0.f ? 1.0f / std::sqrt((float)h->D) : sm_scale;
-  const float scale_log2 = scale * 1.4426950408889634f;
-  if (!std::isnormal(scale) || !std::isnormal(scale_log2))
-    return fail(h, PKV_ERR_INVALID, "sm_scale %g (times log2 e) is no normal fp32 number", sm_scale);
-  const int group = q_heads / h->H, row = q_heads * kHeadDim;
-  if (q_stride == 0) q_stride = row;
-  if (pkv_status r = check_stride(h, "q_stride", q_stride, row)) return r;
-  if (row_off[n] == 0) return PKV_OK;
-  if ((long long)row_off[n] * q_heads > INT_MAX / 16)
-    return fail(h, PKV_ERR_INVALID, "%d rows of %d heads are too many for one call", row_off[n], q_heads);
-  if (misaligned(q) || misaligned(out))
-    return fail(h, PKV_ERR_INVALID, "q/out must be 16-byte aligned device pointers");
-  TokenAttendArgs a;
-  std::memset(&a, 0, offsetof(TokenAttendArgs, item));
-  a.q = static_cast<const uint16_t*>(q);
-  a.out = static_cast<uint16_t*>(out);
-  a.q_stride = q_stride;
-  a.heads = h->H;
-  a.group = group;
-  a.pool = pool_view(h, layer);
-  a.window = window;
-  a.sinks = sinks;
-  a.scale_log2 = scale_log2;
-  a.err = h->d_err;
-  a.joined = h->d_joined;
-  int first[kMaxTokenBatch], last[kMaxTokenBatch];
-  for (int i = 0; i < n; ++i) {
-    const Stream& st = h->streams[sids[i]];
-    const TokenCounts& t = st.tok;
-    const int rows = row_off[i + 1] - row_off[i];
-    if (rows > t.len)
-      return fail(h, PKV_ERR_STATE, "stream %d: %d query rows, but only %d tokens", sids[i], rows, t.len);
-    if (rows == 0) continue;
-    if (!tok_holds(t, tok_window_lo(t.len - rows, window), sinks))
-      return fail(h, PKV_ERR_STATE, "stream %d: keys that its queries see are evicted", sids[i]);
-    TokenQuery& it = a.item[a.n++];
-    it.pages = st.d_pages;
-    it.row0 = row_off[i];
-    it.n = rows;
-    it.pos0 = t.len - rows;
-  }
-  // one launch per kernel: the streams' rows per KV head decide
-  cudaStream_t s = as_stream(cuda_stream);
-  const int n_items = a.n;
-  TokenQuery all[kMaxTokenBatch];
-  std::copy(a.item, a.item + n_items, all);
-  long long rows_sum = 0;
-  int n_small = 0;
-  for (int i = 0; i < n_items; ++i) {
-    const long long r = (long long)all[i].n * group;
-    if (r <= kTokenFewRows) rows_sum += r, ++n_small;
-  }
-  const int few_rows = rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
-  const int max_rows = token_tc_max_rows(h->fp8);
-  // one shape for all streams of the matrix-unit kernel, the largest's. On bf16 pages a second
-  // launch costs more than the lanes that stay idle: 2 .. 34 new tokens of 18 streams, 25.8
-  // against 39.1 us; a chunk of 1500 tokens beside 11 drafts of 20, group 4, 99 against 122 us.
-  // On E4M3 pages it depends: the first batch 36.6 against 56.6 us, the second 165 against 155
-  // us (there the 512-row shape leaves three of a draft's four lanes without rows).
-  int tc_rows = 128;
-  for (int i = 0; i < n_items; ++i)
-    while (tc_rows < max_rows && (long long)all[i].n * group > tc_rows) tc_rows *= 2;
-  for (const int shape : {few_rows, tc_rows}) {
-    const int below = shape == few_rows ? 0 : few_rows;
-    a.n = 0;
-    int most = 0;
-    for (int i = 0; i < n_items; ++i) {
-      const long long r = (long long)all[i].n * group;
-      if (r <= below || (r > shape && shape == few_rows)) continue;
-      a.item[a.n++] = all[i];
-      most = std::max(most, (int)std::min<long long>(r, shape));
-    }
-    if (a.n == 0) continue;
-    const bool few = shape == few_rows;
-    a.rows = !few ? shape : most <= 8 ? 8 : most > 16 && most <= 24 ? 24 : 16;
-    for (int i = 0; i < a.n; ++i) {
-      TokenQuery& it = a.item[i];
-      it.blocks = ceil_div((long long)it.n * group, a.rows);
-      const auto block_tiles = [&](int b) {
-        const int r0 = b * a.rows, r1 = std::min(r0 + a.rows, it.n * group) - 1;
-        return tok_tiles(it.pos0 + r0 / group, it.pos0 + r1 / group, window, sinks).n;
-      };
-      first[i] = block_tiles(0);
-      last[i] = block_tiles(it.blocks - 1);
-    }
-    const int room = std::min<int>(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
-    const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 12, 4, 8, room}
-                             : CtaCost{h->num_sms * token_tc_ctas_per_sm(h->fp8, shape), 10, 4, 8, room};
-    plan_splits(&a, first, last, cost);
-    bool split = false;
-    for (int i = 0; i < a.n; ++i) split = split || a.item[i].splits > 1;
-    if (split) {
-      a.part_o = h->d_token_part;
-      a.part_ml = h->d_token_part + (size_t)a.ctas * a.rows * kHeadDim;
-    }
-    PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, s));
-    if (split && !few) PKV_CUDA(h, launch_token_combine(a, s));
-  }
-  return PKV_OK;
+  if (row_off[n] > 0 && (!parents || (reinterpret_cast<uintptr_t>(parents) & 3u) != 0))
+    return fail(h, PKV_ERR_INVALID, "parents must be a 4-byte aligned device pointer");
+  for (int i = 0; i < n; ++i)
+    if (row_off[i + 1] - row_off[i] > kTreeNodes)
+      return fail(h, PKV_ERR_INVALID, "stream %d: a tree of %d nodes, more than %d", sids[i],
+                  row_off[i + 1] - row_off[i], kTreeNodes);
+  return attend_rows(h, q, q_heads, q_stride, row_off, sids, n, layer, static_cast<const int32_t*>(parents), out,
+                     window, sinks, sm_scale, cuda_stream);
 }
 
 pkv_status pkv_token_info(pkv_t h, int sid, int* n_tokens, int* evicted_from, int* evicted_to) {

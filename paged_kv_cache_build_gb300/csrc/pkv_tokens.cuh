@@ -74,6 +74,7 @@ template <int kStreams>
 struct TokenAttendArgsOf {
   const uint16_t* q;                // [rows][q_heads][64], rows q_stride elements apart
   uint16_t* out;                    // [rows][q_heads][64]
+  const int32_t* parents;           // trees: [rows]
   long long q_stride;
   int heads, group;                 // KV heads, query heads per KV head
   PoolView pool;
@@ -112,13 +113,26 @@ __device__ __forceinline__ int find_item(const Item* item, int n, int x) {
   return lo;
 }
 
+// Page of the list's entry pi; an append on layer 0 takes its new ones from the free stack.
+template <typename Args>
+__device__ __forceinline__ int page_of(const Args& a, const TokenRows& it, int pi) {
+  const int page = a.is_meta && pi >= it.old_pages
+                       ? a.free_stack[a.top - 1 - it.pop0 - (pi - it.old_pages)]
+                       : it.pages[pi];
+  if (page < 0 || page >= a.pool.pool_pages) {
+    atomicOr(a.err, kErrPageRange);
+    return -1;
+  }
+  return page;
+}
+
 // One CTA's share of an attention call.
 struct TokenWork {
   int item, block, head, split;
   int r0, rows;                     // its query rows in the (stream, head): first, count
   int p0, p1;                       // positions of the first and the last row
 };
-template <typename Args>
+template <bool TREE, typename Args>
 __device__ __forceinline__ TokenWork token_work(const Args& a, int cta) {
   TokenWork w;
   w.item = find_item<TokenQuery, &TokenQuery::cta0>(a.item, a.n, cta);
@@ -131,12 +145,77 @@ __device__ __forceinline__ TokenWork token_work(const Args& a, int cta) {
   w.block = t.blocks - 1 - x / a.heads;
   w.r0 = w.block * a.rows;
   w.rows = min(a.rows, t.n * a.group - w.r0);
-  w.p0 = t.pos0 + w.r0 / a.group;
-  w.p1 = t.pos0 + (w.r0 + w.rows - 1) / a.group;
+  // (a tree's nodes may be at any depth)
+  w.p0 = t.pos0 + (TREE ? 0 : w.r0 / a.group);
+  w.p1 = t.pos0 + (TREE ? t.n - 1 : (w.r0 + w.rows - 1) / a.group);
   return w;
 }
 
+// A batch's trees as one stream's CTA sees them: the parents, and what each of `rows` rows
+// (few rows: the CTA's; else every node) sees of the tree's slots.
+template <int kRows>
+struct TreeSmem {
+  uint64_t words[kRows][kTreeWords];
+  int depth[kRows];
+  int16_t parent[kTreeNodes];
+};
+// The stream's parents into shared memory, by `threads` threads; bad ones are noted and
+// taken for none. A barrier must follow.
+template <typename Tree>
+__device__ __forceinline__ void load_parents(Tree& tree, const int32_t* parents, int n, int tid, int threads,
+                                             int* err) {
+  for (int i = tid; i < n; i += threads) {
+    const int p = tree_parent(i, parents[i]);
+    if (p < -1) atomicOr(err, kErrTree);
+    tree.parent[i] = (int16_t)max(p, -1);
+  }
+}
+template <typename Tree>
+__device__ __forceinline__ void walk_tree(Tree& tree, int row, int node, int pos0, int window, int sinks) {
+#pragma unroll
+  for (int i = 0; i < kTreeWords; ++i) tree.words[row][i] = 0;
+  tree.depth[row] = tree_walk(tree.parent, node, pos0, window, sinks, tree.words[row]);
+}
+
+// A rotary append: what turns k and q (pkv_append_tokens_rotary).
+constexpr int kMaxAxes = 4;
+struct RotaryArgs {
+  const uint16_t* q;                // [rows][q_heads][64], rows q_stride elements apart
+  uint16_t* q_out;                  // [rows][q_heads][64]
+  long long q_stride;
+  int q_heads;                      // 0: no q
+  const int32_t* positions;         // [rows][axes]
+  int axes;
+  int distance;                     // between a pair's elements
+  unsigned long long turn[kHeadDim / 2];   // turns per unit of position, 2^64 to the turn
+  uint8_t axis[kHeadDim / 2];
+};
+
+// Accepted drafts of one stream: slots pos0 + kept[i] move to pos0 + i (i < m), and the list
+// entries start, start - 1, .. (count of them) go back on the free stack from top + base on.
+struct TokenKeepItem {
+  const int32_t* pages;
+  int pos0, n, m;                   // nodes, and how many stay
+  int kept0;                        // first of its entries in kept
+  int start, count, base;
+};
+template <int kStreams>
+struct TokenKeepArgsOf {
+  PoolView pool;                    // layer 0's
+  long long layer_bytes;
+  int layers;
+  const int32_t* kept;
+  int32_t* free_stack;
+  int top;
+  int n;
+  int* err;
+  TokenKeepItem item[kStreams];
+};
+using TokenKeepArgs = TokenKeepArgsOf<kMaxTokenBatch>;
+
 cudaError_t launch_token_append(const TokenRowsArgs& a, cudaStream_t s);
+cudaError_t launch_token_append_rotary(const TokenRowsArgs& a, const RotaryArgs& r, cudaStream_t s);
+cudaError_t launch_token_keep(const TokenKeepArgs& a, cudaStream_t s);
 cudaError_t launch_token_read(const TokenRowsArgs& a, cudaStream_t s);
 cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s);
 
