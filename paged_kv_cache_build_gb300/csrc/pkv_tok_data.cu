@@ -131,38 +131,6 @@ __device__ __forceinline__ void find_places(const TokenRowsArgs& a, Places& p) {
   __syncthreads();
 }
 
-// Eight bf16 values to E4M3 codes of v * 2^-e (fp8_row_exponent's e, of the row that 8
-// neighbouring lanes hold), with all arithmetic on pairs. The largest magnitude's bits
-// as an integer are E * 128 + mantissa, and e = E - 135, one more where the mantissa is
-// above 0.75: a carry. v * 2^-e is exact in bf16 but for values that no code reaches.
-__device__ __forceinline__ uint2 quantise8(const uint4& val, int* e_out) {
-  const uint32_t w[4] = {val.x, val.y, val.z, val.w};
-  uint32_t big = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t mag = w[i] & 0x7FFF7FFFu;
-    asm("max.bf16x2 %0, %0, %1;\n" : "+r"(big) : "r"(mag));
-  }
-  const unsigned group = 0xFFu << (threadIdx.x & 24);
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) {
-    const uint32_t other = __shfl_xor_sync(group, big, d);
-    asm("max.bf16x2 %0, %0, %1;\n" : "+r"(big) : "r"(other));
-  }
-  const int top = max((int)(big & 0xFFFFu), (int)(big >> 16));
-  const int e = top == 0 ? 0 : max(((top + 31) >> 7) - 135, -126);
-  *e_out = e;
-  const uint32_t s1 = (uint32_t)(127 - e) << 7, scale = s1 | (s1 << 16);   // 2^-e, -120 <= -e <= 126
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t x;
-    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(x) : "r"(w[i]), "r"(scale));
-    c[i] = fp8_pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
-  }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
-
 template <bool FP8>
 __global__ void __launch_bounds__(kWarps * 32) token_append_many_kernel(const __grid_constant__ TokenRowsArgs a) {
   __shared__ Places p;

@@ -41,13 +41,14 @@ namespace pkv {
 namespace {
 
 constexpr int kBN = kTokTile;
-// bf16 pages, 256 rows: two CTAs of two lanes an SM, so that one's start and end run beside
+// bf16 pages: two CTAs of two lanes an SM, so that one's start and end run beside
 // the other's products (prefill of 8192 tokens, 16 heads: 145 us, 152 with one CTA of 512
-// rows; ragged batch of 12 chunks 245 against 270 us). Else one CTA of four lanes: E4M3 pages,
-// which it converts once for all of them, and 128 rows, which take little time beside the
-// pages' (16 x 4031 keys: 32 us, 37 with two CTAs).
+// rows; ragged batch of 12 chunks 245 against 270 us; 128 rows, 32 streams of 2000 tokens 30
+// against 38 us with one CTA of four lanes, ragged ones of 4001 24 against 32, one of 32000 25
+// as well; but 16 even ones of 4031, a CTA for each of 128 SMs, 35 against 31 us). E4M3 pages:
+// one CTA of four lanes, which converts a tile once for all of them.
 template <int MT, bool FP8>
-constexpr int kLanes = FP8 || MT == 1 ? 4 : 2;
+constexpr int kLanes = FP8 ? 4 : 2;
 template <int MT, bool FP8>
 constexpr int kCtasPerSm = 4 / kLanes<MT, FP8>;
 template <int MT, bool FP8>
@@ -118,7 +119,7 @@ struct __align__(1024) TcSmem {
   const int32_t* pages;
   uint32_t tmem_base;
   int abort;
-  std::conditional_t<TREE, TreeSmem<kTreeNodes>, NoTree> tree;   // by node
+  std::conditional_t<TREE, TreeSmem<(MT == 1 ? 128 : kTreeNodes)>, NoTree> tree;   // by node, from the CTA's first
 };
 
 __device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float s, float c) {
@@ -431,23 +432,23 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     const int wq = warp & 3, r = wq * 32 + lane;           // row of the lane's 128
     const LaneRows rows = lane_rows<TREE>(a, sm.work, sm.pos0, m_blk);
     const int node = (w.r0 + 128 * m_blk + min(r, max(rows.n, 1) - 1)) / G;
-    const int p = sm.pos0 + node;
+    const int p = sm.pos0 + node, node0 = w.r0 / G;
     if constexpr (TREE) {
       // what the nodes see of the tree, if the CTA has a tile that some of them do not see whole
       if (a.window > 0 || (sm.j1 > sm.j0 && tok_tile(sm.tiles, sm.j1 - 1) * kBN + kBN > sm.pos0)) {
         constexpr int kMen = kSoftmaxWarps<MT, FP8> * 32;
-        const int nodes = w.p1 - sm.pos0 + 1;
-        load_parents(sm.tree, a.parents + sm.row0, nodes, threadIdx.x, kMen, a.err);
+        load_parents(sm.tree, a.parents + sm.row0, w.p1 - sm.pos0 + 1, threadIdx.x, kMen, a.err);
         __syncwarp();
         asm volatile("bar.sync 2, %0;\n" ::"n"(kMen) : "memory");
-        for (int i = threadIdx.x; i < nodes; i += kMen) walk_tree(sm.tree, i, i, sm.pos0, a.window, a.sinks);
+        const int nodes = (w.r0 + w.rows - 1) / G - node0 + 1;
+        for (int i = threadIdx.x; i < nodes; i += kMen) walk_tree(sm.tree, i, node0 + i, sm.pos0, a.window, a.sinks);
         __syncwarp();
         asm volatile("bar.sync 2, %0;\n" ::"n"(kMen) : "memory");
       }
     }
     const auto row_bits = [&](int tile) -> uint64_t {
       if constexpr (TREE)
-        return tree_mask(tile * kBN, sm.pos0, sm.tree.depth[node], sm.tree.words[node], a.window, a.sinks);
+        return tree_mask(tile * kBN, sm.pos0, sm.tree.depth[node - node0], sm.tree.words[node - node0], a.window, a.sinks);
       else
         return tok_mask(tile * kBN, p, a.window, a.sinks);
     };
@@ -693,7 +694,12 @@ cudaError_t launch_tc_rows(const TokenAttendArgs& a, cudaStream_t s) {
 
 int token_tc_max_rows(bool fp8) { return fp8 ? 512 : 256; }
 
-int token_tc_ctas_per_sm(bool fp8, int rows) { return !fp8 && rows == 256 ? kCtasPerSm<2, false> : 1; }
+int token_tc_ctas_per_sm(bool fp8, int rows) { return fp8 ? 1 : rows == 256 ? kCtasPerSm<2, false> : kCtasPerSm<1, false>; }
+
+double token_tc_tile_us(bool fp8, int rows) {
+  if (fp8) return rows == 128 ? 0.72 : rows == 256 ? 0.79 : 1.6;
+  return rows == 128 ? 0.65 : 1.05;
+}
 
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s) {
   return a.parents ? launch_tc_rows<true>(a, s) : launch_tc_rows<false>(a, s);

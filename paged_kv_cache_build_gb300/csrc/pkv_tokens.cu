@@ -75,6 +75,7 @@ void rows_args(pkv_t h, int layer, TokenRowsArgs* a) {
 // take 0.25 us a tile and 3 us a CTA, the matrix-unit kernel 0.5 us and 5 us.
 struct CtaCost {
   int slots;                     // CTAs that run at once
+  double tile;                   // us
   int fixed, join;
   int min_piece;                 // tiles below which a range is not cut
   int max_ctas;                  // whose partial results the scratch holds
@@ -82,8 +83,9 @@ struct CtaCost {
 
 // Splits of the items' key ranges over CTAs, given the tiles that an item's first
 // and last block see. All ranges are cut into pieces of one length (at most); of the
-// lengths most/1, most/2, .. the one whose waves of CTAs are estimated to end first.
-void plan_splits(TokenAttendArgs* a, const int* first, const int* last, const CtaCost& c) {
+// lengths most/1, most/2, .. the one whose waves of CTAs are estimated to end first. Returns
+// the estimate in us.
+double plan_splits(TokenAttendArgs* a, const int* first, const int* last, const CtaCost& c) {
   int most = 1;
   for (int i = 0; i < a->n; ++i) most = std::max({most, first[i], last[i]});
   int best = most;
@@ -114,6 +116,50 @@ void plan_splits(TokenAttendArgs* a, const int* first, const int* last, const Ct
     cta += t.blocks * a->heads * t.splits;
   }
   a->ctas = cta;
+  return best_t * c.tile;
+}
+
+// The shares of an attention call in blocks of a kernel's shape (query rows a CTA) with their
+// splits; the estimate in us.
+double plan_shape(pkv_t h, TokenAttendArgs* a, bool few, int shape) {
+  a->rows = shape;
+  int first[kMaxTokenBatch], last[kMaxTokenBatch];
+  for (int i = 0; i < a->n; ++i) {
+    TokenQuery& it = a->item[i];
+    it.blocks = ceil_div((long long)it.n * a->group, shape);
+    const auto block_tiles = [&](int b) {
+      if (a->parents) return tok_tiles(it.pos0, it.pos0 + it.n - 1, a->window, a->sinks).n;
+      const int r0 = b * shape, r1 = std::min(r0 + shape, it.n * a->group) - 1;
+      return tok_tiles(it.pos0 + r0 / a->group, it.pos0 + r1 / a->group, a->window, a->sinks).n;
+    };
+    first[i] = block_tiles(0);
+    last[i] = block_tiles(it.blocks - 1);
+  }
+  const int room = std::min<int>(kTokenScratchBytes / (shape * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
+  const CtaCost cost =
+      few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 0.25, 12, 4, 8, room}
+          : CtaCost{h->num_sms * token_tc_ctas_per_sm(h->fp8, shape), token_tc_tile_us(h->fp8, shape), 10, 4, 8, room};
+  return plan_splits(a, first, last, cost);
+}
+
+// Plans the matrix-unit kernel for a's streams: the shape of its CTAs, and the splits.
+double plan_tc(pkv_t h, TokenAttendArgs* a) {
+  long long most = 0;
+  for (int i = 0; i < a->n; ++i) most = std::max(most, (long long)a->item[i].n * a->group);
+  // one shape for all streams, the largest's: a second launch costs more than the lanes that
+  // stay idle
+  int shape = 128;
+  while (shape < token_tc_max_rows(h->fp8) && most > shape) shape *= 2;
+  // bf16 pages: blocks of 128 read a key once for fewer rows, but leave fewer lanes without rows
+  // and end more evenly. Trees of up to 64 nodes, group 4, 256 / 128 rows: 32 streams of up to 2001
+  // tokens 44 / 36 us, 8 of 4001 27 / 21 us, 16 of them 36 / 39 us; one of 131072 tokens, group 8,
+  // 140 / 150 us.
+  if (!h->fp8 && shape == 256) {
+    const double narrow = plan_shape(h, a, false, 128), wide = plan_shape(h, a, false, 256);
+    if (wide <= narrow) return wide;
+    shape = 128;
+  }
+  return plan_shape(h, a, false, shape);
 }
 
 // The rotation as the kernel takes it: whole turns do not matter for whole positions, so a
@@ -252,7 +298,6 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
   a.scale_log2 = scale_log2;
   a.err = h->d_err;
   a.joined = h->d_joined;
-  int first[kMaxTokenBatch], last[kMaxTokenBatch];
   for (int i = 0; i < n; ++i) {
     const Stream& st = h->streams[sids[i]];
     const TokenCounts& t = st.tok;
@@ -268,65 +313,63 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
     it.n = rows;
     it.pos0 = t.len - rows;
   }
-  // one launch per kernel: the streams' rows per KV head decide
+  // the streams' rows per KV head decide on the kernel
   cudaStream_t s = as_stream(cuda_stream);
   const int n_items = a.n;
-  TokenQuery all[kMaxTokenBatch];
-  std::copy(a.item, a.item + n_items, all);
-  long long rows_sum = 0;
+  long long rows_sum = 0, most = 0;
   int n_small = 0;
   for (int i = 0; i < n_items; ++i) {
-    const long long r = (long long)all[i].n * group;
+    const long long r = (long long)a.item[i].n * group;
     if (r <= kTokenFewRows) rows_sum += r, ++n_small;
   }
   const int few_rows = rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
-  const int max_rows = token_tc_max_rows(h->fp8);
-  // one shape for all streams of the matrix-unit kernel, the largest's. On bf16 pages a second
-  // launch costs more than the lanes that stay idle: 2 .. 34 new tokens of 18 streams, 25.8
-  // against 39.1 us; a chunk of 1500 tokens beside 11 drafts of 20, group 4, 99 against 122 us.
-  // On E4M3 pages it depends: the first batch 36.6 against 56.6 us, the second 165 against 155
-  // us (there the 512-row shape leaves three of a draft's four lanes without rows).
-  int tc_rows = 128;
-  for (int i = 0; i < n_items; ++i)
-    while (tc_rows < max_rows && (long long)all[i].n * group > tc_rows) tc_rows *= 2;
-  for (const int shape : {few_rows, tc_rows}) {
-    const int below = shape == few_rows ? 0 : few_rows;
-    a.n = 0;
-    int most = 0;
-    for (int i = 0; i < n_items; ++i) {
-      const long long r = (long long)all[i].n * group;
-      if (r <= below || (r > shape && shape == few_rows)) continue;
-      a.item[a.n++] = all[i];
-      most = std::max(most, (int)std::min<long long>(r, shape));
-    }
-    if (a.n == 0) continue;
-    const bool few = shape == few_rows;
-    a.rows = !few ? shape : most <= 8 ? 8 : most > 16 && most <= 24 ? 24 : 16;
-    for (int i = 0; i < a.n; ++i) {
-      TokenQuery& it = a.item[i];
-      it.blocks = ceil_div((long long)it.n * group, a.rows);
-      const auto block_tiles = [&](int b) {
-        if (parents) return tok_tiles(it.pos0, it.pos0 + it.n - 1, window, sinks).n;
-        const int r0 = b * a.rows, r1 = std::min(r0 + a.rows, it.n * group) - 1;
-        return tok_tiles(it.pos0 + r0 / group, it.pos0 + r1 / group, window, sinks).n;
-      };
-      first[i] = block_tiles(0);
-      last[i] = block_tiles(it.blocks - 1);
-    }
-    const int room = std::min<int>(kTokenScratchBytes / (a.rows * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
-    const CtaCost cost = few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 12, 4, 8, room}
-                             : CtaCost{h->num_sms * token_tc_ctas_per_sm(h->fp8, shape), 10, 4, 8, room};
-    plan_splits(&a, first, last, cost);
-    bool split = false;
-    for (int i = 0; i < a.n; ++i) split = split || a.item[i].splits > 1;
-    if (split) {
-      a.part_o = h->d_token_part;
-      a.part_ml = h->d_token_part + (size_t)a.ctas * a.rows * kHeadDim;
-    }
-    PKV_CUDA(h, few ? launch_token_few(a, s) : launch_token_tc(a, s));
-    if (split && !few) PKV_CUDA(h, launch_token_combine(a, s));
+  n_small = 0;
+  for (int i = 0; i < n_items; ++i) {
+    const long long r = (long long)a.item[i].n * group;
+    if (r <= few_rows) ++n_small, most = std::max(most, r);
   }
-  return PKV_OK;
+  const auto launch_tc = [&](const TokenAttendArgs& t) -> pkv_status {
+    PKV_CUDA(h, launch_token_tc(t, s));
+    if (t.part_o) PKV_CUDA(h, launch_token_combine(t, s));
+    return PKV_OK;
+  };
+  const auto give_parts = [&](TokenAttendArgs* t) {
+    bool split = false;
+    for (int i = 0; i < t->n; ++i) split = split || t->item[i].splits > 1;
+    t->part_o = split ? h->d_token_part : nullptr;
+    t->part_ml = split ? h->d_token_part + (size_t)t->ctas * t->rows * kHeadDim : nullptr;
+  };
+  if (n_small == 0) {
+    plan_tc(h, &a);
+    give_parts(&a);
+    return launch_tc(a);
+  }
+  const int few_shape = most <= 8 ? 8 : most > 16 && most <= 24 ? 24 : 16;
+  if (n_small == n_items) {
+    plan_shape(h, &a, true, few_shape);
+    give_parts(&a);
+    PKV_CUDA(h, launch_token_few(a, s));
+    return PKV_OK;
+  }
+  // Both kinds: a launch for each, one behind the other, or all in the matrix-unit kernel, as the
+  // estimates say (and 3 us for the launch). Ragged trees of up to 32 nodes, group 4: 16 streams of up to
+  // 4001 tokens 35 us in two launches, 25 in one; 32 of 4000 55 and 45; 4 of 8000 29 and 20 us; on
+  // E4M3 pages 57 and 45, 90 and 77, 38 and 26 us.
+  TokenAttendArgs small = a, large = a;
+  small.n = large.n = 0;
+  for (int i = 0; i < n_items; ++i) {
+    TokenAttendArgs& t = (long long)a.item[i].n * group <= few_rows ? small : large;
+    t.item[t.n++] = a.item[i];
+  }
+  const double apart = plan_shape(h, &small, true, few_shape) + plan_tc(h, &large) + 3.0;
+  if (plan_tc(h, &a) <= apart) {
+    give_parts(&a);
+    return launch_tc(a);
+  }
+  give_parts(&small);
+  PKV_CUDA(h, launch_token_few(small, s));
+  give_parts(&large);
+  return launch_tc(large);
 }
 
 }  // namespace

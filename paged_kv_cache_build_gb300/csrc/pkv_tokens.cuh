@@ -126,6 +126,38 @@ __device__ __forceinline__ int page_of(const Args& a, const TokenRows& it, int p
   return page;
 }
 
+// Eight bf16 values to E4M3 codes of v * 2^-e (fp8_row_exponent's e, of the row that 8
+// neighbouring lanes hold), with all arithmetic on pairs. The largest magnitude's bits
+// as an integer are E * 128 + mantissa, and e = E - 135, one more where the mantissa is
+// above 0.75: a carry. v * 2^-e is exact in bf16 but for values that no code reaches.
+__device__ __forceinline__ uint2 quantise8(const uint4& val, int* e_out) {
+  const uint32_t w[4] = {val.x, val.y, val.z, val.w};
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t mag = w[i] & 0x7FFF7FFFu;
+    asm("max.bf16x2 %0, %0, %1;\n" : "+r"(big) : "r"(mag));
+  }
+  const unsigned group = 0xFFu << (threadIdx.x & 24);
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) {
+    const uint32_t other = __shfl_xor_sync(group, big, d);
+    asm("max.bf16x2 %0, %0, %1;\n" : "+r"(big) : "r"(other));
+  }
+  const int top = max((int)(big & 0xFFFFu), (int)(big >> 16));
+  const int e = top == 0 ? 0 : max(((top + 31) >> 7) - 135, -126);
+  *e_out = e;
+  const uint32_t s1 = (uint32_t)(127 - e) << 7, scale = s1 | (s1 << 16);   // 2^-e, -120 <= -e <= 126
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x;
+    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(x) : "r"(w[i]), "r"(scale));
+    c[i] = fp8_pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
 // One CTA's share of an attention call.
 struct TokenWork {
   int item, block, head, split;
@@ -235,6 +267,8 @@ int token_few_ctas_per_sm();
 // Attention of 128, 256 or (on E4M3 pages) 512 query rows per CTA (a.rows).
 int token_tc_max_rows(bool fp8);
 int token_tc_ctas_per_sm(bool fp8, int rows);
+// What a 64-slot tile takes a CTA of it, in us, beside the SM's others.
+double token_tc_tile_us(bool fp8, int rows);
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s);
 // Joins the splits of the items that have several (launch_token_few does so itself).
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s);
