@@ -14,7 +14,8 @@
 // E4M3 pages: codes have 4 significant bits, so that an error of fp32's size in a value
 // next to the border of two codes would show as a whole step. Values are rotated in fp32, and
 // those whose code (or a row whose exponent) fp32's error could change are rotated again in
-// doubles: one value in 30,000.
+// doubles, one value in some 10,000: by a lane each, behind a warp's K planes, because one takes
+// 1 to 2 us (a row of them in place 20 us, and the launch waited for it).
 //
 // Bounds: memory traffic. A warp takes four tokens, whose sines and cosines its lanes hold in
 // registers, and goes over planes (heads of K, q and V) of 128 bytes a token, the next ones on
@@ -29,8 +30,8 @@ namespace pkv {
 namespace {
 
 constexpr int kQuad = 4;             // tokens of a warp
-constexpr int kWarps = 8;
-constexpr int kFlight = 4;           // planes on their way
+constexpr int kWarps = 4;
+constexpr int kFlight = 8;           // planes on their way
 constexpr int kPairs = kHeadDim / 2;
 
 // Element i of chunk c: the pair that it belongs to, and whether it is its second.
@@ -38,10 +39,6 @@ __device__ __forceinline__ int pair_of(int c, int i, int distance, bool* second)
   const int e = 8 * c + i, in = e & (2 * distance - 1);
   *second = in >= distance;
   return (e - in) / 2 + (in & (distance - 1));
-}
-
-__device__ __forceinline__ unsigned long long phase_of(const RotaryArgs& r, const int32_t* position, int pair) {
-  return (unsigned long long)(long long)position[r.axis[pair]] * r.turn[pair];
 }
 
 // The chunk that holds the other elements of the lane's eight pairs (as many bf16 values).
@@ -66,11 +63,22 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
   }
 }
 
-// fp8_row_exponent of a largest magnitude by its bits: one more where the fraction is above
-// 0.75, a carry.
-__device__ __forceinline__ int row_exponent(float amax) {
-  const int e = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 135;
-  return amax > 0.f ? min(max(e, -126), 126) : 0;
+// (x0, x1) y + (z0, z1), and without z, in one instruction.
+__device__ __forceinline__ float2 fma2(float x0, float x1, float2 y, float2 z) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x0), "f"(x1), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float x0, float x1, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x0), "f"(x1), "f"(y.x), "f"(y.y));
+  return r;
 }
 
 // One code of a double within 448, rounded once. (It goes to fp32 first: to the neighbour on its
@@ -82,54 +90,66 @@ __device__ __forceinline__ uint32_t code_of(double v) {
     z = __uint_as_float(fabs(v) > fabs((double)z) ? b + 1u : b - 1u);
   return fp8_pack2(z, 0.f) & 0xFFu;
 }
+__device__ __forceinline__ double power_of_two(int e) { return __hiloint2double((1023 + e) << 20, 0); }
 
-// A rotated row (8 lanes') whose codes fp32 does not settle: the lane's elements whose code may
-// differ, or all if the exponent is open, again in doubles. Called by the 8 lanes together.
-__device__ __noinline__ uint2 settle(const RotaryArgs& r, const int32_t* position, int c, uint4 vx, uint4 vp, uint2 differ,
-                                     bool open, uint2 codes, int* e_io) {
-  float x[8], p[8];
-  unpack(vx, x);
-  unpack(vp, p);
-  const auto value = [&](int i) {
-    bool second;
-    const int pair = pair_of(c, i, r.distance, &second);
-    const unsigned long long phase = phase_of(r, position, pair);
-    if (phase == 0) return (double)x[i];
-    double sn, cs;
-    sincospi((double)(long long)phase * 0x1p-63, &sn, &cs);
-    return fma((double)x[i], cs, (second ? sn : -sn) * (double)p[i]);
-  };
-  int e = *e_io;
-  if (open) {
-    double big = 0.0;
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) big = fmax(big, fabs(value(i)));
-    const unsigned group = 0xFFu << (threadIdx.x & 24);
-    for (int d = 1; d < 8; d <<= 1) big = fmax(big, __shfl_xor_sync(group, big, d));
-    e = 0;
-    if (big > 0.0) {
-      const double f = frexp(big, &e);
-      e = min(max(e - 9 + (f > 0.875 ? 1 : 0), -126), 126);
-    }
-    *e_io = e;
-    differ.x = differ.y = ~0u;
-  }
-  unsigned long long all = codes.x | (unsigned long long)codes.y << 32;
-  const unsigned long long which = differ.x | (unsigned long long)differ.y << 32;
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    if (((which >> (8 * i)) & 0xFFull) == 0) continue;
-    const unsigned long long code = code_of(ldexp(value(i), -e));
-    all = (all & ~(0xFFull << (8 * i))) | code << (8 * i);
-  }
-  return make_uint2((uint32_t)all, (uint32_t)(all >> 32));
+// Cosine and sine of an angle of phase / 2^64 turns: whole quarters aside, their Taylor series
+// within an eighth of a turn, whose next terms are 2^-60 and less. (In place of sincospi, of which a
+// call's first use costs a microsecond, its code and constants being nowhere near.)
+__device__ __forceinline__ void turn_exactly(unsigned long long phase, double* cs, double* sn) {
+  const unsigned quarter = (unsigned)((phase + (1ull << 61)) >> 62) & 3u;
+  const double a = (double)(long long)(phase - ((unsigned long long)quarter << 62)) * (6.283185307179586 * 0x1p-64);
+  const double q = a * a;
+  double s = 1.0 / 355687428096000.0, c = 1.0 / 20922789888000.0;   // 1 / 17!, 1 / 16!
+  s = fma(s, q, -1.0 / 1307674368000.0);
+  c = fma(c, q, -1.0 / 87178291200.0);
+  s = fma(s, q, 1.0 / 6227020800.0);
+  c = fma(c, q, 1.0 / 479001600.0);
+  s = fma(s, q, -1.0 / 39916800.0);
+  c = fma(c, q, -1.0 / 3628800.0);
+  s = fma(s, q, 1.0 / 362880.0);
+  c = fma(c, q, 1.0 / 40320.0);
+  s = fma(s, q, -1.0 / 5040.0);
+  c = fma(c, q, -1.0 / 720.0);
+  s = fma(s, q, 1.0 / 120.0);
+  c = fma(c, q, 1.0 / 24.0);
+  s = fma(s, q, -1.0 / 6.0);
+  c = fma(c, q, -0.5);
+  s = fma(s * q, a, a);
+  c = fma(c, q, 1.0);
+  const double x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
+  *cs = quarter == 1u || quarter == 2u ? -x : x;
+  *sn = quarter & 2u ? -y : y;
 }
 
-template <bool FP8, typename Args>
-__global__ void __launch_bounds__(kWarps * 32, FP8 ? 3 : 4)
+// Element e of a row as rotated, in doubles: x is its value, p its pair's other one.
+__device__ __noinline__ double turned_exactly(const RotaryArgs& r, const int32_t* position, int e, float x, float p) {
+  bool second;
+  const int pair = pair_of(0, e, r.distance, &second);
+  const unsigned long long phase = (unsigned long long)(long long)position[r.axis[pair]] * r.turn[pair];
+  if (phase == 0) return (double)x;
+  double sn, cs;
+  turn_exactly(phase, &cs, &sn);
+  return fma((double)x, cs, (second ? sn : -sn) * (double)p);
+}
+
+// A value whose code fp32 leaves open, kept until the warp's K planes are done: then a lane each.
+struct Open {
+  uint32_t values;                   // bf16: the element's (low) and its pair's other one
+  int plane;
+  uint8_t token, element;            // of the warp's; of the row
+  int8_t exponent;
+};
+constexpr int kOpen = 64;            // of a warp (what does not fit is settled at once)
+
+template <bool FP8, int U, typename Args>
+__global__ void __launch_bounds__(kWarps * 32, FP8 ? 5 : 8)
     token_append_rotary_kernel(const __grid_constant__ Args a, const __grid_constant__ RotaryArgs r, int shares) {
-  // [token][pair] of each warp; a token's row is 17 float4 apart
+  // each warp's: cosines and sines by [token][pair], and planes on their way, a lane's part in
+  // its own place
   __shared__ __align__(16) float2 turns[kWarps][kQuad][kPairs + 2];
+  __shared__ uint4 ring[kWarps][kFlight][32];
+  __shared__ Open open_list[FP8 ? kWarps : 1][FP8 ? kOpen : 1];
+  __shared__ int n_open[kWarps];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane & 7, q4 = lane >> 3;
@@ -137,22 +157,34 @@ __global__ void __launch_bounds__(kWarps * 32, FP8 ? 3 : 4)
   const long long w = (long long)blockIdx.x * kWarps + warp;
   const long long unit = w / shares * kQuad + q4;
   if (unit - q4 >= a.units) return;              // the warp's tokens
+  if (lane == 0) n_open[warp] = 0;
   const int share = (int)(w % shares);
   const int h0 = (int)((long long)planes * share / shares), h1 = (int)((long long)planes * (share + 1) / shares);
   const bool there = unit < a.units;
   const TokenRows& it = a.item[find_item<TokenRows, &TokenRows::unit0>(a.item, a.n, (int)min(unit, a.units - 1ll))];
   const int i0 = there ? (int)unit - it.unit0 : it.n, pos = it.pos0 + i0;
   const bool row = i0 < it.n;                    // else a slot to be zeroed, or nothing
-  const long long src = it.row0 + i0;
-  // planes: K, q, V; the last ones do not turn
+  const long long src = row ? it.row0 + i0 : 0;
+  // Planes: K, q, V; the last ones do not turn. Each lane has kFlight of its 16 bytes on their way.
   const int turning = H + r.q_heads;
-  const auto source = [&](int hh) {
-    return (hh < H         ? a.k + src * a.k_stride + hh * kHeadDim
-            : hh < turning ? r.q + src * r.q_stride + (hh - H) * kHeadDim
-                           : a.v + src * a.v_stride + (hh - turning) * kHeadDim) + 8 * c;
+  const uint16_t* from = (h0 < H         ? a.k + src * a.k_stride + h0 * kHeadDim
+                          : h0 < turning ? r.q + src * r.q_stride + (h0 - H) * kHeadDim
+                                         : a.v + src * a.v_stride + (h0 - turning) * kHeadDim) + 8 * c;
+  const uint32_t place = smem_u32(&ring[warp][0][lane]);
+  int next = h0;
+  const auto fetch = [&]() {
+    if (next < h1) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(place + (next - h0) % kFlight * 512),
+                   "l"(row ? from : a.k), "r"(row ? 16 : 0)
+                   : "memory");
+      from += kHeadDim;
+      if (++next == H) from = r.q + src * r.q_stride + 8 * c;
+      if (next == turning) from = a.v + src * a.v_stride + 8 * c;
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
   };
-  // (the rows' first plane comes while the angles are worked out)
-  if (row) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(source(h0)));
+#pragma unroll 1
+  for (int u = 0; u < kFlight; ++u) fetch();
   // the token's place in plane 0 of its page
   int slot = 0, page = -1;
   if (there && (h0 < H || h1 > turning)) {
@@ -162,7 +194,11 @@ __global__ void __launch_bounds__(kWarps * 32, FP8 ? 3 : 4)
     if (a.is_meta && page >= 0 && slot == 0 && h0 == 0 && c == 0) it.pages[pi] = page;
   }
   const int32_t* const position = r.positions + src * r.axes;
-  float cs[8], sn[8];                            // sn with its element's sign (first of a pair: -)
+  float2 cs[4], sn[4];                           // sn with its element's sign (first of a pair: -)
+  // fp32 is off by less than 2^-21 (|x| + |p|): an angle rounded to 2^-25 half turns, a sine
+  // and a cosine off by 2^-24, and two roundings. Angles of 0 turn exactly, which matters: such
+  // values may lie on the border of two codes, as many of a text's first token do.
+  float off = 0.f;
   if (h0 < turning) {
     // a pair a lane, for each token; then every lane takes its elements' ones
     const unsigned long long turn = r.turn[lane];
@@ -172,8 +208,9 @@ __global__ void __launch_bounds__(kWarps * 32, FP8 ? 3 : 4)
       const bool is_row = __shfl_sync(0xffffffffu, (int)row, 8 * t) != 0;
       const long long at = __shfl_sync(0xffffffffu, src, 8 * t) * r.axes + axis;
       const unsigned long long phase = is_row ? (unsigned long long)(long long)r.positions[at] * turn : 0ull;
-      float2 x;
+      float2 x;                                  // (a cosine of 2 marks an angle of exactly 0)
       sincospif((float)(int)(phase >> 32) * 0x1p-31f, &x.y, &x.x);
+      if (phase == 0) x.x = 2.f;
       turns[warp][t][lane] = x;
     }
     __syncwarp();
@@ -181,113 +218,221 @@ __global__ void __launch_bounds__(kWarps * 32, FP8 ? 3 : 4)
     for (int i = 0; i < 8; ++i) {
       bool second;
       const float2 x = turns[warp][q4][pair_of(c, i, r.distance, &second)];
-      cs[i] = x.x;
-      sn[i] = second ? x.y : -x.y;
+      if (x.x != 2.f) off = 0x1p-21f;
+      const float y = second ? x.y : -x.y;
+      if (i & 1) cs[i >> 1].y = fminf(x.x, 1.f), sn[i >> 1].y = y;
+      else cs[i >> 1].x = fminf(x.x, 1.f), sn[i >> 1].x = y;
     }
   }
-  // Planes hh0 .. hh1 - 1, consecutive rows of `rows`, kFlight on their way at a time.
-  const auto go = [&](int hh0, int hh1, const uint16_t* rows, auto&& take) {
-    for (int hb = hh0; hb < hh1; hb += kFlight) {
-      uint4 val[kFlight];
+  uint8_t* const base = reinterpret_cast<uint8_t*>(a.pool.base) + (long long)max(page, 0) * a.pool.page_bytes;
+  const long long plane = (long long)Ps * (FP8 ? kHeadDim + 1 : 2 * kHeadDim);
+  // where the lane's part of the next plane goes: in the page, or (q) in q_out
+  uint8_t* to = base + (h0 < H ? h0 : max(h0 - r.q_heads, H)) * plane +
+                (FP8 ? fp8_code_off(H, Ps, 0, 0, slot) + 8 * c
+                     : (long long)slot * kHeadDim * 2 + (swizzle_chunk(slot, c) << 4));
+  const long long exp = fp8_exp_off(H, Ps, 0, 0, slot) - fp8_code_off(H, Ps, 0, 0, slot);   // (of chunk 0)
+  uint16_t* q_to = r.q_out + (src * r.q_heads + max(h0 - H, 0)) * kHeadDim + 8 * c;
+  // U planes at a time, two where a warp has many, so that their chains of shuffles run side by
+  // side; `second`: there are two.
+  int at = 0;
+  const auto take = [&](uint4 (&v)[U], bool second) {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(kFlight - U) : "memory");
 #pragma unroll
-      for (int u = 0; u < kFlight; ++u) {
-        val[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (row && hb + u < hh1) val[u] = *reinterpret_cast<const uint4*>(rows + (hb + u - hh0) * kHeadDim);
-      }
-#pragma unroll
-      for (int u = 0; u < kFlight; ++u)
-        if (hb + u < hh1) take(hb + u, val[u]);
+    for (int u = 0; u < U; ++u) {
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                   : "=r"(v[u].x), "=r"(v[u].y), "=r"(v[u].z), "=r"(v[u].w)
+                   : "r"(place + (at + u) % kFlight * 512)
+                   : "memory");
+      if (u == 1 && !second) v[u] = make_uint4(0u, 0u, 0u, 0u);
     }
+    at += second ? 2 : 1;
+    fetch();
+    if (second) fetch();
   };
-  const auto turned = [&](const float (&x)[8], const float (&p)[8], float (&y)[8]) {
+  const auto turned = [&](const float (&x)[8], const float (&p)[8], float2 (&y)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = fmaf(x[i], cs[i], p[i] * sn[i]);
+    for (int i = 0; i < 4; ++i)
+      y[i] = fma2(x[2 * i], x[2 * i + 1], cs[i], mul2(p[2 * i], p[2 * i + 1], sn[i]));
   };
   const auto rounded = [&](const uint4& v) {
     const uint4 vp = partners(v, r.distance);
-    float x[8], p[8], y[8];
+    float x[8], p[8];
+    float2 y[4];
     unpack(v, x);
     unpack(vp, p);
     turned(x, p, y);
-    return make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    return make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[1].x, y[1].y), pack_bf16(y[2].x, y[2].y),
+                      pack_bf16(y[3].x, y[3].y));
   };
-  uint8_t* const base = reinterpret_cast<uint8_t*>(a.pool.base) + (long long)max(page, 0) * a.pool.page_bytes;
-  const long long plane = (long long)Ps * (FP8 ? kHeadDim + 1 : 2 * kHeadDim);
-  uint8_t* const code = base + (FP8 ? fp8_code_off(H, Ps, 0, 0, slot) + 8 * c
-                                    : (long long)slot * kHeadDim * 2 + (swizzle_chunk(slot, c) << 4));
-  const long long exp = fp8_exp_off(H, Ps, 0, 0, slot) - fp8_code_off(H, Ps, 0, 0, slot);   // (of chunk 0)
-  const auto store8 = [&](int plane_no, const uint2& codes, int e) {
-    if (page < 0) return;
-    uint8_t* const to = code + plane_no * plane;
-    *reinterpret_cast<uint2*>(to) = codes;
-    if (c == 0) to[exp] = (uint8_t)(int8_t)e;
+  const auto store8 = [&](uint8_t* dst, const uint2& codes, int e) {
+    *reinterpret_cast<uint2*>(dst) = codes;
+    if (c == 0) dst[exp] = (uint8_t)(int8_t)e;
   };
-
-  go(h0, min(h1, H), source(h0), [&](int hh, const uint4& v) {
+  int hh = h0;
+#pragma unroll 1
+  for (const int end = min(h1, H); hh < end; hh += U, to += U * plane) {
+    uint4 v[U];
+    const bool second = U == 2 && hh + 1 < end;
+    take(v, second);
     if constexpr (!FP8) {
-      const uint4 out = rounded(v);
-      if (page >= 0) *reinterpret_cast<uint4*>(code + hh * plane) = out;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint4 out = rounded(v[u]);
+        if (page >= 0 && (u == 0 || second)) *reinterpret_cast<uint4*>(to + u * plane) = out;
+      }
     } else {
-      const uint4 vp = partners(v, r.distance);
-      float x[8], p[8], y[8];
-      unpack(v, x);
-      unpack(vp, p);
-      turned(x, p, y);
-      // fp32 is off by less than 2^-21 (|x| + |p|): an angle rounded to 2^-25 half turns, a sine
-      // and a cosine off by 2^-24, and two roundings
-      constexpr float kOff = 0x1p-21f;
-      float big = 0.f, most = 0.f;
+      float x[U][8], p[U][8], big[U];
+      float2 y[U][4];
+      int e[U];
+      unsigned open = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        big = fmaxf(big, fabsf(y[i]));
-        most = fmaxf(most, fabsf(x[i]));
+      for (int u = 0; u < U; ++u) {
+        unpack(v[u], x[u]);
+        unpack(partners(v[u], r.distance), p[u]);
+        turned(x[u], p[u], y[u]);
+        big[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) big[u] = fmaxf(big[u], fmaxf(fabsf(y[u][i].x), fabsf(y[u][i].y)));
+#pragma unroll
+        for (int s = 1; s < 8; s <<= 1) big[u] = fmaxf(big[u], __shfl_xor_sync(0xffffffffu, big[u], s));
+        // The exponent (fp8_row_exponent): the bits' one, one more where the fraction is above
+        // 0.75, a carry. A pair keeps its length, so |x| + |p| is at most twice the larger of its
+        // two values: big is off by 2^-20 of it, 16 of its last places; 20 from a carry it is open.
+        const uint32_t b = __float_as_uint(big[u]) + 0x1FFFFFu;
+        e[u] = big[u] > 0.f ? max((int)(b >> 23) - 135, -126) : 0;
+        open |= (unsigned)(((b + 20u) & 0x7FFFFFu) < 41u) << u;
+      }
+      if (__any_sync(0xffffffffu, open != 0)) {
+        // one value in doubles, or few, says whether the row's largest is above 448 x 2^e, e the
+        // smaller of the two
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          bool above = false;
+          if ((open >> u) & 1u) {
+            const int low = max((int)((__float_as_uint(big[u]) + 0x1FFFFFu - 20u) >> 23) - 135, -126);
+            const double border = 448.0 * power_of_two(low);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (fabsf(i & 1 ? y[u][i >> 1].y : y[u][i >> 1].x) > big[u] * (1.f - 0x1p-18f))
+                above |= fabs(turned_exactly(r, position, 8 * c + i, x[u][i], p[u][i])) > border;
+            e[u] = low;
+          }
+          if ((__ballot_sync(0xffffffffu, above) >> (lane & 24)) & 0xFFu) ++e[u];
+        }
+      }
+      uint2 codes[U], other[U];
+      unsigned some = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float inv = __uint_as_float((uint32_t)(127 - e[u]) << 23), d = inv * off;
+        uint32_t lo[4], differ[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float s0 = fabsf(x[u][2 * i]) + fabsf(p[u][2 * i]);
+          const float s1 = fabsf(x[u][2 * i + 1]) + fabsf(p[u][2 * i + 1]);
+          // (a zero's sign goes, so that pairs of zeros are settled)
+          const float2 z = fma2(y[u][i].x, y[u][i].y, make_float2(inv, inv), make_float2(0.f, 0.f));
+          const float2 l = fma2(s0, s1, make_float2(-d, -d), z), h = fma2(s0, s1, make_float2(d, d), z);
+          lo[i] = fp8_pack2(l.x, l.y);
+          differ[i] = lo[i] ^ fp8_pack2(h.x, h.y);
+        }
+        codes[u] = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        other[u] = make_uint2(differ[0] | (differ[1] << 16), differ[2] | (differ[3] << 16));
+        some |= (other[u].x | other[u].y) != 0;
+      }
+      if (some) {
+        // the lane's open elements go to the list, for a lane each behind the K planes
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t sh = 8 * (i & 3);
+            if ((((i < 4 ? other[u].x : other[u].y) >> sh) & 0xFFu) == 0) continue;
+            const int k = atomicAdd(&n_open[warp], 1);
+            if (k < kOpen) {
+              Open o;
+              o.values = (__float_as_uint(x[u][i]) >> 16) | (__float_as_uint(p[u][i]) & 0xFFFF0000u);
+              o.plane = page >= 0 && (u == 0 || second) ? hh + u : -1;
+              o.token = (uint8_t)q4;
+              o.element = (uint8_t)(8 * c + i);
+              o.exponent = (int8_t)e[u];
+              open_list[warp][k] = o;
+            } else {
+              const double exact = turned_exactly(r, position, 8 * c + i, x[u][i], p[u][i]);
+              uint32_t& word = i < 4 ? codes[u].x : codes[u].y;
+              word = (word & ~(0xFFu << sh)) | code_of(exact * power_of_two(-e[u])) << sh;
+            }
+          }
+        }
       }
 #pragma unroll
-      for (int s = 1; s < 8; s <<= 1) {
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
-      }
-      const float off = most * (2.f * kOff);
-      int e = row_exponent(big + off);
-      const bool open = e != row_exponent(fmaxf(big - off, 0.f));
-      const float inv = __uint_as_float((uint32_t)(127 - e) << 23), d = inv * kOff;
-      uint32_t lo[4], differ[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float s0 = fabsf(x[2 * i]) + fabsf(p[2 * i]), s1 = fabsf(x[2 * i + 1]) + fabsf(p[2 * i + 1]);
-        const float z0 = y[2 * i] * inv, z1 = y[2 * i + 1] * inv;
-        lo[i] = fp8_pack2(fmaf(-d, s0, z0), fmaf(-d, s1, z1));
-        differ[i] = lo[i] ^ fp8_pack2(fmaf(d, s0, z0), fmaf(d, s1, z1));
-      }
-      uint2 codes = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-      const uint2 other = make_uint2(differ[0] | (differ[1] << 16), differ[2] | (differ[3] << 16));
-      const unsigned some = __ballot_sync(0xffffffffu, (other.x | other.y) != 0 || open);
-      if ((some >> (lane & 24)) & 0xFFu) codes = settle(r, position, c, v, vp, other, open, codes, &e);
-      store8(hh, codes, e);
+      for (int u = 0; u < U; ++u)
+        if (page >= 0 && (u == 0 || second)) store8(to + u * plane, codes[u], e[u]);
     }
-  });
-  const int q0 = max(h0, H);
-  uint16_t* const out_row = r.q_out + src * r.q_heads * kHeadDim + 8 * c;
-  go(q0, min(h1, turning), source(q0), [&](int hh, const uint4& v) {
-    const uint4 out = rounded(v);
-    if (row) *reinterpret_cast<uint4*>(out_row + (hh - H) * kHeadDim) = out;
-  });
-  const int v0 = max(h0, turning);
-  go(v0, h1, source(v0), [&](int hh, const uint4& v) {
-    if constexpr (FP8) {
-      int e;
-      const uint2 codes = quantise8(v, &e);
-      store8(hh - r.q_heads, codes, e);
-    } else if (page >= 0) {
-      *reinterpret_cast<uint4*>(code + (hh - r.q_heads) * plane) = v;
+  }
+  if (h0 < H && hh > min(h1, H)) to -= plane;    // behind an odd one
+  if constexpr (FP8) {
+    // what is open, a lane each
+    __syncwarp();
+    const int n = min(n_open[warp], kOpen);
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      Open o;
+      o.plane = -1;
+      o.token = 0;
+      if (k0 + lane < n) o = open_list[warp][k0 + lane];
+      const long long token = __shfl_sync(0xffffffffu, src, 8 * o.token);
+      uint8_t* const its_base = reinterpret_cast<uint8_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(base), 8 * o.token));
+      const int its_slot = __shfl_sync(0xffffffffu, slot, 8 * o.token);
+      if (o.plane >= 0) {
+        const double y = turned_exactly(r, r.positions + token * r.axes, o.element,
+                                        __uint_as_float(o.values << 16), __uint_as_float(o.values & 0xFFFF0000u));
+        its_base[o.plane * plane + fp8_code_off(H, Ps, 0, 0, its_slot) + o.element] =
+            (uint8_t)code_of(y * power_of_two(-o.exponent));
+      }
     }
-  });
+  }
+  hh = max(h0, min(hh, H));
+#pragma unroll 1
+  for (const int end = min(h1, turning); hh < end; hh += U, q_to += U * kHeadDim) {
+    uint4 v[U];
+    const bool second = U == 2 && hh + 1 < end;
+    take(v, second);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint4 out = rounded(v[u]);
+      if (row && (u == 0 || second)) *reinterpret_cast<uint4*>(q_to + u * kHeadDim) = out;
+    }
+  }
+  hh = max(h0, min(hh, turning));
+#pragma unroll 1
+  for (; hh < h1; hh += U, to += U * plane) {
+    uint4 v[U];
+    const bool second = U == 2 && hh + 1 < h1;
+    take(v, second);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool there = page >= 0 && (u == 0 || second);
+      if constexpr (FP8) {
+        int e;
+        const uint2 codes = quantise8(v[u], &e);
+        if (there) store8(to + u * plane, codes, e);
+      } else if (there) {
+        *reinterpret_cast<uint4*>(to + u * plane) = v[u];
+      }
+    }
+  }
 }
 
-template <typename Args>
+template <bool FP8, int U, typename Args>
 cudaError_t launch_rotary(const Args& a, const RotaryArgs& r, int blocks, int shares, cudaStream_t s) {
-  return a.pool.fp8 ? launch_pdl(token_append_rotary_kernel<true, Args>, dim3(blocks), dim3(kWarps * 32), 0, s, a, r, shares)
-                    : launch_pdl(token_append_rotary_kernel<false, Args>, dim3(blocks), dim3(kWarps * 32), 0, s, a, r, shares);
+  return launch_pdl(token_append_rotary_kernel<FP8, U, Args>, dim3(blocks), dim3(kWarps * 32), 0, s, a, r, shares);
+}
+template <typename Args>
+cudaError_t launch_rotary_args(const Args& a, const RotaryArgs& r, int blocks, int shares, bool one, cudaStream_t s) {
+  if (one) return a.pool.fp8 ? launch_rotary<true, 1>(a, r, blocks, shares, s) : launch_rotary<false, 1>(a, r, blocks, shares, s);
+  return a.pool.fp8 ? launch_rotary<true, 2>(a, r, blocks, shares, s) : launch_rotary<false, 2>(a, r, blocks, shares, s);
 }
 
 }  // namespace
@@ -296,11 +441,12 @@ cudaError_t launch_token_append_rotary(const TokenRowsArgs& a, const RotaryArgs&
   const long long quads = ((long long)a.units + kQuad - 1) / kQuad;
   const int planes = 2 * a.pool.heads + r.q_heads;
   // few tokens: a plane a warp; else enough warps for the SMs, so that angles are shared
-  const long long want = 152 * 48;
+  const long long want = 152 * (a.pool.fp8 ? 24 : 96);
   const int shares = (int)std::max<long long>(1, std::min<long long>(planes, want / quads));
   const int blocks = (int)((quads * shares + kWarps - 1) / kWarps);
-  const cudaError_t e = a.n <= kSmallTokenBatch ? launch_rotary(small_args(a), r, blocks, shares, s)
-                                                : launch_rotary(a, r, blocks, shares, s);
+  const bool one = shares == planes;
+  const cudaError_t e = a.n <= kSmallTokenBatch ? launch_rotary_args(small_args(a), r, blocks, shares, one, s)
+                                                : launch_rotary_args(a, r, blocks, shares, one, s);
   count_launches(1);
   return e;
 }
