@@ -40,11 +40,7 @@ namespace pkv {
 namespace {
 
 // Consumer warps (and one producer). Up to 16 rows: four, at 168 registers a thread. 24 rows:
-// three, so that two CTAs' warps have 255 (a fourth warp makes them spill: 4 % slower). A
-// block of 24 against two of 16, 16 streams of 4001 tokens with 17, 20, 21 or 24 rows, which
-// take the same: 29.8 against 36.9 us, of 500 .. 4001 tokens 22.6 against 31.6 us, on E4M3
-// pages 35.4 against 43.6 and 26.1 against 37.4 us. With 32 rows the block takes longer than
-// two of 16: 36 against 29 us, and 47 against 41 on E4M3 pages.
+// three, so that two CTAs' warps have 255 (a fourth warp makes them spill: 4 % slower).
 template <int NT>
 constexpr int kWarps = NT <= 2 ? 4 : 3;
 template <int NT>
@@ -248,18 +244,6 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
     uint32_t qb[NT][4][2];
     float sl2[NT][2];                            // score scale of queries 2 tq, 2 tq + 1
     int pos[NT][2];                              // trees: the row in the block instead
-    if constexpr (TREE) {
-      // what the rows see of the tree, if the CTA has a tile that some of them do not see whole
-      if (a.window > 0 || (nT > 0 && tok_tile(tiles, j1 - 1) * kTokTile + kTokTile > t.pos0)) {
-        load_parents(sm.tree, a.parents + t.row0, t.n, threadIdx.x, kWarps<NT> * 32, a.err);
-        __syncwarp();
-        asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps<NT> * 32) : "memory");
-        if (threadIdx.x < w.rows)
-          walk_tree(sm.tree, threadIdx.x, (w.r0 + threadIdx.x) / a.group, t.pos0, a.window, a.sinks);
-        __syncwarp();
-        asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps<NT> * 32) : "memory");
-      }
-    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = n * 8 + g;
@@ -302,6 +286,18 @@ __global__ void __launch_bounds__(kThreads<NT>, kCtasPerSm) token_few_kernel(con
         sl2[n][i] = a.scale_log2 * __uint_as_float((uint32_t)(127 + er) << 23);
         const int rq = min(n * 8 + 2 * tq + i, w.rows - 1);
         pos[n][i] = TREE ? rq : t.pos0 + (w.r0 + rq) / a.group;
+      }
+    }
+    if constexpr (TREE) {
+      // what the rows see of the tree, if the CTA has a tile that some of them do not see whole
+      if (a.window > 0 || (nT > 0 && tok_tile(tiles, j1 - 1) * kTokTile + kTokTile > t.pos0)) {
+        load_parents(sm.tree, a.parents + t.row0, t.n, threadIdx.x, kWarps<NT> * 32, a.err);
+        __syncwarp();
+        asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps<NT> * 32) : "memory");
+        if (threadIdx.x < w.rows)
+          walk_tree(sm.tree, threadIdx.x, (w.r0 + threadIdx.x) / a.group, t.pos0, a.window, a.sinks);
+        __syncwarp();
+        asm volatile("bar.sync 1, %0;\n" ::"n"(kWarps<NT> * 32) : "memory");
       }
     }
 

@@ -7,6 +7,8 @@
 // blocks'). With few tokens a warp moves four consecutive ones of one (K or V, head): 8 lanes
 // of 16 bytes a token. Their slots are neighbours in a page, so on E4M3 pages the warp writes
 // one run of 256 code bytes and 4 neighbouring exponent bytes.
+#include <algorithm>
+
 #include "pkv_tokens.cuh"
 
 namespace pkv {
@@ -236,11 +238,14 @@ __global__ void __launch_bounds__(256) token_drop_kernel(const __grid_constant__
   }
 }
 
-// Accepted drafts move to the front of their tree's slots, in every layer; a warp takes one
-// (stream, layer, K or V, head), 32 rows at a time, read before any of them is written. A row's
-// destination is never behind its source, so what later rounds read is not overwritten. The
-// blocks behind those return the dropped pages.
-constexpr int kKeepRows = 8;         // rows a lane has on their way
+// Accepted drafts move to the front of their tree's slots, in every layer; a block takes one
+// (stream, layer, K or V, head), 16 rows a warp at a time, read before any of them is
+// written. A row's destination is never behind its source, so what later rounds read is not
+// overwritten. The blocks behind those return the dropped pages.
+// Bounds: latency (a launch, then the loads of numbers, pages and rows, each behind the one
+// before; every step's loads of a lane are on their way together). So a block has as many
+// warps as hold the longest list at once, up to 8.
+constexpr int kKeepRows = 4;         // rows a lane has on their way
 template <typename Args>
 __global__ void __launch_bounds__(kWarps * 32) token_keep_kernel(const __grid_constant__ Args a, int move_blocks) {
   pdl_wait();
@@ -254,67 +259,83 @@ __global__ void __launch_bounds__(kWarps * 32) token_keep_kernel(const __grid_co
     }
     return;
   }
-  const int lane = threadIdx.x & 31, c = lane & 7, t0 = lane >> 3;
-  const int H2 = 2 * a.pool.heads, Ps = a.pool.page_size;
-  const int w = blockIdx.x * kWarps + (threadIdx.x >> 5), planes = a.layers * H2;
-  if (w >= a.n * planes) return;
+  const int c = threadIdx.x & 7, t0 = threadIdx.x >> 3, step = blockDim.x >> 3;
+  const int H2 = 2 * a.pool.heads, Ps = a.pool.page_size, fp8 = a.pool.fp8;
+  const int w = blockIdx.x, planes = a.layers * H2;
   const TokenKeepItem& it = a.item[w / planes];
-  const int layer = w % planes / H2, hh = w % H2, kv = hh >= a.pool.heads ? 1 : 0, h = hh - kv * a.pool.heads;
-  uint8_t* const base = reinterpret_cast<uint8_t*>(a.pool.base) + layer * a.layer_bytes;
+  const int layer = w % planes / H2, hh = w % H2;
+  const int B = fp8_block_rows(Ps);              // a power of two
+  const long long plane = (long long)hh * Ps * (fp8 ? kHeadDim + 1 : 2 * kHeadDim);
+  uint8_t* const base = reinterpret_cast<uint8_t*>(a.pool.base) + layer * a.layer_bytes + plane;
   const int32_t* const kept = a.kept + it.kept0;
-  const auto page_at = [&](int pos) {
-    const int page = it.pages[pos / Ps];
-    if (page >= 0 && page < a.pool.pool_pages) return page;
-    atomicOr(a.err, kErrPageRange);
-    return -1;
+  const bool notes = hh == 0 && layer == 0 && c == 0;
+  // the lane's part of a slot's row in its page
+  const auto part = [&](int slot) {
+    const int rb = slot & (B - 1);
+    return fp8 ? (slot - rb) * (kHeadDim + 1) + rb * kHeadDim + 8 * c
+               : slot * kHeadDim * 2 + (swizzle_chunk(slot, c) << 4);
   };
-  for (int r0 = 0; r0 < it.m; r0 += kQuad * kKeepRows) {
+  const auto exponent = [&](int slot) {
+    const int rb = slot & (B - 1);
+    return (slot - rb) * (kHeadDim + 1) + B * kHeadDim + rb;
+  };
+  for (int r0 = 0; r0 < it.m; r0 += step * kKeepRows) {
+    int x[kKeepRows], before[kKeepRows], page[kKeepRows], to_page[kKeepRows];
     uint4 val[kKeepRows];
     int exp[kKeepRows];
-    uint32_t moves = 0;
 #pragma unroll
     for (int u = 0; u < kKeepRows; ++u) {
-      const int i = r0 + u * kQuad + t0;
-      exp[u] = 0;
-      val[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (i >= it.m) continue;
-      const int x = kept[i];
-      if (x < i || x >= it.n || (i > 0 && kept[i - 1] >= x)) {
-        if (hh == 0 && layer == 0 && c == 0) atomicOr(a.err, kErrTree);
-        if (x < i || x >= it.n) continue;
+      const int i = r0 + u * step + t0;
+      x[u] = i < it.m ? kept[i] : i;
+      before[u] = i < it.m && i > 0 ? kept[i - 1] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kKeepRows; ++u) {
+      const int i = r0 + u * step + t0;
+      const bool inside = x[u] >= i && x[u] < it.n;
+      if (i < it.m && notes && (!inside || before[u] >= x[u])) atomicOr(a.err, kErrTree);
+      if (i >= it.m || !inside) x[u] = i;        // stays
+      page[u] = to_page[u] = 0;
+      if (x[u] != i) {
+        page[u] = it.pages[(it.pos0 + x[u]) / Ps];
+        to_page[u] = it.pages[(it.pos0 + i) / Ps];
       }
-      if (x == i) continue;
-      const int pos = it.pos0 + x, page = page_at(pos), slot = pos % Ps;
-      if (page < 0) continue;
-      const uint8_t* const p = base + (long long)page * a.pool.page_bytes;
-      if (a.pool.fp8) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p + fp8_code_off(a.pool.heads, Ps, kv, h, slot) + 8 * c);
+    }
+#pragma unroll
+    for (int u = 0; u < kKeepRows; ++u) {
+      const int i = r0 + u * step + t0;
+      const bool there = (unsigned)page[u] < (unsigned)a.pool.pool_pages && (unsigned)to_page[u] < (unsigned)a.pool.pool_pages;
+      if (!there) {
+        if (notes) atomicOr(a.err, kErrPageRange);
+        x[u] = i;
+      }
+      if (x[u] == i) continue;
+      const int slot = (it.pos0 + x[u]) % Ps;
+      const uint8_t* const from = base + (long long)page[u] * a.pool.page_bytes;
+      if (fp8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(from + part(slot));
         val[u].x = v.x;
         val[u].y = v.y;
-        if (c == 0) exp[u] = p[fp8_exp_off(a.pool.heads, Ps, kv, h, slot)];
+        exp[u] = from[exponent(slot)];
       } else {
-        val[u] = *reinterpret_cast<const uint4*>(
-            p + (((long long)hh * Ps + slot) * kHeadDim + swizzle_chunk(slot, c) * 8) * 2);
+        val[u] = *reinterpret_cast<const uint4*>(from + part(slot));
       }
-      moves |= 1u << u;
     }
-    __syncwarp();                                // read before written
+    __syncthreads();                             // read before written
 #pragma unroll
     for (int u = 0; u < kKeepRows; ++u) {
-      if (!((moves >> u) & 1u)) continue;
-      const int pos = it.pos0 + r0 + u * kQuad + t0, page = page_at(pos), slot = pos % Ps;
-      if (page < 0) continue;
-      uint8_t* const p = base + (long long)page * a.pool.page_bytes;
-      if (a.pool.fp8) {
-        *reinterpret_cast<uint2*>(p + fp8_code_off(a.pool.heads, Ps, kv, h, slot) + 8 * c) =
-            make_uint2(val[u].x, val[u].y);
-        if (c == 0) p[fp8_exp_off(a.pool.heads, Ps, kv, h, slot)] = (uint8_t)exp[u];
+      const int i = r0 + u * step + t0;
+      if (x[u] == i) continue;
+      const int slot = (it.pos0 + i) % Ps;
+      uint8_t* const to = base + (long long)to_page[u] * a.pool.page_bytes;
+      if (fp8) {
+        *reinterpret_cast<uint2*>(to + part(slot)) = make_uint2(val[u].x, val[u].y);
+        if (c == 0) to[exponent(slot)] = (uint8_t)exp[u];
       } else {
-        *reinterpret_cast<uint4*>(p + (((long long)hh * Ps + slot) * kHeadDim + swizzle_chunk(slot, c) * 8) * 2) =
-            val[u];
+        *reinterpret_cast<uint4*>(to + part(slot)) = val[u];
       }
     }
-    __syncwarp();
+    __syncthreads();
   }
 }
 
@@ -380,8 +401,11 @@ cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_token_keep(const TokenKeepArgs& a, cudaStream_t s) {
-  const int blocks = (a.n * a.layers * 2 * a.pool.heads + kWarps - 1) / kWarps;
-  const dim3 grid(blocks + a.n), threads(kWarps * 32);
+  int most = 1;
+  for (int i = 0; i < a.n; ++i) most = std::max(most, a.item[i].m);
+  const int blocks = a.n * a.layers * 2 * a.pool.heads;
+  const int warps = std::min(kWarps, (most + kQuad * kKeepRows - 1) / (kQuad * kKeepRows));
+  const dim3 grid(blocks + a.n), threads(warps * 32);
   const cudaError_t e =
       a.n <= kSmallTokenBatch
           ? launch_pdl(token_keep_kernel<SmallKeepArgs>, grid, threads, 0, s, small_args(a), blocks)

@@ -178,18 +178,27 @@ PKV_HD bool tree_tile_full(int b, int pos0, int n, int window, int sinks) {
   return tok_tile_full(b, pos0 - 1, pos0 + n - 1, window, sinks);
 }
 // Node i's depth, and the tree's slots that it sees: bit x % 64 of words[x / 64], x counted
-// from the start of pos0's tile (words: zeros before).
+// from the start of pos0's tile (words: zeros before). Parents come before their nodes, so
+// words are left for good.
 template <typename Parent>
 PKV_HD int tree_walk(const Parent* parent, int i, int pos0, int window, int sinks, uint64_t* words) {
   int depth = -1;
-  for (int a = i; a >= 0; a = parent[a]) ++depth;
-  int k = 0;
-  for (int a = i; a >= 0; a = parent[a], ++k)
-    if (window == 0 || k < window || pos0 + depth - k < sinks) {
-      const int x = pos0 % kTokTile + a;
-      words[x / kTokTile] |= 1ull << (x % kTokTile);
+  if (window > 0)                                // else it takes one walk
+    for (int a = i; a >= 0; a = parent[a]) ++depth;
+  int k = 0, w = (pos0 % kTokTile + i) / kTokTile;
+  uint64_t bits = 0;
+  for (int a = i; a >= 0; a = parent[a], ++k) {
+    if (window > 0 && k >= window && pos0 + depth - k >= sinks) continue;
+    const int x = pos0 % kTokTile + a;
+    if (x / kTokTile != w) {
+      words[w] = bits;
+      bits = 0;
+      w = x / kTokTile;
     }
-  return depth;
+    bits |= 1ull << (x % kTokTile);
+  }
+  words[w] = bits;
+  return k - 1;
 }
 // Bit i: whether slot b + i is seen by a node at that depth with those words.
 PKV_HD uint64_t tree_mask(int b, int pos0, int depth, const uint64_t* words, int window, int sinks) {

@@ -71,8 +71,8 @@ void rows_args(pkv_t h, int layer, TokenRowsArgs* a) {
 }
 
 // What a kernel's CTA costs, in the time of one 64-slot tile: its start and end, and
-// (when it leaves partial results) their share of the join. As measured: decode steps
-// take 0.25 us a tile and 3 us a CTA, the matrix-unit kernel 0.5 us and 5 us.
+// (when it leaves partial results) their share of the join. A tile is what it takes beside the
+// SM's other CTAs.
 struct CtaCost {
   int slots;                     // CTAs that run at once
   double tile;                   // us
@@ -137,7 +137,7 @@ double plan_shape(pkv_t h, TokenAttendArgs* a, bool few, int shape) {
   }
   const int room = std::min<int>(kTokenScratchBytes / (shape * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
   const CtaCost cost =
-      few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), 0.25, 12, 4, 8, room}
+      few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), token_few_tile_us(shape), 12, 4, 8, room}
           : CtaCost{h->num_sms * token_tc_ctas_per_sm(h->fp8, shape), token_tc_tile_us(h->fp8, shape), 10, 4, 8, room};
   return plan_splits(a, first, last, cost);
 }
@@ -344,9 +344,20 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
     give_parts(&a);
     return launch_tc(a);
   }
-  const int few_shape = most <= 8 ? 8 : most > 16 && most <= 24 ? 24 : 16;
+  const auto plan_few = [&](TokenAttendArgs* t) {
+    if (most <= 8) return plan_shape(h, t, true, 8);
+    // 17 to 24 rows: a block of 24 with three warps, or two of 16 with four, of which the second
+    // finds the keys in L2. (21 rows, 24 / 16 + 16, pages not in L2: a stream of 16000 tokens 21.6 / 16.0
+    // us, on E4M3 pages 25 / 19; 16 streams of 2000 19.6 / 16.2 us, of 16000 84 / 93, on E4M3 pages
+    // 115 / 141; 48 ragged ones of up to 4000 49 / 44 us.)
+    if (most > 16 && most <= 24) {
+      const double two = plan_shape(h, t, true, 16), one = plan_shape(h, t, true, 24);
+      if (one < two) return one;
+    }
+    return plan_shape(h, t, true, 16);
+  };
   if (n_small == n_items) {
-    plan_shape(h, &a, true, few_shape);
+    plan_few(&a);
     give_parts(&a);
     PKV_CUDA(h, launch_token_few(a, s));
     return PKV_OK;
@@ -361,7 +372,7 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
     TokenAttendArgs& t = (long long)a.item[i].n * group <= few_rows ? small : large;
     t.item[t.n++] = a.item[i];
   }
-  const double apart = plan_shape(h, &small, true, few_shape) + plan_tc(h, &large) + 3.0;
+  const double apart = plan_few(&small) + plan_tc(h, &large) + 3.0;
   if (plan_tc(h, &a) <= apart) {
     give_parts(&a);
     return launch_tc(a);

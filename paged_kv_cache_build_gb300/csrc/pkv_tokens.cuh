@@ -262,6 +262,8 @@ cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s);
 constexpr int kTokenFewRows = 64;
 constexpr int kTokenFewRowsAll = 32;
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s);
+// What a 64-slot tile takes a CTA of that many rows, in us, beside the SM's other one.
+inline double token_few_tile_us(int rows) { return rows == 24 ? 0.8 : 0.55; }
 // Resident CTAs per SM of that kernel.
 int token_few_ctas_per_sm();
 // Attention of 128, 256 or (on E4M3 pages) 512 query rows per CTA (a.rows).
