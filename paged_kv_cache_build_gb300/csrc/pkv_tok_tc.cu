@@ -41,76 +41,77 @@ namespace pkv {
 namespace {
 
 constexpr int kBN = kTokTile;
-// bf16 pages: two CTAs of two lanes an SM, so that one's start and end run beside
-// the other's products (prefill of 8192 tokens, 16 heads: 145 us, 152 with one CTA of 512
-// rows; ragged batch of 12 chunks 245 against 270 us; 128 rows, 32 streams of 2000 tokens 30
-// against 38 us with one CTA of four lanes, ragged ones of 4001 24 against 32, one of 32000 25
-// as well; but 16 even ones of 4031, a CTA for each of 128 SMs, 35 against 31 us). E4M3 pages:
-// one CTA of four lanes, which converts a tile once for all of them.
-template <int MT, bool FP8>
-constexpr int kLanes = FP8 ? 4 : 2;
-template <int MT, bool FP8>
-constexpr int kCtasPerSm = 4 / kLanes<MT, FP8>;
-template <int MT, bool FP8>
-constexpr int kSoftmaxWarps = 4 * kLanes<MT, FP8>;
-template <int MT, bool FP8>
-constexpr int kIssuer0 = kSoftmaxWarps<MT, FP8>;
-template <int MT, bool FP8>
-constexpr int kProducer = kIssuer0<MT, FP8> + kLanes<MT, FP8>;
-template <int MT, bool FP8>
-constexpr int kConvert0 = kProducer<MT, FP8> + 1;
+// kLanes = 2: two CTAs of two lanes an SM, so that one's start and end run beside the other's
+// products; 4: one CTA of four. bf16 pages take two (prefill of 8192 tokens, 16 heads, 256 rows: 145
+// us, 152 with one CTA of 512 rows; ragged batch of 12 chunks 245 against 270 us; 128 rows, 32
+// streams of 2000 tokens 30 against 38 us, ragged ones of 4001 24 against 32, one of 32000 25 as
+// well; but 16 even ones of 4031, a CTA for each of 128 SMs, 35 against 31 us). E4M3 pages take
+// four, which share a tile's conversion, or, with 128 rows, what is estimated to end first: 64
+// streams of 2000 tokens 100 us with two and 120 with four, 16 ragged ones of 4001 41 and 46, 16 even
+// ones 56 and 52, one of 16000 28 and 24 us. (256 rows with two: 71 against 63 us.)
+template <int MT, bool FP8, int kLanes>
+constexpr int kCtasPerSm = 4 / kLanes;
+template <int MT, bool FP8, int kLanes>
+constexpr int kSoftmaxWarps = 4 * kLanes;
+template <int MT, bool FP8, int kLanes>
+constexpr int kIssuer0 = kSoftmaxWarps<MT, FP8, kLanes>;
+template <int MT, bool FP8, int kLanes>
+constexpr int kProducer = kIssuer0<MT, FP8, kLanes> + kLanes;
+template <int MT, bool FP8, int kLanes>
+constexpr int kConvert0 = kProducer<MT, FP8, kLanes> + 1;
 // The conversion sets E4M3 pages' pace: with one or two row blocks seven warps do it (16
 // streams of 8030 keys, 120 rows: 97 us, 160 with three), with four there are registers for
 // three only.
-template <int MT, bool FP8>
-constexpr int kConvertWarps = kLanes<MT, FP8> == 2 ? 1 : FP8 && MT < 4 ? 7 : 3;   // (bf16: idle, whole warpgroups)
-template <int MT, bool FP8>
-constexpr int kThreads = 32 * (kConvert0<MT, FP8> + kConvertWarps<MT, FP8>);
+template <int MT, bool FP8, int kLanes>
+constexpr int kConvertWarps = kLanes == 2 ? (FP8 ? 5 : 1) : MT < 4 ? 7 : 3;   // (bf16: idle, whole warpgroups)
+template <int MT, bool FP8, int kLanes>
+constexpr int kThreads = 32 * (kConvert0<MT, FP8, kLanes> + kConvertWarps<MT, FP8, kLanes>);
 // Registers a thread at launch; the softmax warpgroups then take what the others give up.
-template <int MT, bool FP8>
-constexpr int kLaunchRegs = FP8 && MT < 4 ? 72 : 80;
-template <int MT, bool FP8>
-constexpr int kOtherRegs = FP8 && MT < 4 ? 40 : 32;
-template <int MT, bool FP8>
+template <int MT, bool FP8, int kLanes>
+constexpr int kLaunchRegs = !FP8 || MT == 4 ? 80 : kLanes == 2 ? 64 : 72;
+template <int MT, bool FP8, int kLanes>
+constexpr int kOtherRegs = FP8 && MT < 4 && kLanes == 4 ? 40 : 32;
+template <int MT, bool FP8, int kLanes>
 constexpr int kSoftmaxRegs = FP8 && MT < 4 ? 96 : 104;
-template <int MT, bool FP8>
+template <int MT, bool FP8, int kLanes>
 constexpr bool kRegsFit =
-    kSoftmaxRegs<MT, FP8> * kSoftmaxWarps<MT, FP8> +
-        kOtherRegs<MT, FP8> * (kThreads<MT, FP8> / 32 - kSoftmaxWarps<MT, FP8>) <=
-    kLaunchRegs<MT, FP8> * (kThreads<MT, FP8> / 32);
-template <int MT, bool FP8>
-constexpr int kQThreads = 32 * kProducer<MT, FP8>;   // softmax warps and issuers
+    kSoftmaxRegs<MT, FP8, kLanes> * kSoftmaxWarps<MT, FP8, kLanes> +
+        kOtherRegs<MT, FP8, kLanes> * (kThreads<MT, FP8, kLanes> / 32 - kSoftmaxWarps<MT, FP8, kLanes>) <=
+    kLaunchRegs<MT, FP8, kLanes> * (kThreads<MT, FP8, kLanes> / 32);
+template <int MT, bool FP8, int kLanes>
+constexpr int kQThreads = 32 * kProducer<MT, FP8, kLanes>;   // softmax warps and issuers
 // The ring's stages belong to one part of the tiles each: a multiple of kLanes / MT.
-template <int MT, bool FP8>
-constexpr int kRing = kLanes<MT, FP8> == 2 ? 4 : MT == 4 ? 6 : 8;
-constexpr int kCodeRing = 4;
+template <int MT, bool FP8, int kLanes>
+constexpr int kRing = kLanes == 2 ? 4 : MT == 4 ? 6 : 8;
+template <int kLanes>
+constexpr int kCodeRing = kLanes == 2 ? 2 : 4;   // (two CTAs an SM leave room for two)
 constexpr int kCodeBytes = kBN * (kHeadDim + 1);
 // TMEM: S of lane i at 64 i, O at 64 (kLanes + i)
-template <int MT, bool FP8>
-constexpr uint32_t kTmemCols = 128 * kLanes<MT, FP8>;
+template <int MT, bool FP8, int kLanes>
+constexpr uint32_t kTmemCols = 128 * kLanes;
 constexpr float kSumLimit = 1024.0f;           // values up to 2^90 cannot take O past fp32's end
 
 struct NoTree {};
 
-template <int MT, bool FP8, bool TREE>
+template <int MT, bool FP8, int kLanes, bool TREE>
 struct __align__(1024) TcSmem {
   uint8_t q[MT][128 * 128];
   union {
     struct {
-      uint8_t k[kRing<MT, FP8>][kBN * 128];
-      uint8_t v[kRing<MT, FP8>][kBN * 128];
+      uint8_t k[kRing<MT, FP8, kLanes>][kBN * 128];
+      uint8_t v[kRing<MT, FP8, kLanes>][kBN * 128];
     };
-    float o[kLanes<MT, FP8> - MT + (MT == kLanes<MT, FP8>)][kHeadDim][128];   // parts 1.. of the tiles, for the join
+    float o[kLanes - MT + (MT == kLanes)][kHeadDim][128];   // parts 1.. of the tiles, for the join
   };
-  uint8_t code[FP8 ? kCodeRing : 1][FP8 ? 2 * kCodeBytes : 16];
-  float ml[kLanes<MT, FP8>][128][2];
-  uint64_t kv_full[kRing<MT, FP8>];
-  uint64_t kv_empty[kRing<MT, FP8>];
-  uint64_t code_full[kCodeRing];
-  uint64_t code_empty[kCodeRing];
-  uint64_t s_full[kLanes<MT, FP8>];
-  uint64_t p_full[kLanes<MT, FP8>];
-  uint64_t done[kLanes<MT, FP8>];
+  uint8_t code[FP8 ? kCodeRing<kLanes> : 1][FP8 ? 2 * kCodeBytes : 16];
+  float ml[kLanes][128][2];
+  uint64_t kv_full[kRing<MT, FP8, kLanes>];
+  uint64_t kv_empty[kRing<MT, FP8, kLanes>];
+  uint64_t code_full[kCodeRing<kLanes>];
+  uint64_t code_empty[kCodeRing<kLanes>];
+  uint64_t s_full[kLanes];
+  uint64_t p_full[kLanes];
+  uint64_t done[kLanes];
   // the CTA's work, kept here for the roles to read what they need of it
   TokenWork work;
   TokTiles tiles;
@@ -179,26 +180,26 @@ __device__ __forceinline__ LaneRows lane_rows(const TokenAttendArgs& a, const To
   return l;
 }
 
-template <int MT, bool FP8, bool TREE>
-__global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
+template <int MT, bool FP8, int kLanes, bool TREE>
+__global__ void __launch_bounds__(kThreads<MT, FP8, kLanes>, kCtasPerSm<MT, FP8, kLanes>)
     token_tc_kernel(const __grid_constant__ TokenAttendArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  TcSmem<MT, FP8, TREE>& sm = *reinterpret_cast<TcSmem<MT, FP8, TREE>*>(
+  TcSmem<MT, FP8, kLanes, TREE>& sm = *reinterpret_cast<TcSmem<MT, FP8, kLanes, TREE>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  constexpr int kS = kRing<MT, FP8>;
-  constexpr int kParts = kLanes<MT, FP8> / MT;
+  constexpr int kS = kRing<MT, FP8, kLanes>;
+  constexpr int kParts = kLanes / MT;
   static_assert(kS % kParts == 0, "a stage's tiles belong to one part");
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kS; ++s) {
-      mbar_init(&sm.kv_full[s], FP8 ? kConvertWarps<MT, FP8> : 1);
+      mbar_init(&sm.kv_full[s], FP8 ? kConvertWarps<MT, FP8, kLanes> : 1);
       mbar_init(&sm.kv_empty[s], MT);
     }
-    for (int s = 0; s < kCodeRing; ++s) {
+    for (int s = 0; s < kCodeRing<kLanes>; ++s) {
       mbar_init(&sm.code_full[s], 1);
-      mbar_init(&sm.code_empty[s], kConvertWarps<MT, FP8>);
+      mbar_init(&sm.code_empty[s], kConvertWarps<MT, FP8, kLanes>);
     }
-    for (int i = 0; i < kLanes<MT, FP8>; ++i) {
+    for (int i = 0; i < kLanes; ++i) {
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.done[i], 1);
@@ -206,10 +207,10 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     sm.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == kIssuer0<MT, FP8>) {
+  if (warp == kIssuer0<MT, FP8, kLanes>) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      smem_u32(&sm.tmem_base)),
-                 "r"(kTmemCols<MT, FP8>));
+                 "r"(kTmemCols<MT, FP8, kLanes>));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
   if (threadIdx.x == 32) {
@@ -231,15 +232,15 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
   volatile int* abort = &sm.abort;
   const TokenWork& w = sm.work;
   const int G = a.group;
-  static_assert(kRegsFit<MT, FP8>, "the register split is within the launch's registers");
+  static_assert(kRegsFit<MT, FP8, kLanes>, "the register split is within the launch's registers");
   pdl_wait();
   pdl_trigger();
 
-  if (warp < kProducer<MT, FP8>) {
+  if (warp < kProducer<MT, FP8, kLanes>) {
     // Q rows as swizzled operand tiles, all on their way at once; rows behind the last
     // one as zeros
-    // (row r + kQThreads<MT, FP8> / 8 is dt tokens and dm members of the group further)
-    constexpr int kStepRows = kQThreads<MT, FP8> / 8;
+    // (row r + kQThreads<MT, FP8, kLanes> / 8 is dt tokens and dm members of the group further)
+    constexpr int kStepRows = kQThreads<MT, FP8, kLanes> / 8;
     const int c = threadIdx.x & 7, dt = kStepRows / G, dm = kStepRows - dt * G;
     int r = threadIdx.x >> 3, tok = (w.r0 + r) / G, mem = w.r0 + r - tok * G;
     for (; r < MT * 128; r += kStepRows) {
@@ -259,12 +260,12 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
     fence_proxy_async();
-    asm volatile("bar.sync 1, %0;\n" ::"r"(kQThreads<MT, FP8>) : "memory");
+    asm volatile("bar.sync 1, %0;\n" ::"r"(kQThreads<MT, FP8, kLanes>) : "memory");
   }
 
-  if (warp == kProducer<MT, FP8>) {
+  if (warp == kProducer<MT, FP8, kLanes>) {
     // ---------------------------------------------------------------- producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8, kLanes>));
     const int Ps = a.pool.page_size;
     const int nT = sm.j1 - sm.j0, j0 = sm.j0, p0 = w.p0, p1 = w.p1, head = w.head;
     const TokTiles tiles = sm.tiles;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     const int rows = min(Ps, kBN);                       // slots per block
     const int per = kBN / rows, group = 32 / per;
     constexpr uint32_t kOperand = FP8 ? kCodeBytes : kBN * 128;   // bytes of K or V in a tile
-    constexpr int kRingN = FP8 ? kCodeRing : kS;
+    constexpr int kRingN = FP8 ? kCodeRing<kLanes> : kS;
     uint64_t* const full = FP8 ? sm.code_full : sm.kv_full;
     uint64_t* const empty = FP8 ? sm.code_empty : sm.kv_empty;
     const uint32_t block_bytes = kOperand / per;
@@ -319,20 +320,20 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     if (lane == 0)
       for (int j = max(0, issued - kRingN); j < issued; ++j)
         tok_wait(&full[j % kRingN], (j / kRingN) & 1, abort, a.err, false);
-  } else if (warp >= kConvert0<MT, FP8>) {
+  } else if (warp >= kConvert0<MT, FP8, kLanes>) {
     // ------------------------------------------------- E4M3 tiles to operands
     // 4 lanes a row, 16 codes a lane; 8 rows of K or of V a warp at a time
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8, kLanes>));
     const int B = min(kBN, a.pool.page_size);    // rows of a code block
     const int nT = FP8 ? sm.j1 - sm.j0 : 0;
-    const int cw = warp - kConvert0<MT, FP8>;
+    const int cw = warp - kConvert0<MT, FP8, kLanes>;
     int u0 = cw;                                 // takes turns with the tile's larger shares
     for (int j = 0; j < nT; ++j) {
-      const int c8 = j % kCodeRing, s = j % kS;
-      if (!tok_wait(&sm.code_full[c8], (j / kCodeRing) & 1, abort, a.err)) break;
+      const int c8 = j % kCodeRing<kLanes>, s = j % kS;
+      if (!tok_wait(&sm.code_full[c8], (j / kCodeRing<kLanes>) & 1, abort, a.err)) break;
       if (!tok_wait(&sm.kv_empty[s], ((j / kS) & 1) ^ 1, abort, a.err)) break;
 #pragma unroll (MT == 4 ? 3 : 2)
-      for (int u = u0; u < 2 * kBN / 8; u += kConvertWarps<MT, FP8>) {
+      for (int u = u0; u < 2 * kBN / 8; u += kConvertWarps<MT, FP8, kLanes>) {
         const int kv = u >= kBN / 8 ? 1 : 0;
         const int r = (u - kv * (kBN / 8)) * 8 + (lane >> 2), q4 = lane & 3;
         const uint8_t* blk = sm.code[c8] + kv * kCodeBytes + (r & ~(B - 1)) * (kHeadDim + 1);
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
         *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(row + (swizzle_chunk(r, 2 * q4 + 1) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
       }
-      u0 = u0 + 1 < kConvertWarps<MT, FP8> ? u0 + 1 : 0;
+      u0 = u0 + 1 < kConvertWarps<MT, FP8, kLanes> ? u0 + 1 : 0;
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) {
@@ -362,11 +363,11 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
         mbar_arrive(&sm.code_empty[c8]);
       }
     }
-  } else if (warp >= kIssuer0<MT, FP8>) {
+  } else if (warp >= kIssuer0<MT, FP8, kLanes>) {
     // ------------------------------------------------------------- MMA issuer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs<MT, FP8, kLanes>));
     {
-      const int li = warp - kIssuer0<MT, FP8>;
+      const int li = warp - kIssuer0<MT, FP8, kLanes>;
       const TokSpan span = lane_rows<TREE>(a, sm.work, sm.pos0, li % MT).span;
       const int nT = sm.j1 - sm.j0, j0 = sm.j0;
       const TokTiles tiles = sm.tiles;
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
       constexpr uint32_t kIdQK = idesc_bf16(128, kBN, false);
       constexpr uint32_t kIdPV = idesc_bf16(128, kHeadDim, true);
       const uint64_t qa = sdesc(smem_u32(&sm.q[li % MT][0]));
-      const uint32_t t_s = tmem + 64 * li, t_o = t_s + 64 * kLanes<MT, FP8>;
+      const uint32_t t_s = tmem + 64 * li, t_o = t_s + 64 * kLanes;
       uint32_t phase = 0;
       bool ok = true, busy = false;              // busy: a tile's P is to come
       uint32_t some = 0;                         // O holds something
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs<MT, FP8>));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs<MT, FP8, kLanes>));
     const int li = warp >> 2, m_blk = li % MT, part = li / MT;
     const int wq = warp & 3, r = wq * 32 + lane;           // row of the lane's 128
     const LaneRows rows = lane_rows<TREE>(a, sm.work, sm.pos0, m_blk);
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     if constexpr (TREE) {
       // what the nodes see of the tree, if the CTA has a tile that some of them do not see whole
       if (a.window > 0 || (sm.j1 > sm.j0 && tok_tile(sm.tiles, sm.j1 - 1) * kBN + kBN > sm.pos0)) {
-        constexpr int kMen = kSoftmaxWarps<MT, FP8> * 32;
+        constexpr int kMen = kSoftmaxWarps<MT, FP8, kLanes> * 32;
         load_parents(sm.tree, a.parents + sm.row0, w.p1 - sm.pos0 + 1, threadIdx.x, kMen, a.err);
         __syncwarp();
         asm volatile("bar.sync 2, %0;\n" ::"n"(kMen) : "memory");
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     };
     const uint32_t tmem = sm.tmem_base;
     const uint32_t t_lane = (uint32_t)(wq * 32) << 16;
-    const uint32_t t_s = tmem + t_lane + 64 * li, t_o = t_s + 64 * kLanes<MT, FP8>;
+    const uint32_t t_s = tmem + t_lane + 64 * li, t_o = t_s + 64 * kLanes;
     const float sl2 = a.scale_log2;
     float m_run = -INFINITY, l_run = 0.f;
     uint32_t n = 0;
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
     tc_fence_after();
     if (kParts > 1) {
       // ---- join the parts of the tiles: parts 1.. leave O, m and l to part 0
-      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps<MT, FP8> * 32) : "memory");   // the ring is free
+      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps<MT, FP8, kLanes> * 32) : "memory");   // the ring is free
       if (part > 0) {
 #pragma unroll
         for (int c = 0; c < kHeadDim; c += 16) {
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
         sm.ml[li][r][0] = m_run;
         sm.ml[li][r][1] = l_run;
       }
-      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps<MT, FP8> * 32) : "memory");
+      asm volatile("bar.sync 2, %0;\n" ::"r"(kSoftmaxWarps<MT, FP8, kLanes> * 32) : "memory");
     }
     if (alive && part == 0 && wq * 32 < rows.n) {
       float f0 = 1.f, fp[kParts];
@@ -651,32 +652,32 @@ __global__ void __launch_bounds__(kThreads<MT, FP8>, kCtasPerSm<MT, FP8>)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssuer0<MT, FP8>) {
+  if (warp == kIssuer0<MT, FP8, kLanes>) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tmem_base),
-                 "r"(kTmemCols<MT, FP8>));
+                 "r"(kTmemCols<MT, FP8, kLanes>));
   }
 }
 
-template <int MT, bool FP8, bool TREE>
+template <int MT, bool FP8, int kLanes, bool TREE>
 cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
-  constexpr int smem = (int)sizeof(TcSmem<MT, FP8, TREE>) + 1024;
-  static_assert((smem + 1024) * kCtasPerSm<MT, FP8> <= 228 * 1024, "shared memory per SM");
+  constexpr int smem = (int)sizeof(TcSmem<MT, FP8, kLanes, TREE>) + 1024;
+  static_assert((smem + 1024) * kCtasPerSm<MT, FP8, kLanes> <= 228 * 1024, "shared memory per SM");
   static std::atomic<unsigned long long> configured{0};   // a bit per device
   int dev = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (dev >= 64 || !(configured.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(token_tc_kernel<MT, FP8, TREE>,
+    const cudaError_t e = cudaFuncSetAttribute(token_tc_kernel<MT, FP8, kLanes, TREE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // a warpgroup that asks for more registers than the launch brought would wait for ever
     cudaFuncAttributes attr;
-    if (cudaError_t e2 = cudaFuncGetAttributes(&attr, token_tc_kernel<MT, FP8, TREE>)) return e2;
-    if (attr.numRegs < kLaunchRegs<MT, FP8>) return cudaErrorInvalidConfiguration;
+    if (cudaError_t e2 = cudaFuncGetAttributes(&attr, token_tc_kernel<MT, FP8, kLanes, TREE>)) return e2;
+    if (attr.numRegs < kLaunchRegs<MT, FP8, kLanes>) return cudaErrorInvalidConfiguration;
     if (dev < 64) configured.fetch_or(bit);
   }
-  const cudaError_t e = launch_pdl(token_tc_kernel<MT, FP8, TREE>, dim3(a.ctas), dim3(kThreads<MT, FP8>), smem, s, a);
+  const cudaError_t e = launch_pdl(token_tc_kernel<MT, FP8, kLanes, TREE>, dim3(a.ctas), dim3(kThreads<MT, FP8, kLanes>), smem, s, a);
   count_launches(1);
   return e;
 }
@@ -684,20 +685,20 @@ cudaError_t launch_tc(const TokenAttendArgs& a, cudaStream_t s) {
 template <bool TREE>
 cudaError_t launch_tc_rows(const TokenAttendArgs& a, cudaStream_t s) {
   if (a.pool.fp8)
-    return a.rows == 128   ? launch_tc<1, true, TREE>(a, s)
-           : a.rows == 256 ? launch_tc<2, true, TREE>(a, s)
-                           : launch_tc<4, true, TREE>(a, s);
-  return a.rows == 128 ? launch_tc<1, false, TREE>(a, s) : launch_tc<2, false, TREE>(a, s);
+    return a.rows == 128   ? (a.lanes == 2 ? launch_tc<1, true, 2, TREE>(a, s) : launch_tc<1, true, 4, TREE>(a, s))
+           : a.rows == 256 ? launch_tc<2, true, 4, TREE>(a, s)
+                           : launch_tc<4, true, 4, TREE>(a, s);
+  return a.rows == 128 ? launch_tc<1, false, 2, TREE>(a, s) : launch_tc<2, false, 2, TREE>(a, s);
 }
 
 }  // namespace
 
 int token_tc_max_rows(bool fp8) { return fp8 ? 512 : 256; }
 
-int token_tc_ctas_per_sm(bool fp8, int rows) { return fp8 ? 1 : rows == 256 ? kCtasPerSm<2, false> : kCtasPerSm<1, false>; }
+int token_tc_ctas_per_sm(int lanes) { return 4 / lanes; }
 
-double token_tc_tile_us(bool fp8, int rows) {
-  if (fp8) return rows == 128 ? 0.72 : rows == 256 ? 0.79 : 1.6;
+double token_tc_tile_us(bool fp8, int rows, int lanes) {
+  if (fp8) return rows == 128 ? (lanes == 2 ? 1.08 : 0.72) : rows == 256 ? 0.79 : 1.6;
   return rows == 128 ? 0.65 : 1.05;
 }
 

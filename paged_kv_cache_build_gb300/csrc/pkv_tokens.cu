@@ -121,8 +121,9 @@ double plan_splits(TokenAttendArgs* a, const int* first, const int* last, const 
 
 // The shares of an attention call in blocks of a kernel's shape (query rows a CTA) with their
 // splits; the estimate in us.
-double plan_shape(pkv_t h, TokenAttendArgs* a, bool few, int shape) {
+double plan_shape(pkv_t h, TokenAttendArgs* a, bool few, int shape, int lanes = 0) {
   a->rows = shape;
+  a->lanes = lanes;
   int first[kMaxTokenBatch], last[kMaxTokenBatch];
   for (int i = 0; i < a->n; ++i) {
     TokenQuery& it = a->item[i];
@@ -138,7 +139,7 @@ double plan_shape(pkv_t h, TokenAttendArgs* a, bool few, int shape) {
   const int room = std::min<int>(kTokenScratchBytes / (shape * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
   const CtaCost cost =
       few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), token_few_tile_us(shape), 12, 4, 8, room}
-          : CtaCost{h->num_sms * token_tc_ctas_per_sm(h->fp8, shape), token_tc_tile_us(h->fp8, shape), 10, 4, 8, room};
+          : CtaCost{h->num_sms * token_tc_ctas_per_sm(lanes), token_tc_tile_us(h->fp8, shape, lanes), 10, 4, 8, room};
   return plan_splits(a, first, last, cost);
 }
 
@@ -155,11 +156,16 @@ double plan_tc(pkv_t h, TokenAttendArgs* a) {
   // tokens 44 / 36 us, 8 of 4001 27 / 21 us, 16 of them 36 / 39 us; one of 131072 tokens, group 8,
   // 140 / 150 us.
   if (!h->fp8 && shape == 256) {
-    const double narrow = plan_shape(h, a, false, 128), wide = plan_shape(h, a, false, 256);
+    const double narrow = plan_shape(h, a, false, 128, 2), wide = plan_shape(h, a, false, 256, 2);
     if (wide <= narrow) return wide;
     shape = 128;
   }
-  return plan_shape(h, a, false, shape);
+  if (h->fp8 && shape == 128) {
+    const double two = plan_shape(h, a, false, 128, 2), four = plan_shape(h, a, false, 128, 4);
+    if (four <= two) return four;
+    return plan_shape(h, a, false, 128, 2);
+  }
+  return plan_shape(h, a, false, shape, h->fp8 ? 4 : 2);
 }
 
 // The rotation as the kernel takes it: whole turns do not matter for whole positions, so a

@@ -87,6 +87,7 @@ struct TokenAttendArgsOf {
   int n;
   int ctas;
   int rows;                         // query rows per CTA
+  int lanes;                        // matrix-unit kernel: its lanes per CTA, 2 or 4
   TokenQuery item[kStreams];
 };
 using TokenAttendArgs = TokenAttendArgsOf<kMaxTokenBatch>;
@@ -268,9 +269,9 @@ inline double token_few_tile_us(int rows) { return rows == 24 ? 0.8 : 0.55; }
 int token_few_ctas_per_sm();
 // Attention of 128, 256 or (on E4M3 pages) 512 query rows per CTA (a.rows).
 int token_tc_max_rows(bool fp8);
-int token_tc_ctas_per_sm(bool fp8, int rows);
+int token_tc_ctas_per_sm(int lanes);
 // What a 64-slot tile takes a CTA of it, in us, beside the SM's others.
-double token_tc_tile_us(bool fp8, int rows);
+double token_tc_tile_us(bool fp8, int rows, int lanes);
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s);
 // Joins the splits of the items that have several (launch_token_few does so itself).
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s);
