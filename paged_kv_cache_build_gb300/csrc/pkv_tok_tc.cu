@@ -699,7 +699,7 @@ int token_tc_ctas_per_sm(int lanes) { return 4 / lanes; }
 
 double token_tc_tile_us(bool fp8, int rows, int lanes) {
   if (fp8) return rows == 128 ? (lanes == 2 ? 1.08 : 0.72) : rows == 256 ? 0.79 : 1.6;
-  return rows == 128 ? 0.65 : 1.05;
+  return rows == 128 ? 0.62 : 1.05;
 }
 
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s) {
