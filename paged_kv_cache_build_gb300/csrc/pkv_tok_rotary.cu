@@ -141,7 +141,7 @@ struct Open {
 };
 constexpr int kOpen = 64;            // of a warp (what does not fit is settled at once)
 
-template <bool FP8, int U, typename Args>
+template <bool FP8, typename Args>
 __global__ void __launch_bounds__(kWarps * 32, FP8 ? 5 : 8)
     token_append_rotary_kernel(const __grid_constant__ Args a, const __grid_constant__ RotaryArgs r, int shares) {
   // each warp's: cosines and sines by [token][pair], and planes on their way, a lane's part in
@@ -232,145 +232,110 @@ __global__ void __launch_bounds__(kWarps * 32, FP8 ? 5 : 8)
                      : (long long)slot * kHeadDim * 2 + (swizzle_chunk(slot, c) << 4));
   const long long exp = fp8_exp_off(H, Ps, 0, 0, slot) - fp8_code_off(H, Ps, 0, 0, slot);   // (of chunk 0)
   uint16_t* q_to = r.q_out + (src * r.q_heads + max(h0 - H, 0)) * kHeadDim + 8 * c;
-  // U planes at a time, two where a warp has many, so that their chains of shuffles run side by
-  // side; `second`: there are two.
+  // the next plane
   int at = 0;
-  const auto take = [&](uint4 (&v)[U], bool second) {
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(kFlight - U) : "memory");
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
-                   : "=r"(v[u].x), "=r"(v[u].y), "=r"(v[u].z), "=r"(v[u].w)
-                   : "r"(place + (at + u) % kFlight * 512)
-                   : "memory");
-      if (u == 1 && !second) v[u] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    at += second ? 2 : 1;
+  const auto take = [&]() {
+    uint4 v;
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(kFlight - 1) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(place + at % kFlight * 512)
+                 : "memory");
+    ++at;
     fetch();
-    if (second) fetch();
+    return v;
   };
-  const auto turned = [&](const float (&x)[8], const float (&p)[8], float2 (&y)[4]) {
+  const auto turned = [&](const uint4& v, float (&x)[8], float (&p)[8], float2 (&y)[4]) {
+    unpack(v, x);
+    unpack(partners(v, r.distance), p);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       y[i] = fma2(x[2 * i], x[2 * i + 1], cs[i], mul2(p[2 * i], p[2 * i + 1], sn[i]));
   };
   const auto rounded = [&](const uint4& v) {
-    const uint4 vp = partners(v, r.distance);
     float x[8], p[8];
     float2 y[4];
-    unpack(v, x);
-    unpack(vp, p);
-    turned(x, p, y);
+    turned(v, x, p, y);
     return make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[1].x, y[1].y), pack_bf16(y[2].x, y[2].y),
                       pack_bf16(y[3].x, y[3].y));
   };
-  const auto store8 = [&](uint8_t* dst, const uint2& codes, int e) {
-    *reinterpret_cast<uint2*>(dst) = codes;
-    if (c == 0) dst[exp] = (uint8_t)(int8_t)e;
+  const auto store8 = [&](const uint2& codes, int e) {
+    if (page < 0) return;
+    *reinterpret_cast<uint2*>(to) = codes;
+    if (c == 0) to[exp] = (uint8_t)(int8_t)e;
   };
   int hh = h0;
 #pragma unroll 1
-  for (const int end = min(h1, H); hh < end; hh += U, to += U * plane) {
-    uint4 v[U];
-    const bool second = U == 2 && hh + 1 < end;
-    take(v, second);
+  for (const int end = min(h1, H); hh < end; ++hh, to += plane) {
+    const uint4 v = take();
     if constexpr (!FP8) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const uint4 out = rounded(v[u]);
-        if (page >= 0 && (u == 0 || second)) *reinterpret_cast<uint4*>(to + u * plane) = out;
-      }
+      const uint4 out = rounded(v);
+      if (page >= 0) *reinterpret_cast<uint4*>(to) = out;
     } else {
-      float x[U][8], p[U][8], big[U];
-      float2 y[U][4];
-      int e[U];
-      unsigned open = 0;
+      float x[8], p[8], big = 0.f;
+      float2 y[4];
+      turned(v, x, p, y);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        unpack(v[u], x[u]);
-        unpack(partners(v[u], r.distance), p[u]);
-        turned(x[u], p[u], y[u]);
-        big[u] = 0.f;
+      for (int i = 0; i < 4; ++i) big = fmaxf(big, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) big[u] = fmaxf(big[u], fmaxf(fabsf(y[u][i].x), fabsf(y[u][i].y)));
-#pragma unroll
-        for (int s = 1; s < 8; s <<= 1) big[u] = fmaxf(big[u], __shfl_xor_sync(0xffffffffu, big[u], s));
-        // The exponent (fp8_row_exponent): the bits' one, one more where the fraction is above
-        // 0.75, a carry. A pair keeps its length, so |x| + |p| is at most twice the larger of its
-        // two values: big is off by 2^-20 of it, 16 of its last places; 20 from a carry it is open.
-        const uint32_t b = __float_as_uint(big[u]) + 0x1FFFFFu;
-        e[u] = big[u] > 0.f ? max((int)(b >> 23) - 135, -126) : 0;
-        open |= (unsigned)(((b + 20u) & 0x7FFFFFu) < 41u) << u;
-      }
-      if (__any_sync(0xffffffffu, open != 0)) {
+      for (int s = 1; s < 8; s <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
+      // The exponent (fp8_row_exponent): the bits' one, one more where the fraction is above
+      // 0.75, a carry. A pair keeps its length, so |x| + |p| is at most twice the larger of its
+      // two values: big is off by 2^-20 of it, 16 of its last places; 20 from a carry it is open.
+      const uint32_t b = __float_as_uint(big) + 0x1FFFFFu;
+      int e = big > 0.f ? max((int)(b >> 23) - 135, -126) : 0;
+      const bool open = ((b + 20u) & 0x7FFFFFu) < 41u;
+      if (__any_sync(0xffffffffu, open)) {
         // one value in doubles, or few, says whether the row's largest is above 448 x 2^e, e the
         // smaller of the two
+        bool above = false;
+        if (open) {
+          e = max((int)((b - 20u) >> 23) - 135, -126);
+          const double border = 448.0 * power_of_two(e);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          bool above = false;
-          if ((open >> u) & 1u) {
-            const int low = max((int)((__float_as_uint(big[u]) + 0x1FFFFFu - 20u) >> 23) - 135, -126);
-            const double border = 448.0 * power_of_two(low);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (fabsf(i & 1 ? y[u][i >> 1].y : y[u][i >> 1].x) > big[u] * (1.f - 0x1p-18f))
-                above |= fabs(turned_exactly(r, position, 8 * c + i, x[u][i], p[u][i])) > border;
-            e[u] = low;
-          }
-          if ((__ballot_sync(0xffffffffu, above) >> (lane & 24)) & 0xFFu) ++e[u];
+          for (int i = 0; i < 8; ++i)
+            if (fabsf(i & 1 ? y[i >> 1].y : y[i >> 1].x) > big * (1.f - 0x1p-18f))
+              above |= fabs(turned_exactly(r, position, 8 * c + i, x[i], p[i])) > border;
         }
+        if ((__ballot_sync(0xffffffffu, above) >> (lane & 24)) & 0xFFu) ++e;
       }
-      uint2 codes[U], other[U];
-      unsigned some = 0;
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23), d = inv * off;
+      uint32_t lo[4], differ[4];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float inv = __uint_as_float((uint32_t)(127 - e[u]) << 23), d = inv * off;
-        uint32_t lo[4], differ[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float s0 = fabsf(x[u][2 * i]) + fabsf(p[u][2 * i]);
-          const float s1 = fabsf(x[u][2 * i + 1]) + fabsf(p[u][2 * i + 1]);
-          // (a zero's sign goes, so that pairs of zeros are settled)
-          const float2 z = fma2(y[u][i].x, y[u][i].y, make_float2(inv, inv), make_float2(0.f, 0.f));
-          const float2 l = fma2(s0, s1, make_float2(-d, -d), z), h = fma2(s0, s1, make_float2(d, d), z);
-          lo[i] = fp8_pack2(l.x, l.y);
-          differ[i] = lo[i] ^ fp8_pack2(h.x, h.y);
-        }
-        codes[u] = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-        other[u] = make_uint2(differ[0] | (differ[1] << 16), differ[2] | (differ[3] << 16));
-        some |= (other[u].x | other[u].y) != 0;
+      for (int i = 0; i < 4; ++i) {
+        const float s0 = fabsf(x[2 * i]) + fabsf(p[2 * i]), s1 = fabsf(x[2 * i + 1]) + fabsf(p[2 * i + 1]);
+        // (a zero's sign goes, so that pairs of zeros are settled)
+        const float2 z = fma2(y[i].x, y[i].y, make_float2(inv, inv), make_float2(0.f, 0.f));
+        const float2 l = fma2(s0, s1, make_float2(-d, -d), z), h = fma2(s0, s1, make_float2(d, d), z);
+        lo[i] = fp8_pack2(l.x, l.y);
+        differ[i] = lo[i] ^ fp8_pack2(h.x, h.y);
       }
-      if (some) {
+      uint2 codes = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+      if (differ[0] | differ[1] | differ[2] | differ[3]) {
         // the lane's open elements go to the list, for a lane each behind the K planes
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8; ++i) {
+          if (((differ[i >> 1] >> (8 * (i & 1))) & 0xFFu) == 0) continue;
+          const int k = atomicAdd(&n_open[warp], 1);
+          if (k < kOpen) {
+            Open o;
+            o.values = (__float_as_uint(x[i]) >> 16) | (__float_as_uint(p[i]) & 0xFFFF0000u);
+            o.plane = page >= 0 ? hh : -1;
+            o.token = (uint8_t)q4;
+            o.element = (uint8_t)(8 * c + i);
+            o.exponent = (int8_t)e;
+            open_list[warp][k] = o;
+          } else {
+            const double exact = turned_exactly(r, position, 8 * c + i, x[i], p[i]);
             const uint32_t sh = 8 * (i & 3);
-            if ((((i < 4 ? other[u].x : other[u].y) >> sh) & 0xFFu) == 0) continue;
-            const int k = atomicAdd(&n_open[warp], 1);
-            if (k < kOpen) {
-              Open o;
-              o.values = (__float_as_uint(x[u][i]) >> 16) | (__float_as_uint(p[u][i]) & 0xFFFF0000u);
-              o.plane = page >= 0 && (u == 0 || second) ? hh + u : -1;
-              o.token = (uint8_t)q4;
-              o.element = (uint8_t)(8 * c + i);
-              o.exponent = (int8_t)e[u];
-              open_list[warp][k] = o;
-            } else {
-              const double exact = turned_exactly(r, position, 8 * c + i, x[u][i], p[u][i]);
-              uint32_t& word = i < 4 ? codes[u].x : codes[u].y;
-              word = (word & ~(0xFFu << sh)) | code_of(exact * power_of_two(-e[u])) << sh;
-            }
+            uint32_t& word = i < 4 ? codes.x : codes.y;
+            word = (word & ~(0xFFu << sh)) | code_of(exact * power_of_two(-e)) << sh;
           }
         }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (page >= 0 && (u == 0 || second)) store8(to + u * plane, codes[u], e[u]);
+      store8(codes, e);
     }
   }
-  if (h0 < H && hh > min(h1, H)) to -= plane;    // behind an odd one
   if constexpr (FP8) {
     // what is open, a lane each
     __syncwarp();
@@ -393,46 +358,28 @@ __global__ void __launch_bounds__(kWarps * 32, FP8 ? 5 : 8)
       }
     }
   }
-  hh = max(h0, min(hh, H));
 #pragma unroll 1
-  for (const int end = min(h1, turning); hh < end; hh += U, q_to += U * kHeadDim) {
-    uint4 v[U];
-    const bool second = U == 2 && hh + 1 < end;
-    take(v, second);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint4 out = rounded(v[u]);
-      if (row && (u == 0 || second)) *reinterpret_cast<uint4*>(q_to + u * kHeadDim) = out;
-    }
+  for (const int end = min(h1, turning); hh < end; ++hh, q_to += kHeadDim) {
+    const uint4 out = rounded(take());
+    if (row) *reinterpret_cast<uint4*>(q_to) = out;
   }
-  hh = max(h0, min(hh, turning));
 #pragma unroll 1
-  for (; hh < h1; hh += U, to += U * plane) {
-    uint4 v[U];
-    const bool second = U == 2 && hh + 1 < h1;
-    take(v, second);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool there = page >= 0 && (u == 0 || second);
-      if constexpr (FP8) {
-        int e;
-        const uint2 codes = quantise8(v[u], &e);
-        if (there) store8(to + u * plane, codes, e);
-      } else if (there) {
-        *reinterpret_cast<uint4*>(to + u * plane) = v[u];
-      }
+  for (; hh < h1; ++hh, to += plane) {
+    const uint4 v = take();
+    if constexpr (FP8) {
+      int e;
+      const uint2 codes = quantise8(v, &e);
+      store8(codes, e);
+    } else if (page >= 0) {
+      *reinterpret_cast<uint4*>(to) = v;
     }
   }
 }
 
-template <bool FP8, int U, typename Args>
-cudaError_t launch_rotary(const Args& a, const RotaryArgs& r, int blocks, int shares, cudaStream_t s) {
-  return launch_pdl(token_append_rotary_kernel<FP8, U, Args>, dim3(blocks), dim3(kWarps * 32), 0, s, a, r, shares);
-}
 template <typename Args>
-cudaError_t launch_rotary_args(const Args& a, const RotaryArgs& r, int blocks, int shares, bool one, cudaStream_t s) {
-  if (one) return a.pool.fp8 ? launch_rotary<true, 1>(a, r, blocks, shares, s) : launch_rotary<false, 1>(a, r, blocks, shares, s);
-  return a.pool.fp8 ? launch_rotary<true, 2>(a, r, blocks, shares, s) : launch_rotary<false, 2>(a, r, blocks, shares, s);
+cudaError_t launch_rotary(const Args& a, const RotaryArgs& r, int blocks, int shares, cudaStream_t s) {
+  return a.pool.fp8 ? launch_pdl(token_append_rotary_kernel<true, Args>, dim3(blocks), dim3(kWarps * 32), 0, s, a, r, shares)
+                    : launch_pdl(token_append_rotary_kernel<false, Args>, dim3(blocks), dim3(kWarps * 32), 0, s, a, r, shares);
 }
 
 }  // namespace
@@ -440,13 +387,15 @@ cudaError_t launch_rotary_args(const Args& a, const RotaryArgs& r, int blocks, i
 cudaError_t launch_token_append_rotary(const TokenRowsArgs& a, const RotaryArgs& r, cudaStream_t s) {
   const long long quads = ((long long)a.units + kQuad - 1) / kQuad;
   const int planes = 2 * a.pool.heads + r.q_heads;
-  // few tokens: a plane a warp; else enough warps for the SMs, so that angles are shared
+  // Few tokens: a plane a warp. Else so many warps an SM, each with an equal share of the planes: angles
+  // cost a warp what 5 to 10 planes do, but on bf16 pages one warp's loads and products run beside
+  // another's angles (13754 tokens, 48 planes, 24 / 96 / 192 warps an SM: 31.1 / 28.7 / 35.2 us; 10992
+  // tokens on E4M3 pages 29.1 / 42 / 52 us).
   const long long want = 152 * (a.pool.fp8 ? 24 : 96);
   const int shares = (int)std::max<long long>(1, std::min<long long>(planes, want / quads));
   const int blocks = (int)((quads * shares + kWarps - 1) / kWarps);
-  const bool one = shares == planes;
-  const cudaError_t e = a.n <= kSmallTokenBatch ? launch_rotary_args(small_args(a), r, blocks, shares, one, s)
-                                                : launch_rotary_args(a, r, blocks, shares, one, s);
+  const cudaError_t e = a.n <= kSmallTokenBatch ? launch_rotary(small_args(a), r, blocks, shares, s)
+                                                : launch_rotary(a, r, blocks, shares, s);
   count_launches(1);
   return e;
 }
