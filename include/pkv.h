@@ -504,10 +504,10 @@ typedef struct {
  * orders tokens by slots alone (drafted tokens of a tree share positions, pkv_attend_tree).
  * q: device bf16 [row_off[n]][q_heads][64], rows q_stride apart (0: contiguous); q_out: the
  * same, contiguous; it may be q itself where that is contiguous, and overlaps nothing else.
- * q_heads = 0: no q (q and q_out are not used). freq / 2 pi is kept to 2^-65 of a turn, and whole
+ * q_heads = 0: no q (q and q_out are not used). freq / 2 pi is kept to 2^-64 of a turn, and whole
  * turns are taken off exactly; sines, cosines and sums are fp32, and what is stored is rounded
  * once: to bf16, or, on an E4M3 cache, to the codes and exponent of the row as turned (those of
- * the exact values, but where these lie within |position| 2^-62 + 2^-48 of a border of two codes,
+ * the exact values, but where these lie within |position| 2^-61 + 2^-48 of a border of two codes,
  * relatively). Slots, pages, layers and the rest are as in pkv_append_tokens; k must stay below
  * 2^125 in magnitude.
  * Errors: as pkv_append_tokens; INVALID for a null rotary or one outside its limits, q_heads
@@ -561,9 +561,9 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* stream_ids, const int* pos
  * stream's first `sinks` tokens stay visible beside it.
  * q: device bf16 [row_off[n]][q_heads][64], rows q_stride apart; out: the same,
  * contiguous. A call takes fewer than 2^27 rows x q_heads. fp32 accumulation and softmax;
- * the probabilities are rounded to bf16 for the second product, or, in streams with few
- * rows x query heads per KV head
- * (up to 64) on E4M3 pages, to f16 (and q as well), which loses what is below 2^-39 of an
+ * the probabilities are rounded to bf16 for the second product, or, on E4M3 pages, in streams
+ * with few rows x query heads per KV head (up to 64) to f16 (and q as well; not where the call's
+ * other streams bring them all into one launch), which loses what is below 2^-39 of an
  * output row's largest contribution. sm_scale <= 0 means 1 / sqrt(64).
  * Results depend on the batch only by rounding (the kernel and the split of the keys
  * are chosen for the whole call) and are the same bits for the same call. The

@@ -8,6 +8,7 @@
 // and the live ones 0 .. min(keep0, n_pages)-1 and gap1 .. n_pages-1.
 #pragma once
 
+#include <cmath>
 #include <stdint.h>
 
 #ifndef PKV_HD
@@ -157,6 +158,22 @@ PKV_HD uint64_t tok_mask(int b, int p, int window, int sinks) {
   return tok_low_bits(p - b + 1) & (~tok_low_bits(tok_window_lo(p, window) - b) | tok_low_bits(sinks - b));
 }
 
+
+// ---------------------------------------------------------- rotary positions
+// Turns per unit of position of a frequency in radians, 2^64 to the turn, to 1.1 of these: whole
+// turns do not matter for whole positions, so position x this, in 64-bit arithmetic that wraps,
+// is the angle, for every 32-bit position. |freq| <= 2^20. freq / 2 pi is taken with twice a
+// double's digits; t is volatile because a compiler that contracts freq * inv - rint(t) would
+// count what t rounds off twice.
+inline uint64_t rotary_turn(double freq) {
+  const double inv = 0.15915494309189535, inv_low = -9.839338337591243e-18;   // 1 / 2 pi
+  const double two64 = 18446744073709551616.0;
+  const volatile double t = freq * inv;
+  const double low = std::fma(freq, inv, -t) + freq * inv_low;
+  const double part = t - std::rint(t);          // exact, within half a turn
+  const uint64_t high = part == 0.5 ? 1ull << 63 : (uint64_t)std::llrint(part * two64);
+  return high + (uint64_t)std::llrint(low * two64);
+}
 
 // ---------------------------------------------------------- trees of drafted tokens
 // A stream's last n tokens, slots pos0 .. pos0 + n - 1, are the nodes of a tree: node i's

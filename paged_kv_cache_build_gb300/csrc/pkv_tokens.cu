@@ -191,9 +191,7 @@ double plan_tc(pkv_t h, TokenAttendArgs* a) {
   return plan_shape(h, a, false, shape, h->fp8 ? 4 : 2);
 }
 
-// The rotation as the kernel takes it: whole turns do not matter for whole positions, so a
-// pair's angle is position x turn in 64-bit arithmetic that wraps, 2^64 to the turn, exact for
-// every 32-bit position. freq / 2 pi is taken with twice a double's digits.
+// The rotation as the kernel takes it.
 pkv_status rotary_args(pkv_t h, const pkv_rotary* r, RotaryArgs* a) {
   if (!r) return fail(h, PKV_ERR_INVALID, "null rotary");
   if (r->axes < 1 || r->axes > kMaxAxes)
@@ -209,13 +207,7 @@ pkv_status rotary_args(pkv_t h, const pkv_rotary* r, RotaryArgs* a) {
       return fail(h, PKV_ERR_INVALID, "pair %d: axis %d of %d", i, r->axis[i], r->axes);
     if (!(std::fabs(r->freq[i]) <= kMaxFreq))
       return fail(h, PKV_ERR_INVALID, "pair %d: a frequency of %g (at most %g in magnitude)", i, r->freq[i], kMaxFreq);
-    const double inv = 0.15915494309189535, inv_low = -9.839338337591243e-18;   // 1 / 2 pi
-    const double t = r->freq[i] * inv;
-    const double low = std::fma(r->freq[i], inv, -t) + r->freq[i] * inv_low;
-    const double part = t - std::rint(t);        // exact, within half a turn
-    const double two64 = 18446744073709551616.0;
-    a->turn[i] = (part == 0.5 ? 1ull << 63 : (unsigned long long)std::llrint(part * two64)) +
-                 (unsigned long long)std::llrint(low * two64);
+    a->turn[i] = rotary_turn(r->freq[i]);
     a->axis[i] = (uint8_t)r->axis[i];
   }
   return PKV_OK;

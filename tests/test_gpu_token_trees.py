@@ -6,8 +6,9 @@ the same bound (test_gpu_tokens). A rotated value y = x_a cos - x_b sin stored i
 half a step (2^-8 |y|), and before that off by fp32's cosine and sine (2^-22, angles cut to
 2^-32 of a turn and rounded once among it) and three roundings: 2^-21 (|x_a| + |x_b|). E4M3 rows are held to
 the codes of the exact values, or of values next to them that lie on the other side of a border: a
-frequency is kept to 2^-65 of a turn, so that an angle is off by position x 2^-65 x 2 pi < position x
-2^-62, and doubles add a few 2^-53: (position x 2^-62 + 2^-48) (|x_a| + |x_b|)."""
+frequency is kept to 1.1 x 2^-64 of a turn (two roundings to half of that), so that an angle is off by
+position x 1.1 x 2^-64 x 2 pi < position x 2^-61, and doubles add a few 2^-53:
+(position x 2^-61 + 2^-48) (|x_a| + |x_b|)."""
 
 import numpy as np
 import pytest
@@ -225,7 +226,7 @@ def check_rotary(p, sids, counts, positions, freq, axis, distance, group, layer=
         size = np.zeros_like(x64)
         size[..., first] = size[..., first + distance] = np.abs(x64[..., first]) + np.abs(x64[..., first + distance])
         if x is k and p.fp8:
-            got, near = f64(y), size * (np.abs(positions).max() * 2.0 ** -62 + 2.0 ** -48)
+            got, near = f64(y), size * (np.abs(positions).max() * 2.0 ** -61 + 2.0 ** -48)
             other = (got != stored64(want)) & (got != stored64(want - near)) & (got != stored64(want + near))
             assert not other.any(), (got[other], want[other])
             continue

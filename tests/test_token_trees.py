@@ -136,6 +136,31 @@ def test_the_oracles_rotation(distance):
     assert np.count_nonzero(got) == 2
 
 
+@pytest.mark.parametrize("flags", [[], ["-ffp-contract=fast", "-mfma"]], ids=["plain", "contracted"])
+def test_frequencies_to_turns(tmp_path, flags):
+    """freq / 2 pi to 1.1 x 2^-64 of a turn, against fractions, also where the compiler fuses
+    products and sums (as it does on Arm)."""
+    import platform
+    from fractions import Fraction
+    from oracle.tokens import TWO_PI
+    if platform.machine() != "x86_64":
+        flags = [f for f in flags if f != "-mfma"]
+    src, so = str(tmp_path / "turn.cpp"), str(tmp_path / "turn.so")
+    with open(src, "w") as f:
+        f.write('#include "pkv_token_plan.h"\nextern "C" uint64_t turn(double f) { return pkv::rotary_turn(f); }\n')
+    subprocess.run(["g++", "-std=c++17", "-O3", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC] + flags + [src, "-o", so],
+                   check=True)
+    turn = ctypes.CDLL(so).turn
+    turn.restype, turn.argtypes = ctypes.c_uint64, [ctypes.c_double]
+    rng = random.Random(0)
+    freqs = [0.0, 1.0, -1.0, np.pi, 2 * np.pi, -np.pi, 4 * np.pi, 1e-30, -1e-30, 2.0 ** 20, -2.0 ** 20, 2.0 ** -64, 1e-5]
+    freqs += [10000.0 ** (-i / 32) for i in range(32)] + [rng.uniform(-1, 1) * 2.0 ** rng.uniform(-40, 20) for _ in range(500)]
+    for f in freqs:
+        exact = Fraction(float(f)) / Fraction(TWO_PI) * 2 ** 64
+        off = (Fraction(turn(f)) - exact + 2 ** 63) % 2 ** 64 - 2 ** 63
+        assert abs(off) <= Fraction(11, 10), f     # two roundings to whole numbers, and the digits' end
+
+
 # --------------------------------------------------------- the library's host code
 def numbers(n, fill=0):
     import torch
