@@ -1,6 +1,9 @@
 // Causal attention of a token stream's last tokens over its pages, for few query
 // rows per KV head: single tokens, drafted tokens to verify, short chunks. With a
-// window, a query at position p sees j > p - window and j < sinks; always j <= p.
+// window, a query at position p sees j > p - window and j < sinks; always j <= p. TREE: the rows
+// are the nodes of a drafted tree (pkv_attend_tree); what each sees of the tree's slots is walked
+// out of the parents while the first tiles come (a tree of 16 nodes over 776 tokens 7.6 us,
+// as a chain in the causal kernel 7.0).
 //
 //   out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),   s_j = log2(e) sm_scale q . k_j
 //

@@ -337,14 +337,13 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
   // the streams' rows per KV head decide on the kernel
   cudaStream_t s = as_stream(cuda_stream);
   const int n_items = a.n;
-  long long rows_sum = 0, most = 0;
+  long long few_ctas = 0, most = 0;
   int n_small = 0;
   for (int i = 0; i < n_items; ++i) {
     const long long r = (long long)a.item[i].n * group;
-    if (r <= kTokenFewRows) rows_sum += r, ++n_small;
+    if (r <= kTokenFewRows) few_ctas += (long long)ceil_div(r, 16) * h->H;
   }
-  const int few_rows = rows_sum <= (long long)kTokenFewRowsAll * n_small ? kTokenFewRows : kTokenFewRowsAll;
-  n_small = 0;
+  const int few_rows = few_ctas <= h->num_sms ? kTokenFewRows : kTokenFewRowsAll;
   for (int i = 0; i < n_items; ++i) {
     const long long r = (long long)a.item[i].n * group;
     if (r <= few_rows) ++n_small, most = std::max(most, r);

@@ -253,13 +253,13 @@ cudaError_t launch_token_read(const TokenRowsArgs& a, cudaStream_t s);
 cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s);
 
 // Attention in blocks of 8, 16 or 24 query rows (a.rows). A stream of more rows reads its keys
-// once a block, from L2 but for the first, so this kernel takes at most kTokenFewRowsAll of
-// them per KV head, or kTokenFewRows where the streams up to that size have no more than
-// kTokenFewRowsAll on average. (16 streams of 4001 tokens, 8 KV heads, all of them with
-// 32 / 48 / 64 rows: 29.5 / 52.4 / 49.7 us on bf16 pages and 41 / 75 / 80 us on E4M3 pages
-// against 31.8 and 53 us in launch_token_tc's blocks of 128 rows. Streams of 500 .. 4001
-// tokens, with 32 / 4 .. 48 / 4 .. 64 rows: 28 / 25 / 33 against 32 / 40 / 40 us, and on
-// E4M3 pages 36 / 40 / 46 against 46 / 54 / 55 us.)
+// once a block, from L2 but for the first, so this kernel takes streams of at most
+// kTokenFewRowsAll rows per KV head, or of kTokenFewRows where all such blocks of 16 run at once,
+// one an SM. (16 streams of 4001 tokens, 8 KV heads, 32 / 48 / 64 rows: 28 / 51 / 49 us on bf16
+// pages and 39 / 72 / 77 us on E4M3 pages, in launch_token_tc's blocks of 128 rows 33 / 34 / 34 and 50 /
+// 51 / 51 us; streams of 500 .. 4001 tokens with 4 .. 48 / 4 .. 64 rows: 25 / 32 against 24 / 24
+// us, on E4M3 pages 37 / 45 against 32 / 33 us. One stream of 4000 tokens, 48 / 64 rows: 11.1 / 11.3
+// against 13.2 us, on E4M3 pages 14.7 / 14.8 against 16.5; four of 2000: 11.5 / 13.0 against 12.4.)
 constexpr int kTokenFewRows = 64;
 constexpr int kTokenFewRowsAll = 32;
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s);
