@@ -642,3 +642,56 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(k2, kk[rows]) and torch.equal(v2, vv[rows])
     cache.sync()
     cache.close()
+
+
+@FP8
+@pytest.mark.parametrize("heads,group,past,nodes", [
+    (4, 4, [190 + 7 * i for i in range(40)], [9 + i % 3 for i in range(40)]),       # blocks of 128 rows in many CTAs
+    (8, 2, [300] * 20 + [2500], [1 + i % 8 for i in range(20)] + [70]),             # few and many rows
+    (8, 1, [1500] * 60 + [40], [1] * 60 + [200]),                                   # mostly single nodes
+    (2, 4, [2000, 9, 640, 5000], [16, 64, 33, 3]),                                  # unequal, split
+    (8, 3, [4100, 3000], [5, 15]),                                                  # 15 and 45 rows, alone on the card
+    (1, 8, [9000], [200]),
+], ids=["many", "mixed", "single nodes", "unequal", "alone", "large"])
+def test_batches_of_every_shape(heads, group, past, nodes, fp8):
+    """Batches that take each kernel, alone and together, with few and many CTAs."""
+    rng = np.random.default_rng(sum(nodes))
+    p = Pool(sum(-(-(a + b) // 64) for a, b in zip(past, nodes)) + 2, 64, heads, fp8, max_streams=64)
+    sids = [p.open(a + b) for a, b in zip(past, nodes)]
+    p.append(sids, past)
+    p.append(sids, nodes)
+    check_tree(p, sids, [random_parents(rng, n) for n in nodes], group)
+    check_tree(p, sids, [random_parents(rng, n) for n in nodes], group, 300, 70)
+    p.check_attend(sids, nodes, group)
+    p.cache.close()
+
+
+@FP8
+def test_two_graphs_of_one_handle(fp8):
+    """Two captured tree calls share the handle's partial results and counters: replayed in turn
+    they give what the calls give."""
+    rng = np.random.default_rng(2)
+    p = Pool(300, 16, 2, fp8)
+    sids = [p.open(), p.open()]
+    p.append(sids, [3000, 900])
+    calls = []
+    p.append(sids, [40, 5])
+    for sid, n, group in ((sids[0], 40, 4), (sids[1], 5, 2)):
+        batch, q = p.cache.token_batch([sid], [n]), p.rows(n, 2 * group)
+        calls.append((batch, q, ints(random_parents(rng, n))))
+    eager = [p.cache.attend_tree(*c) for c in calls]
+    graphs, outs = [], []
+    for c in calls:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(p.cache.attend_tree(*c))
+        graphs.append(g)
+        torch.cuda.current_stream().wait_stream(s)
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], eager[i])
+    p.cache.sync()
+    p.cache.close()

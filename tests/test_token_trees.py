@@ -380,3 +380,29 @@ def test_calls_are_accepted_as_the_page_state_allows(lib, cache, seed):
             free = ctypes.c_int()
             lib.pkv_free_pages(cache.h, ctypes.byref(free))
             assert (cache.token_info(i)[0], free.value) == (st["len"], len(ora.free))
+
+
+def test_outputs_of_a_side_streams_call_are_allocated_for_it(lib, cache, monkeypatch):
+    """A block from the current stream's pool may still be in use there."""
+    import contextlib
+    import torch
+    from paged_kv_cache_build_gb300 import Rotary
+    b = cache.token_batch([cache.open_token_stream(100)], [3])
+    s, on, made = HostStream(), [None], []
+
+    @contextlib.contextmanager
+    def stream(x):
+        on[0] = x
+        yield
+        on[0] = None
+
+    def alloc(like, **kw):
+        made.append(on[0])
+        return rows(*like[:2])
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    positions, q, k, parents = numbers(3), rows(3, 4), rows(3, 2), numbers(3, -1)
+    monkeypatch.setattr(torch, "empty", alloc)
+    assert cache.append_tokens_rotary(b, k, k, positions, Rotary([1.0] * 32), q=q, stream=s).shape == (3, 4, 64)
+    assert cache.attend_tree(b, q, parents, stream=s).shape == (3, 4, 64)
+    assert made == [s, s]
