@@ -532,8 +532,8 @@ pkv_status pkv_drop_tokens(pkv_t h, int n, const int* stream_ids, const int* cou
  * those numbered kept[keep_off[i]] .. kept[keep_off[i + 1] - 1] stay: in every layer their K and
  * V rows move, as they are stored, to the first of these tokens' slots, and the stream is that
  * much shorter. keep_off: n + 1 host ints that start at 0; kept: device int32, rising strictly
- * within a stream (NULL where nothing stays). Pages left empty go back on the free stack, the last stream's first. The next append on layer > 0
- * needs one on layer 0 first, as after a drop.
+ * within a stream (NULL where nothing stays). Pages left empty go back on the free stack, the
+ * last stream's first. The next append on layer > 0 needs one on layer 0 first, as after a drop.
  * A kept number out of its range or order is noted (pkv_sync: DEVICE) and leaves the
  * rows of its stream undefined; no other memory is touched.
  * Errors: INVALID (offsets, more to keep than tokens, more tokens than the stream has, a
@@ -580,8 +580,9 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
  * nodes of a tree: parents[r] (device int32 [row_off[n]]) is the number, from 0 within the
  * stream's rows, of row r's parent, which comes before it, or -1: a child of the token before the
  * tree (several may be). With P the stream's tokens before the tree, a node's position is
- * P + depth (depth 0 where the parent is -1), and it sees the P tokens before the tree, its ancestors and itself,
- * with a window only those whose position is above its own - window or below sinks:
+ * P + depth (depth 0 where the parent is -1), and it sees the P tokens before the tree, its
+ * ancestors and itself, with a window only those whose position is above its own - window or
+ * below sinks:
  *   out[r][g] = softmax over those j of (sm_scale * q[r][g] . k[j]) v[j].
  * A tree without branches gives pkv_attend_tokens' results but for rounding. Everything else is
  * as in pkv_attend_tokens. A parent that does not come before its node is taken for -1, and noted
