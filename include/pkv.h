@@ -562,8 +562,8 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* stream_ids, const int* pos
  * q: device bf16 [row_off[n]][q_heads][64], rows q_stride apart; out: the same,
  * contiguous. A call takes fewer than 2^27 rows x q_heads. fp32 accumulation and softmax;
  * the probabilities are rounded to bf16 for the second product, or, on E4M3 pages, in streams
- * with few rows x query heads per KV head (up to 64) to f16 (and q as well; not where the call's
- * other streams bring them all into one launch), which loses what is below 2^-39 of an
+ * with few rows x query heads per KV head (32; 64 where the call's streams of up to 64 have 32 or
+ * fewer on average, or are few) to f16 (and q as well), which loses what is below 2^-39 of an
  * output row's largest contribution. sm_scale <= 0 means 1 / sqrt(64).
  * Results depend on the batch only by rounding (the kernel and the split of the keys
  * are chosen for the whole call) and are the same bits for the same call. The
@@ -584,7 +584,8 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
  * ancestors and itself, with a window only those whose position is above its own - window or
  * below sinks:
  *   out[r][g] = softmax over those j of (sm_scale * q[r][g] . k[j]) v[j].
- * A tree without branches gives pkv_attend_tokens' results but for rounding. Everything else is
+ * A tree without branches gives pkv_attend_tokens' results but for rounding (on E4M3 pages the
+ * call's other streams may bring those of few rows to bf16 probabilities). Everything else is
  * as in pkv_attend_tokens. A parent that does not come before its node is taken for -1, and noted
  * (pkv_sync: DEVICE).
  * Errors: as pkv_attend_tokens; INVALID for more than 256 rows of a stream, and for parents

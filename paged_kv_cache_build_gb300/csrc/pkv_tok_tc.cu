@@ -67,7 +67,7 @@ constexpr int kConvert0 = kProducer<MT, FP8, kLanes> + 1;
 // streams of 8030 keys, 120 rows: 97 us, 160 with three), with four there are registers for
 // three only.
 template <int MT, bool FP8, int kLanes>
-constexpr int kConvertWarps = kLanes == 2 ? (FP8 ? 5 : 1) : MT < 4 ? 7 : 3;   // (bf16: idle, whole warpgroups)
+constexpr int kConvertWarps = kLanes == 2 ? (FP8 ? 5 : 1) : FP8 && MT < 4 ? 7 : 3;   // (bf16: idle, whole warpgroups)
 template <int MT, bool FP8, int kLanes>
 constexpr int kThreads = 32 * (kConvert0<MT, FP8, kLanes> + kConvertWarps<MT, FP8, kLanes>);
 // Registers a thread at launch; the softmax warpgroups then take what the others give up.

@@ -337,13 +337,20 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
   // the streams' rows per KV head decide on the kernel
   cudaStream_t s = as_stream(cuda_stream);
   const int n_items = a.n;
-  long long few_ctas = 0, most = 0;
-  int n_small = 0;
+  long long few_ctas = 0, rows_sum = 0, most = 0;
+  int n_up_to = 0, n_small = 0;
   for (int i = 0; i < n_items; ++i) {
     const long long r = (long long)a.item[i].n * group;
-    if (r <= kTokenFewRows) few_ctas += (long long)ceil_div(r, 16) * h->H;
+    if (r <= kTokenFewRows) few_ctas += (long long)ceil_div(r, 16) * h->H, rows_sum += r, ++n_up_to;
   }
-  const int few_rows = few_ctas <= h->num_sms ? kTokenFewRows : kTokenFewRowsAll;
+  // E4M3 pages: the kernel for few rows has f16 weights, the matrix-unit kernel bf16 ones, so what the
+  // former takes of a call of pkv_attend_tokens does not go by speed: streams of up to
+  // kTokenFewRowsAll rows, and of up to kTokenFewRows where these have no more than
+  // kTokenFewRowsAll on average. (What that costs: 16 streams of 500 .. 4001 tokens with 4 .. 48
+  // rows 36 against 32 us, with 4 .. 64 rows 46 against 33.)
+  const bool f16_weights = h->fp8 && !parents;
+  const bool up_to_64 = few_ctas <= h->num_sms || (f16_weights && rows_sum <= (long long)kTokenFewRowsAll * n_up_to);
+  const int few_rows = up_to_64 ? kTokenFewRows : kTokenFewRowsAll;
   for (int i = 0; i < n_items; ++i) {
     const long long r = (long long)a.item[i].n * group;
     if (r <= few_rows) ++n_small, most = std::max(most, r);
@@ -382,8 +389,8 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
     PKV_CUDA(h, launch_token_few(a, s));
     return PKV_OK;
   }
-  // Both kinds: a launch for each, one behind the other, or all in the matrix-unit kernel, as the
-  // estimates say (and 3 us for the launch). Ragged trees of up to 32 nodes, group 4: 16 streams of up to
+  // Both kinds: a launch for each, one behind the other, or (where weights may be bf16) all in the
+  // matrix-unit kernel, as the estimates say (and 3 us for the launch). Ragged trees of up to 32 nodes, group 4: 16 streams of up to
   // 4001 tokens 35 us in two launches, 25 in one; 32 of 4000 55 and 45; 4 of 8000 29 and 20 us; on
   // E4M3 pages 57 and 45, 90 and 77, 38 and 26 us.
   TokenAttendArgs small = a, large = a;
@@ -393,7 +400,7 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
     t.item[t.n++] = a.item[i];
   }
   const double apart = plan_few(&small) + plan_tc(h, &large) + 3.0;
-  if (plan_tc(h, &a) <= apart) {
+  if (!f16_weights && plan_tc(h, &a) <= apart) {
     give_parts(&a);
     return launch_tc(a);
   }

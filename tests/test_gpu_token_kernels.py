@@ -1,0 +1,51 @@
+"""Token streams' attention by the kernel that a call takes, against the fp64 oracle (needs a GB300).
+
+Tolerance where weights are f16 (E4M3 pages, few rows): as in test_gpu_tokens, with 2^-11 of A, half
+a step of f16, in place of bf16's 2^-8; n 2^-40 for weights below f16's range is less than the 2^-20
+that stands there for the exponentials."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle.tokens import causal_attend_fp64
+
+from .test_gpu_tokens import SCALE, Pool, _built, f64, stored, tolerance   # noqa: F401 (_built: a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def opposite_values(p, sid, n):
+    """n tokens more whose values come in pairs that cancel but for the weights' difference: a weight's
+    rounding shows in full where the output's own is small."""
+    batch = p.cache.token_batch([sid], [n])
+    p.ora.append([sid], [n])
+    k = (p.rows(n, p.heads) * 0.5).bfloat16()
+    v = (1 + torch.randint(0, 8, (n, p.heads, 64), generator=p.gen, device="cuda") / 8).bfloat16()
+    v[1::2] = -v[0:n - 1:2]
+    p.cache.append_tokens(batch, k, v)
+    p.kv[sid][0] = [np.concatenate([old, stored(x, p.fp8)]) for old, x in zip(p.kv[sid][0], (k, v))]
+
+
+@pytest.mark.parametrize("small,large", [([1] * 8, [200]), ([1, 8, 2, 4] * 3, [60, 300]), ([16, 1, 2, 12, 1, 3] * 12, [])],
+                         ids=["single tokens beside a chunk", "drafts beside chunks", "up to 64 rows"])
+def test_few_rows_on_e4m3_pages_have_f16_weights(small, large):
+    heads, group = 2, 4
+    p = Pool(200, 64, heads, True, max_streams=100)
+    counts = small + large
+    sids = [p.open() for _ in counts]
+    for s, n in zip(sids, counts):
+        opposite_values(p, s, n + n % 2 + (2 if n < 100 else 100))
+    q, out = p.check_attend(sids, counts, group)
+    qq, got, at = f64(q), f64(out), 0
+    for sid, n in zip(sids, counts):
+        if n in small:
+            k, v = p.kv[sid][0]
+            x = qq[at:at + n]
+            ref = causal_attend_fp64(x, k, v, len(k) - n, 0, 0, SCALE)
+            a = causal_attend_fp64(x, k, np.abs(v), len(k) - n, 0, 0, SCALE)
+            tol = tolerance(x, k, v, ref, len(k) - n, 0, 0, SCALE) - (2.0 ** -8 - 2.0 ** -11) * a
+            err = np.abs(got[at:at + n] - ref)
+            assert (err <= tol).all(), f"stream {sid}: worst {(err / tol).max():.2f} of the tolerance"
+        at += n
+    p.cache.close()

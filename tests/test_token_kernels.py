@@ -1,0 +1,90 @@
+"""Which kernel an attention call on token streams takes, without a GPU: the library's own host code,
+linked with a CUDA runtime that keeps what was launched (recording_cudart.cpp)."""
+
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+OK = 0
+FEW = re.compile(r"token_few_kernelILi(\d)ELb([01])ELb([01])E")
+TC = re.compile(r"token_tc_kernelILi(\d)ELb([01])ELi(\d)ELb([01])E")
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    from paged_kv_cache_build_gb300 import build
+    from paged_kv_cache_build_gb300._lib import SIGNATURES
+    build.build()
+    so = str(tmp_path_factory.mktemp("host") / "recording.so")
+    objs = [os.path.join(build.BUILD, os.path.basename(s)[:-3] + ".o") for s in build.sources()]
+    include = os.path.join(os.path.dirname(os.path.dirname(build.nvcc())), "include")
+    # -Bsymbolic: not the runtime that torch has loaded
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I", include, "-I", HERE,
+                    os.path.join(HERE, "recording_cudart.cpp")] + objs + ["-o", so], check=True)
+    L = ctypes.CDLL(so)
+    for name, (res, args) in SIGNATURES.items():
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = res, args
+    L.recorded_kernel.restype = ctypes.c_char_p
+    return L
+
+
+def launches(lib, past, new, heads, group, fp8, tree=False, page=64):
+    """What attending each stream's last new[i] of past[i] + new[i] tokens launches: ("few", 8-row
+    groups a block), ("tc", row blocks of 128, lanes) or ("join",), in order."""
+    ints = lambda x: (ctypes.c_int * len(x))(*x)  # noqa: E731
+    h = ctypes.c_void_p()
+    create = lib.pkv_create_fp8 if fp8 else lib.pkv_create_ex
+    lengths = [a + b for a, b in zip(past, new)]
+    pages = sum(-(-n // page) for n in lengths)
+    assert create(pages, page, heads, 64, 1, len(past), ctypes.byref(h)) == OK
+    mem = ctypes.create_string_buffer(64)
+    at = (ctypes.addressof(mem) + 15) // 16 * 16
+    sids = []
+    for n in lengths:
+        sid = ctypes.c_int()
+        assert lib.pkv_stream_open_tokens(h, n, 0, 0, ctypes.byref(sid)) == OK
+        sids.append(sid.value)
+        assert lib.pkv_append_tokens(h, 1, ints([sid.value]), ints([0, n]), 0, at, at, 0, 0, None) == OK
+    off = [0]
+    for n in new:
+        off.append(off[-1] + n)
+    lib.recorded_clear()
+    if tree:
+        r = lib.pkv_attend_tree(h, at, heads * group, 0, ints(off), ints(sids), len(sids), 0, at, at, 0, 0, 0.0, None)
+    else:
+        r = lib.pkv_attend_tokens(h, at, heads * group, 0, ints(off), ints(sids), len(sids), 0, at, 0, 0, 0.0, None)
+    assert r == OK, lib.pkv_last_error(h)
+    got = []
+    for i in range(lib.recorded_launches()):
+        name = lib.recorded_kernel(i).decode()
+        few, tc = FEW.search(name), TC.search(name)
+        assert few or tc or "token_combine_kernel" in name, name
+        assert not (few or tc) or bool(int((few or tc).group(2))) == fp8
+        assert not (few or tc) or bool(int((few or tc).groups()[-1])) == tree
+        got.append(("few", int(few.group(1))) if few else ("tc", int(tc.group(1)), int(tc.group(3))) if tc else ("join",))
+    assert lib.pkv_destroy(h) == OK
+    return got
+
+
+def kinds(got):
+    return [x[0] for x in got if x[0] != "join"]
+
+
+@pytest.mark.parametrize("past,new", [([4000] * 12, [1500] + [1] * 11), ([4000] * 16, list(range(4, 68, 4))),
+                                      ([300, 300], [1, 200]), ([2000] * 101, [1500] + [1] * 100)], ids=str)
+def test_few_rows_on_e4m3_pages_keep_f16_weights(lib, past, new):
+    """Streams of few rows go through the kernel whose weights are f16, whatever else the batch holds:
+    the matrix-unit kernel's are bf16, three bits less."""
+    assert kinds(launches(lib, past, new, 8, 4, True)) == ["few", "tc"]
+
+
+@pytest.mark.parametrize("rows", [[4, 8, 16, 24, 32, 40, 48, 64] * 2, [64, 1, 1, 1] * 10], ids=str)
+def test_up_to_64_rows_on_e4m3_pages_keep_f16_weights(lib, rows):
+    """So do those of up to 64 rows where such streams have 32 at most on average."""
+    assert kinds(launches(lib, [2000] * len(rows), rows, 8, 1, True)) == ["few"]
