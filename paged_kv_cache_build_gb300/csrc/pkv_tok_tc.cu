@@ -46,13 +46,14 @@ namespace {
 
 constexpr int kBN = kTokTile;
 // kLanes = 2: two CTAs of two lanes an SM, so that one's start and end run beside the other's
-// products; 4: one CTA of four. bf16 pages take two (prefill of 8192 tokens, 16 heads, 256 rows: 145
-// us, 152 with one CTA of 512 rows; ragged batch of 12 chunks 245 against 270 us; 128 rows, 32
-// streams of 2000 tokens 30 against 38 us, ragged ones of 4001 24 against 32, one of 32000 25 as
-// well; but 16 even ones of 4031, a CTA for each of 128 SMs, 35 against 31 us). E4M3 pages take
-// four, which share a tile's conversion, or, with 128 rows, what is estimated to end first: 64
-// streams of 2000 tokens 100 us with two and 120 with four, 16 ragged ones of 4001 41 and 46, 16 even
-// ones 56 and 52, one of 16000 28 and 24 us. (256 rows with two: 71 against 63 us.)
+// products; 4: one CTA of four. With 128 rows what is estimated to end first: two where CTAs come in
+// waves or differ in length, four where each SM has one and a key range need not be cut twice as often
+// (bf16 pages, 120 rows, 8 KV heads, two / four: 16 streams of 4031 tokens 35.1 / 30.7 us, of 1000 16.6 /
+// 12.8, 18 of 4000 36.7 / 32.0, one of 131000 61 / 57; 32 of 2000 30.6 / 38.4, 16 ragged ones of 500 ..
+// 4001 22.7 / 32.1, 64 of 300 21.5 / 37.1. E4M3 pages, where four lanes share a tile's conversion: 64 of
+// 2000 100 / 120, 16 ragged ones 41 / 46, 16 even ones 56 / 52, one of 16000 28 / 24). With more
+// rows bf16 pages take two (prefill of 8192 tokens, 16 heads, 256 rows: 145 us, 152 with one CTA of 512
+// rows; ragged batch of 12 chunks 245 against 270 us), E4M3 pages four (256 rows 63 us, 71 with two).
 template <int MT, bool FP8, int kLanes>
 constexpr int kCtasPerSm = 4 / kLanes;
 template <int MT, bool FP8, int kLanes>
@@ -701,7 +702,9 @@ cudaError_t launch_tc_rows(const TokenAttendArgs& a, cudaStream_t s) {
     return a.rows == 128   ? (a.lanes == 2 ? launch_tc<1, true, 2, TREE>(a, s) : launch_tc<1, true, 4, TREE>(a, s))
            : a.rows == 256 ? launch_tc<2, true, 4, TREE>(a, s)
                            : launch_tc<4, true, 4, TREE>(a, s);
-  return a.rows == 128 ? launch_tc<1, false, 2, TREE>(a, s) : launch_tc<2, false, 2, TREE>(a, s);
+  return a.rows == 256  ? launch_tc<2, false, 2, TREE>(a, s)
+         : a.lanes == 2 ? launch_tc<1, false, 2, TREE>(a, s)
+                        : launch_tc<1, false, 4, TREE>(a, s);
 }
 
 }  // namespace
@@ -712,8 +715,9 @@ int token_tc_ctas_per_sm(int lanes) { return 4 / lanes; }
 
 double token_tc_tile_us(bool fp8, int rows, int lanes) {
   if (fp8) return rows == 128 ? (lanes == 2 ? 1.08 : 0.72) : rows == 256 ? 0.79 : 1.6;
-  return rows == 128 ? 0.62 : 1.05;
+  return rows == 256 ? 1.29 : lanes == 2 ? 0.76 : 0.38;
 }
+double token_tc_start_us(bool fp8, int lanes) { return !fp8 && lanes == 4 ? 3.0 : 0.0; }
 
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s) {
   return a.parents ? launch_tc_rows<true>(a, s) : launch_tc_rows<false>(a, s);

@@ -160,10 +160,13 @@ double plan_shape(pkv_t h, TokenAttendArgs* a, bool few, int shape, int lanes = 
     last[i] = block_tiles(it.blocks - 1);
   }
   const int room = std::min<int>(kTokenScratchBytes / (shape * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
-  const CtaCost cost =
-      few ? CtaCost{h->num_sms * token_few_ctas_per_sm(), token_few_tile_us(shape), 12, 4, 8, room, false}
-          : CtaCost{h->num_sms * token_tc_ctas_per_sm(lanes), token_tc_tile_us(h->fp8, shape, lanes), 10, 4, 8, room, true};
-  return plan_splits(a, first, last, cost);
+  if (few)
+    return plan_splits(a, first, last, CtaCost{h->num_sms * token_few_ctas_per_sm(), token_few_tile_us(shape), 12, 4, 8, room, false});
+  double us = plan_splits(a, first, last, CtaCost{h->num_sms * token_tc_ctas_per_sm(lanes), token_tc_tile_us(h->fp8, shape, lanes), 10, 4, 8, room, true});
+  us += token_tc_start_us(h->fp8, lanes);
+  int splits = 1;
+  for (int i = 0; i < a->n; ++i) splits = std::max(splits, a->item[i].splits);
+  return splits > 1 ? us + splits * kTokenSplitUs : us;
 }
 
 // Plans the matrix-unit kernel for a's streams: the shape of its CTAs, and the splits.
@@ -180,13 +183,12 @@ double plan_tc(pkv_t h, TokenAttendArgs* a) {
   // 140 / 150 us.
   if (!h->fp8 && shape == 256) {
     const double narrow = plan_shape(h, a, false, 128, 2), wide = plan_shape(h, a, false, 256, 2);
-    if (wide <= narrow) return wide;
-    shape = 128;
+    return wide <= narrow ? wide : plan_shape(h, a, false, 128, 2);
   }
-  if (h->fp8 && shape == 128) {
+  // 128 rows: two CTAs of two lanes an SM, or one of four (each with a quarter of the tiles)
+  if (shape == 128) {
     const double two = plan_shape(h, a, false, 128, 2), four = plan_shape(h, a, false, 128, 4);
-    if (four <= two) return four;
-    return plan_shape(h, a, false, 128, 2);
+    return four <= two ? four : plan_shape(h, a, false, 128, 2);
   }
   return plan_shape(h, a, false, shape, h->fp8 ? 4 : 2);
 }
@@ -390,16 +392,16 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
     return PKV_OK;
   }
   // Both kinds: a launch for each, one behind the other, or (where weights may be bf16) all in the
-  // matrix-unit kernel, as the estimates say (and 3 us for the launch). Ragged trees of up to 32 nodes, group 4: 16 streams of up to
-  // 4001 tokens 35 us in two launches, 25 in one; 32 of 4000 55 and 45; 4 of 8000 29 and 20 us; on
-  // E4M3 pages 57 and 45, 90 and 77, 38 and 26 us.
+  // matrix-unit kernel, as the estimates say (and 4 us for the launch). Ragged trees of up to 32 nodes,
+  // group 4: 16 streams of up to 4001 tokens 35 us in two launches, 25 in one; 32 of 4000 55 and 45; 4 of
+  // 8000 29 and 20 us; on E4M3 pages 57 and 45, 90 and 77, 38 and 26 us.
   TokenAttendArgs small = a, large = a;
   small.n = large.n = 0;
   for (int i = 0; i < n_items; ++i) {
     TokenAttendArgs& t = (long long)a.item[i].n * group <= few_rows ? small : large;
     t.item[t.n++] = a.item[i];
   }
-  const double apart = plan_few(&small) + plan_tc(h, &large) + 3.0;
+  const double apart = plan_few(&small) + plan_tc(h, &large) + 4.0;
   if (!f16_weights && plan_tc(h, &a) <= apart) {
     give_parts(&a);
     return launch_tc(a);

@@ -272,6 +272,9 @@ int token_tc_max_rows(bool fp8);
 int token_tc_ctas_per_sm(int lanes);
 // What a 64-slot tile takes a CTA of it, in us, beside the SM's others.
 double token_tc_tile_us(bool fp8, int rows, int lanes);
+// What a CTA's start and end take beyond CtaCost's tiles, in us; and what a split adds to the join.
+double token_tc_start_us(bool fp8, int lanes);
+constexpr double kTokenSplitUs = 0.25;
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s);
 // Joins the splits of the items that have several (launch_token_few does so itself).
 cudaError_t launch_token_combine(const TokenAttendArgs& a, cudaStream_t s);

@@ -10,7 +10,9 @@ import torch
 
 from oracle.tokens import causal_attend_fp64
 
+from .test_gpu_token_trees import check_tree, random_parents
 from .test_gpu_tokens import SCALE, Pool, _built, f64, stored, tolerance   # noqa: F401 (_built: a fixture)
+from .test_token_kernels import SMALL_LANES
 
 pytestmark = pytest.mark.gpu
 
@@ -48,4 +50,19 @@ def test_few_rows_on_e4m3_pages_have_f16_weights(small, large):
             err = np.abs(got[at:at + n] - ref)
             assert (err <= tol).all(), f"stream {sid}: worst {(err / tol).max():.2f} of the tolerance"
         at += n
+    p.cache.close()
+
+
+@pytest.mark.parametrize("past,heads,lanes", SMALL_LANES, ids=["even", "ragged", "waves", "ragged waves"])
+def test_both_numbers_of_lanes(past, heads, lanes):
+    """Blocks of 128 rows on bf16 pages, in CTAs of two and of four lanes."""
+    p = Pool(sum(-(-(n + 30) // 16) for n in past), 16, heads, max_streams=len(past))
+    sids = [p.open(n + 30) for n in past]
+    new = [30] * len(past)
+    p.append(sids, past)
+    p.append(sids, new)
+    rng = np.random.default_rng(lanes)
+    for window, sinks in ((0, 0), (50, 3)):
+        p.check_attend(sids, new, 4, window, sinks)
+        check_tree(p, sids, [random_parents(rng, 30) for _ in past], 4, window, sinks)
     p.cache.close()

@@ -88,3 +88,27 @@ def test_few_rows_on_e4m3_pages_keep_f16_weights(lib, past, new):
 def test_up_to_64_rows_on_e4m3_pages_keep_f16_weights(lib, rows):
     """So do those of up to 64 rows where such streams have 32 at most on average."""
     assert kinds(launches(lib, [2000] * len(rows), rows, 8, 1, True)) == ["few"]
+
+
+# (past, KV heads, lanes): 30 new tokens of four query heads a KV head, few keys
+SMALL_LANES = [([100] * 3, 2, 4), ([700, 3, 1300], 3, 4), ([90 + 3 * i for i in range(51)], 3, 2),
+               ([40 * i for i in range(90)], 2, 2)]
+
+
+# bf16 pages, 8 KV heads of four query heads, 30 new tokens: what takes 128-row blocks
+@pytest.mark.parametrize("tree", [False, True], ids=["tokens", "tree"])
+@pytest.mark.parametrize("past,lanes", [([4001] * 16, 4), ([1000] * 16, 4), ([4000] * 18, 4), ([131000], 4),
+                                        ([2000] * 32, 2), ([4000] * 12, 2), ([500 + 233 * i for i in range(16)], 2),
+                                        ([300] * 64, 2)], ids=str)
+def test_lanes_of_128_row_blocks(lib, past, lanes, tree):
+    """One CTA of four lanes an SM where each SM has one CTA, two of two lanes where they come in waves or
+    differ in length (16 even streams of 4031 tokens 30.7 us with four, 35.1 with two)."""
+    got = launches(lib, past, [30] * len(past), 8, 4, False, tree)
+    assert got[0] == ("tc", 1, lanes)
+    assert kinds(got) == ["tc"]
+
+
+@pytest.mark.parametrize("past,heads,lanes", SMALL_LANES, ids=["even", "ragged", "waves", "ragged waves"])
+def test_lanes_of_the_gpu_tests_shapes(lib, past, heads, lanes):
+    for tree in (False, True):
+        assert launches(lib, past, [30] * len(past), heads, 4, False, tree, page=16)[0] == ("tc", 1, lanes)
