@@ -160,8 +160,16 @@ double plan_shape(pkv_t h, TokenAttendArgs* a, bool few, int shape, int lanes = 
     last[i] = block_tiles(it.blocks - 1);
   }
   const int room = std::min<int>(kTokenScratchBytes / (shape * (kHeadDim + 2) * sizeof(float)), kTokenJoins);
-  if (few)
-    return plan_splits(a, first, last, CtaCost{h->num_sms * token_few_ctas_per_sm(), token_few_tile_us(shape), 12, 4, 8, room, false});
+  if (few) {
+    const CtaCost cost{h->num_sms * token_few_ctas_per_sm(), token_few_tile_us(shape), 12, 4, 8, room, false};
+    const double us = plan_splits(a, first, last, cost);
+    int blocks = 0, most = 0;
+    for (int i = 0; i < a->n; ++i) blocks += a->item[i].blocks, most = std::max(most, a->item[i].blocks);
+    if (h->fp8 || most <= 2) return us;
+    // bf16 pages: where several blocks read the same keys, a tile is the warps' own time, not the HBM's
+    const double tile = std::max(kTokenFewSharedTileUs, cost.tile * a->n / blocks);
+    return us / cost.tile * tile + cost.fixed * (cost.tile - tile);
+  }
   double us = plan_splits(a, first, last, CtaCost{h->num_sms * token_tc_ctas_per_sm(lanes), token_tc_tile_us(h->fp8, shape, lanes), 10, 4, 8, room, true});
   us += token_tc_start_us(h->fp8, lanes);
   int splits = 1;
@@ -187,8 +195,8 @@ double plan_tc(pkv_t h, TokenAttendArgs* a) {
   }
   // 128 rows: two CTAs of two lanes an SM, or one of four (each with a quarter of the tiles)
   if (shape == 128) {
-    const double two = plan_shape(h, a, false, 128, 2), four = plan_shape(h, a, false, 128, 4);
-    return four <= two ? four : plan_shape(h, a, false, 128, 2);
+    const double four = plan_shape(h, a, false, 128, 4), two = plan_shape(h, a, false, 128, 2);
+    return two < four ? two : plan_shape(h, a, false, 128, 4);
   }
   return plan_shape(h, a, false, shape, h->fp8 ? 4 : 2);
 }
@@ -339,41 +347,33 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
   // the streams' rows per KV head decide on the kernel
   cudaStream_t s = as_stream(cuda_stream);
   const int n_items = a.n;
-  long long few_ctas = 0, rows_sum = 0, most = 0;
-  int n_up_to = 0, n_small = 0;
+  long long rows_sum = 0;
+  int n_all = 0, n_up_to = 0;                    // of up to kTokenFewRowsAll and kTokenFewRows rows
   for (int i = 0; i < n_items; ++i) {
     const long long r = (long long)a.item[i].n * group;
-    if (r <= kTokenFewRows) few_ctas += (long long)ceil_div(r, 16) * h->H, rows_sum += r, ++n_up_to;
+    if (r <= kTokenFewRowsAll) ++n_all;
+    if (r <= kTokenFewRows) rows_sum += r, ++n_up_to;
   }
-  // E4M3 pages: the kernel for few rows has f16 weights, the matrix-unit kernel bf16 ones, so what the
-  // former takes of a call of pkv_attend_tokens does not go by speed: streams of up to
-  // kTokenFewRowsAll rows, and of up to kTokenFewRows where these have no more than
-  // kTokenFewRowsAll on average. (What that costs: 16 streams of 500 .. 4001 tokens with 4 .. 48
-  // rows 36 against 32 us, with 4 .. 64 rows 46 against 33.)
-  const bool f16_weights = h->fp8 && !parents;
-  const bool up_to_64 = few_ctas <= h->num_sms || (f16_weights && rows_sum <= (long long)kTokenFewRowsAll * n_up_to);
-  const int few_rows = up_to_64 ? kTokenFewRows : kTokenFewRowsAll;
-  for (int i = 0; i < n_items; ++i) {
-    const long long r = (long long)a.item[i].n * group;
-    if (r <= few_rows) ++n_small, most = std::max(most, r);
-  }
-  const auto launch_tc = [&](const TokenAttendArgs& t) -> pkv_status {
-    PKV_CUDA(h, launch_token_tc(t, s));
-    if (t.part_o) PKV_CUDA(h, launch_token_combine(t, s));
-    return PKV_OK;
-  };
   const auto give_parts = [&](TokenAttendArgs* t) {
     bool split = false;
     for (int i = 0; i < t->n; ++i) split = split || t->item[i].splits > 1;
     t->part_o = split ? h->d_token_part : nullptr;
     t->part_ml = split ? h->d_token_part + (size_t)t->ctas * t->rows * kHeadDim : nullptr;
   };
-  if (n_small == 0) {
-    plan_tc(h, &a);
-    give_parts(&a);
-    return launch_tc(a);
-  }
+  const auto launch_tc = [&](TokenAttendArgs* t) -> pkv_status {
+    give_parts(t);
+    PKV_CUDA(h, launch_token_tc(*t, s));
+    if (t->part_o) PKV_CUDA(h, launch_token_combine(*t, s));
+    return PKV_OK;
+  };
+  const auto launch_few = [&](TokenAttendArgs* t) -> pkv_status {
+    give_parts(t);
+    PKV_CUDA(h, launch_token_few(*t, s));
+    return PKV_OK;
+  };
   const auto plan_few = [&](TokenAttendArgs* t) {
+    long long most = 0;
+    for (int i = 0; i < t->n; ++i) most = std::max(most, (long long)t->item[i].n * group);
     if (most <= 8) return plan_shape(h, t, true, 8);
     // 17 to 24 rows: a block of 24 with three warps, or two of 16 with four, of which the second
     // finds the keys in L2. (21 rows, 24 / 16 + 16, pages not in L2: a stream of 16000 tokens 21.6 / 16.0
@@ -385,31 +385,58 @@ pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, 
     }
     return plan_shape(h, t, true, 16);
   };
-  if (n_small == n_items) {
+  if (n_up_to == 0) {
+    plan_tc(h, &a);
+    return launch_tc(&a);
+  }
+  if (n_all == n_items) {
     plan_few(&a);
-    give_parts(&a);
-    PKV_CUDA(h, launch_token_few(a, s));
-    return PKV_OK;
+    return launch_few(&a);
   }
-  // Both kinds: a launch for each, one behind the other, or (where weights may be bf16) all in the
-  // matrix-unit kernel, as the estimates say (and 4 us for the launch). Ragged trees of up to 32 nodes,
-  // group 4: 16 streams of up to 4001 tokens 35 us in two launches, 25 in one; 32 of 4000 55 and 45; 4 of
-  // 8000 29 and 20 us; on E4M3 pages 57 and 45, 90 and 77, 38 and 26 us.
-  TokenAttendArgs small = a, large = a;
-  small.n = large.n = 0;
-  for (int i = 0; i < n_items; ++i) {
-    TokenAttendArgs& t = (long long)a.item[i].n * group <= few_rows ? small : large;
-    t.item[t.n++] = a.item[i];
+  // E4M3 pages: the kernel for few rows has f16 weights, the matrix-unit kernel bf16 ones, so what the
+  // former takes of a call of pkv_attend_tokens does not go by speed alone: streams of up to
+  // kTokenFewRowsAll rows, and of up to kTokenFewRows where these have no more than
+  // kTokenFewRowsAll on average. (What that costs: 16 streams of 500 .. 4001 tokens with 4 .. 48
+  // rows 36 against 32 us, with 4 .. 64 rows 46 against 33.)
+  const bool f16_weights = h->fp8 && !parents;
+  // Streams of both kinds: a launch for each, one behind the other, or (where weights may be bf16) all
+  // in the matrix-unit kernel, as the estimates say (and 4 us for the launch). Ragged trees of up to 32
+  // nodes, group 4: 16 streams of up to 4001 tokens 35 us in two launches, 25 in one; 32 of 4000 55 and
+  // 45; 4 of 8000 29 and 20 us; on E4M3 pages 57 and 45, 90 and 77, 38 and 26 us.
+  struct Division {
+    TokenAttendArgs small, large;
+    double us;
+    bool together;
+  };
+  const double one = f16_weights ? 0.0 : plan_tc(h, &a);
+  const auto divide = [&](Division* d, int few_rows) {
+    std::memcpy(static_cast<void*>(&d->small), &a, offsetof(TokenAttendArgs, item));
+    std::memcpy(static_cast<void*>(&d->large), &a, offsetof(TokenAttendArgs, item));
+    d->small.n = d->large.n = 0;
+    for (int i = 0; i < n_items; ++i) {
+      TokenAttendArgs& t = (long long)a.item[i].n * group <= few_rows ? d->small : d->large;
+      t.item[t.n++] = a.item[i];
+    }
+    const bool both = d->small.n > 0 && d->large.n > 0;
+    // (where all are large, that is `one`)
+    d->us = d->small.n == 0 && !f16_weights ? one
+            : (d->small.n > 0 ? plan_few(&d->small) : 0.0) + (d->large.n > 0 ? plan_tc(h, &d->large) : 0.0) +
+                  (both ? 4.0 : 0.0);
+    d->together = !f16_weights && (d->small.n == 0 || (both && one <= d->us));
+    if (d->together) d->us = one;
+  };
+  Division by[2], *best = &by[0];
+  const bool up_to_64 = f16_weights && rows_sum <= (long long)kTokenFewRowsAll * n_up_to;
+  divide(best, up_to_64 ? kTokenFewRows : kTokenFewRowsAll);
+  if (!up_to_64 && n_up_to > n_all) {
+    // 33 .. 64 rows: up to four blocks of 16 read the keys as often, from L2 but for the first
+    divide(&by[1], kTokenFewRows);
+    if (by[1].us <= best->us) best = &by[1];
   }
-  const double apart = plan_few(&small) + plan_tc(h, &large) + 4.0;
-  if (!f16_weights && plan_tc(h, &a) <= apart) {
-    give_parts(&a);
-    return launch_tc(a);
-  }
-  give_parts(&small);
-  PKV_CUDA(h, launch_token_few(small, s));
-  give_parts(&large);
-  return launch_tc(large);
+  if (best->together) return launch_tc(&a);
+  if (best->small.n > 0)
+    if (pkv_status r = launch_few(&best->small)) return r;
+  return best->large.n > 0 ? launch_tc(&best->large) : PKV_OK;
 }
 
 }  // namespace

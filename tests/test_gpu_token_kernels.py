@@ -66,3 +66,15 @@ def test_both_numbers_of_lanes(past, heads, lanes):
         p.check_attend(sids, new, 4, window, sinks)
         check_tree(p, sids, [random_parents(rng, 30) for _ in past], 4, window, sinks)
     p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("past,rows", [([40000], [16]), ([30000, 100], [12, 16])], ids=str)
+def test_up_to_64_rows_over_long_histories(past, rows, fp8):
+    p = Pool(1300, 64, 2, fp8)
+    sids = [p.open() for _ in past]
+    p.append(sids, past)
+    p.append(sids, rows)
+    p.check_attend(sids, rows, 4)
+    check_tree(p, sids, [random_parents(np.random.default_rng(n), n) for n in rows], 4)
+    p.cache.close()

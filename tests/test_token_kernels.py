@@ -112,3 +112,30 @@ def test_lanes_of_128_row_blocks(lib, past, lanes, tree):
 def test_lanes_of_the_gpu_tests_shapes(lib, past, heads, lanes):
     for tree in (False, True):
         assert launches(lib, past, [30] * len(past), heads, 4, False, tree, page=16)[0] == ("tc", 1, lanes)
+
+
+# (streams, past, rows, fp8, few): measured, 8 KV heads of four query heads
+LENGTHS = [(1, 1000, 64, False, True), (1, 4000, 64, False, True), (1, 8000, 48, False, True),
+           (1, 32000, 64, False, False), (1, 131000, 40, False, False), (1, 131000, 64, False, False),
+           (2, 16000, 64, False, False), (4, 500, 48, False, True), (4, 8000, 64, False, False),
+           (1, 4000, 64, True, True), (1, 8000, 64, True, True), (1, 131000, 48, True, False),
+           (1, 131000, 64, True, False), (2, 16000, 64, True, False), (4, 8000, 64, True, False)]
+
+
+@pytest.mark.parametrize("tree", [False, True], ids=["tokens", "tree"])
+@pytest.mark.parametrize("streams,past,rows,fp8,few", LENGTHS, ids=str)
+def test_33_to_64_rows_by_length(lib, streams, past, rows, fp8, few, tree):
+    """Blocks of 16 rows read such a stream's keys several times: the longer they are, the sooner the
+    matrix-unit kernel ends (64 rows over 131000 tokens 56 us, 80 in blocks of 16; over 4000 12.9 and 11.1)."""
+    got = launches(lib, [past] * streams, [rows // 4] * streams, 8, 4, fp8, tree)
+    assert kinds(got) == ["few" if few else "tc"]
+
+
+@pytest.mark.parametrize("past,rows,heads,few", [([2000] * 64, [64] * 4 + [1] * 60, 8, True),
+                                                 ([200 + 40 * i for i in range(100)], [1 + i % 48 for i in range(100)], 1, True),
+                                                 ([500] * 64, [64] * 16 + [8] * 48, 2, True),
+                                                 ([4000] * 16, [48] * 16, 8, False), ([1000] * 128, [40] * 128, 1, False)],
+                         ids=["a few of 64 among single tokens", "ragged", "short", "even", "many"])
+def test_33_to_64_rows_in_batches(lib, past, rows, heads, few):
+    """Measured, few rows / matrix units: 47 / 55, 17 / 19, 7 / 10, 51 / 31 us; the last 13 there."""
+    assert kinds(launches(lib, past, rows, heads, 1, False)) == ["few" if few else "tc"]
