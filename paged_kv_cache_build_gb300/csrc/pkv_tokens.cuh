@@ -274,10 +274,11 @@ int token_few_ctas_per_sm();
 // Attention of 128, 256 or (on E4M3 pages) 512 query rows per CTA (a.rows).
 int token_tc_max_rows(bool fp8);
 int token_tc_ctas_per_sm(int lanes);
-// What a 64-slot tile takes a CTA of it, in us, beside the SM's others.
-double token_tc_tile_us(bool fp8, int rows, int lanes);
+// What a 64-slot tile takes a CTA of it, in us, beside the SM's others, where a stream has up to
+// `most` rows.
+double token_tc_tile_us(bool fp8, int rows, int lanes, int most);
 // What a CTA's start and end take beyond CtaCost's tiles, in us; and what a split adds to the join.
-double token_tc_start_us(bool fp8, int lanes);
+double token_tc_start_us(bool fp8, int lanes, bool tree);
 constexpr double kTokenSplitUs = 0.25;
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s);
 // Joins the splits of the items that have several (launch_token_few does so itself).

@@ -91,11 +91,11 @@ def test_up_to_64_rows_on_e4m3_pages_keep_f16_weights(lib, rows):
 
 
 # (past, KV heads, lanes): 30 new tokens of four query heads a KV head, few keys
-SMALL_LANES = [([100] * 3, 2, 4), ([700, 3, 1300], 3, 4), ([90 + 3 * i for i in range(51)], 3, 2),
+SMALL_LANES = [([700] * 3, 2, 4), ([700, 3, 1300], 3, 4), ([90 + 3 * i for i in range(51)], 3, 2),
                ([40 * i for i in range(90)], 2, 2)]
 
 
-# bf16 pages, 8 KV heads of four query heads, 30 new tokens: what takes 128-row blocks
+# bf16 pages, 8 KV heads of four query heads, 30 new tokens: blocks of 128 rows
 @pytest.mark.parametrize("tree", [False, True], ids=["tokens", "tree"])
 @pytest.mark.parametrize("past,lanes", [([4001] * 16, 4), ([1000] * 16, 4), ([4000] * 18, 4), ([131000], 4),
                                         ([2000] * 32, 2), ([4000] * 12, 2), ([500 + 233 * i for i in range(16)], 2),
@@ -139,3 +139,25 @@ def test_33_to_64_rows_by_length(lib, streams, past, rows, fp8, few, tree):
 def test_33_to_64_rows_in_batches(lib, past, rows, heads, few):
     """Measured, few rows / matrix units: 47 / 55, 17 / 19, 7 / 10, 51 / 31 us; the last 13 there."""
     assert kinds(launches(lib, past, rows, heads, 1, False)) == ["few" if few else "tc"]
+
+
+@pytest.mark.parametrize("tree", [False, True], ids=["tokens", "tree"])
+@pytest.mark.parametrize("past,new,lanes", [([4001] * 16, 30, 4), ([131000], 30, 4), ([1000] * 16, 30, 4),
+                                            ([16000], 30, 4), ([131000], 16, 2), ([4000] * 16, 12, 2), ([2000] * 32, 30, 2),
+                                            ([500 + 233 * i for i in range(16)], 30, 2), ([300] * 64, 30, 2)], ids=str)
+def test_lanes_of_128_row_blocks_on_e4m3_pages(lib, past, new, lanes, tree):
+    """Two lanes and four: 56 / 51 us for 16 even streams of 4031 tokens with 120 rows, 97 / 91 for one of
+    131000, 86 / 91 where it has 64 rows."""
+    got = launches(lib, past, [new] * len(past), 8, 4, True, tree)
+    assert got[0] == ("tc", 1, lanes) and kinds(got) == ["tc"]
+
+
+def test_ragged_trees_on_e4m3_pages_go_together(lib):
+    """33 us in one launch, 41 in two."""
+    past = [500 + 233 * i for i in range(16)]
+    assert kinds(launches(lib, past, [1 + i * 11 // 15 for i in range(16)], 8, 4, True, True)) == ["tc"]
+
+
+def test_a_few_long_trees_take_two_lanes(lib):
+    """23 us, 24 with four."""
+    assert launches(lib, [8000] * 4, [4, 16, 8, 32], 8, 4, False, True)[0] == ("tc", 1, 2)
