@@ -87,19 +87,28 @@ struct CtaCost {
 // lengths most/1, most/2, .. the one whose waves of CTAs are estimated to end first. Returns
 // the estimate in us.
 double plan_splits(TokenAttendArgs* a, const int* first, const int* last, const CtaCost& c) {
+  // (a batch of many streams is gone through some ten times: no integer divisions in there)
+  double range[kMaxTokenBatch], pairs[kMaxTokenBatch], mean[kMaxTokenBatch];
   int most = 1;
-  for (int i = 0; i < a->n; ++i) most = std::max({most, first[i], last[i]});
+  for (int i = 0; i < a->n; ++i) {
+    most = std::max({most, first[i], last[i]});
+    range[i] = std::max(first[i], last[i]);
+    pairs[i] = (double)a->item[i].blocks * a->heads;
+    mean[i] = 0.5 * (first[i] + last[i]);
+  }
   int best = most;
   double best_t = 0;
   const auto cut = [&](int piece, double* work) {
-    double ctas = 0;
-    *work = 0;
+    // range / piece rounded up: the argument is 0.5 / piece or more from a whole number, and a product
+    // with the reciprocal is off by 2^-27 of that at most (ranges have up to 2^22 tiles)
+    const double more = piece - 0.5, inv = 1.0 / piece;
+    double ctas = 0, sum = 0;
     for (int i = 0; i < a->n; ++i) {
-      const double pairs = (double)a->item[i].blocks * a->heads;
-      const int splits = ceil_div(std::max(first[i], last[i]), piece);
-      ctas += pairs * splits;
-      *work += pairs * (0.5 * (first[i] + last[i]) + splits * (c.fixed + (splits > 1 ? c.join : 0)));
+      const int splits = (int)((range[i] + more) * inv);
+      ctas += pairs[i] * splits;
+      sum += pairs[i] * (mean[i] + splits * (c.fixed + (splits > 1 ? c.join : 0)));
     }
+    *work = sum;
     return ctas;
   };
   const auto consider = [&](int piece, double ctas, double work) {
@@ -134,7 +143,7 @@ double plan_splits(TokenAttendArgs* a, const int* first, const int* last, const 
   int cta = 0;
   for (int i = 0; i < a->n; ++i) {
     TokenQuery& t = a->item[i];
-    t.splits = std::max(1, ceil_div(std::max(first[i], last[i]), best));
+    t.splits = std::max(1, (std::max(first[i], last[i]) + best - 1) / best);
     t.cta0 = cta;
     cta += t.blocks * a->heads * t.splits;
   }
@@ -150,7 +159,7 @@ double plan_shape(pkv_t h, TokenAttendArgs* a, bool few, int shape, int lanes = 
   int first[kMaxTokenBatch], last[kMaxTokenBatch];
   for (int i = 0; i < a->n; ++i) {
     TokenQuery& it = a->item[i];
-    it.blocks = ceil_div((long long)it.n * a->group, shape);
+    it.blocks = (it.n * a->group + shape - 1) / shape;   // (fewer than 2^27 rows in all)
     const auto block_tiles = [&](int b) {
       if (a->parents) return tok_tiles(it.pos0, it.pos0 + it.n - 1, a->window, a->sinks).n;
       const int r0 = b * shape, r1 = std::min(r0 + shape, it.n * a->group) - 1;
