@@ -10,7 +10,7 @@ import torch
 
 from oracle.tokens import causal_attend_fp64
 
-from .test_gpu_token_trees import check_tree, random_parents
+from .test_gpu_token_trees import check_rotary, check_tree, random_parents, rotation
 from .test_gpu_tokens import SCALE, Pool, _built, f64, stored, tolerance   # noqa: F401 (_built: a fixture)
 from .test_token_kernels import SMALL_LANES
 
@@ -77,4 +77,28 @@ def test_up_to_64_rows_over_long_histories(past, rows, fp8):
     p.append(sids, rows)
     p.check_attend(sids, rows, 4)
     check_tree(p, sids, [random_parents(np.random.default_rng(n), n) for n in rows], 4)
+    p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("streams", [16, 17, 64, 256])
+def test_rotary_of_batches_of_many_streams(streams, fp8):
+    """A server's step: streams of 0 to 4 rows, empty ones first, between and last, so that a warp's four
+    tokens are of several streams, some of them slots that a new page's end leaves to be zeroed."""
+    rng = np.random.default_rng(streams)
+    freq, axis = rotation(32, 3)
+    p = Pool(2 * streams + 10, 16, 2, fp8, layers=2, max_streams=streams)
+    sids = [p.open(100) for _ in range(streams)]
+    p.append(sids, [(i * 7) % 19 for i in range(streams)])
+    counts = [0] + [int(rng.integers(0, 5)) for _ in range(streams - 2)] + [0]
+    positions = rng.integers(0, 3000, (sum(counts), 3))
+    for layer in range(2):
+        check_rotary(p, sids, counts, positions, freq, axis, 32, 4, layer)
+    p.check_state(sids)
+    for sid in sids[::7]:
+        n = len(p.kv[sid][0][0])
+        for layer in range(2):
+            for x, want in zip(p.cache.read_tokens(p.cache.token_batch([sid], [n]), layer=layer), p.kv[sid][layer]):
+                np.testing.assert_array_equal(f64(x), want)
+    p.check_attend(sids, [min(1, n) for n in counts], 4)
     p.cache.close()
