@@ -10,7 +10,7 @@ import torch
 
 from oracle.tokens import causal_attend_fp64
 
-from .test_gpu_token_trees import check_rotary, check_tree, random_parents, rotation
+from .test_gpu_token_trees import check_rotary, check_tree, ints, random_parents, rotation
 from .test_gpu_tokens import SCALE, Pool, _built, f64, stored, tolerance   # noqa: F401 (_built: a fixture)
 from .test_token_kernels import SMALL_LANES
 
@@ -101,4 +101,31 @@ def test_rotary_of_batches_of_many_streams(streams, fp8):
             for x, want in zip(p.cache.read_tokens(p.cache.token_batch([sid], [n]), layer=layer), p.kv[sid][layer]):
                 np.testing.assert_array_equal(f64(x), want)
     p.check_attend(sids, [min(1, n) for n in counts], 4)
+    p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("n,group", [(1, 1), (5, 4), (24, 1), (64, 1), (90, 3), (200, 2)])
+def test_a_tree_without_branches_to_a_rounding(n, group, fp8):
+    """A chain as a tree and as a draft of attend_tokens: each within the tolerance of every element, so
+    that a tile that is left out (0.05 in most outputs, 0.003 of tolerance) shows."""
+    p = Pool(100, 64, 2, fp8)
+    sid = p.open()
+    p.append([sid], [700])
+    batch = p.append([sid], [n])
+    q = p.rows(n, 2 * group)
+    chain = p.cache.attend_tokens(batch, q)
+    tree = p.cache.attend_tree(batch, q, ints(range(-1, n - 1)))
+    p.cache.sync()
+    k, v = p.kv[sid][0]
+    ref = causal_attend_fp64(f64(q), k, v, 700, 0, 0, SCALE)
+    tol = tolerance(f64(q), k, v, ref, 700, 0, 0, SCALE)
+    assert (np.abs(f64(chain) - ref) <= tol).all() and (np.abs(f64(tree) - ref) <= tol).all()
+    # (what this would miss: the last whole tile's share of the outputs)
+    hole = np.ones(len(k), dtype=bool)
+    hole[640:700 // 64 * 64 + 64] = False
+    hole[700:] = True
+    less = np.stack([causal_attend_fp64(f64(q)[i:i + 1], k[:700 + i + 1][hole[:700 + i + 1]], v[:700 + i + 1][hole[:700 + i + 1]],
+                                        int(hole[:700 + i + 1].sum()) - 1, 0, 0, SCALE)[0] for i in range(n)])
+    assert (np.abs(less - ref) > 2 * tol).mean() > 0.5
     p.cache.close()
