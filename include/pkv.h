@@ -507,8 +507,8 @@ typedef struct {
  * q_heads = 0: no q (q and q_out are not used). freq / 2 pi is kept to 2^-64 of a turn, and whole
  * turns are taken off exactly; sines, cosines and sums are fp32, and what is stored is rounded
  * once: to bf16, or, on an E4M3 cache, to the codes and exponent of the row as turned (those of
- * the exact values, but where these lie within |position| 2^-61 + 2^-48 of a border of two codes,
- * relatively). Slots, pages, layers and the rest are as in pkv_append_tokens; k must stay below
+ * the exact values, but where these lie within (|position| 2^-61 + 2^-48) (|x[a]| + |x[a + d]|) of a
+ * border of two codes). Slots, pages, layers and the rest are as in pkv_append_tokens; k must stay below
  * 2^125 in magnitude.
  * Errors: as pkv_append_tokens; INVALID for a null rotary or one outside its limits, q_heads
  * outside 0 .. 128 x heads, a q_stride that is no multiple of 8 or below a row, positions, q or

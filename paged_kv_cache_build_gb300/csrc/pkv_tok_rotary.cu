@@ -95,7 +95,7 @@ __device__ __forceinline__ uint32_t code_of(double v) {
 __device__ __forceinline__ double power_of_two(int e) { return __hiloint2double((1023 + e) << 20, 0); }
 
 // Cosine and sine of an angle of phase / 2^64 turns: whole quarters aside, their Taylor series
-// within an eighth of a turn, whose next terms are 2^-60 and less. (In place of sincospi, of which a
+// within an eighth of a turn, whose next terms are 2^-58 and less. (In place of sincospi, of which a
 // call's first use costs a microsecond, its code and constants being nowhere near.)
 __device__ __forceinline__ void turn_exactly(unsigned long long phase, double* cs, double* sn) {
   const unsigned quarter = (unsigned)((phase + (1ull << 61)) >> 62) & 3u;
