@@ -386,15 +386,20 @@ cudaError_t launch_rotary(const Args& a, const RotaryArgs& r, int blocks, int sh
 
 }  // namespace
 
-cudaError_t launch_token_append_rotary(const TokenRowsArgs& a, const RotaryArgs& r, cudaStream_t s) {
+cudaError_t launch_token_append_rotary(const TokenRowsArgs& a, const RotaryArgs& r, int num_sms, cudaStream_t s) {
   const long long quads = ((long long)a.units + kQuad - 1) / kQuad;
   const int planes = 2 * a.pool.heads + r.q_heads;
-  // Few tokens: a plane a warp. Else so many warps an SM, each with an equal share of the planes: angles
-  // cost a warp what 5 to 10 planes do, but on bf16 pages one warp's loads and products run beside
-  // another's angles (13754 tokens, 48 planes, 24 / 96 / 192 warps an SM: 31.1 / 28.7 / 35.2 us; 10992
-  // tokens on E4M3 pages 29.1 / 42 / 52 us).
-  const long long want = 152 * (a.pool.fp8 ? 24 : 96);
-  const int shares = (int)std::max<long long>(1, std::min<long long>(planes, want / quads));
+  // Equal shares of the planes for so many warps a quad. Angles cost a warp what 5 to 10 planes do, so
+  // shares have kSharePlanes of them or more, but where that leaves an SM fewer than kFewWarps warps: there
+  // latency counts (a plane a warp at the least). More warps than many_warps an SM bring nothing.
+  // (Tokens x planes on bf16 pages, with 8 / 24 / 96 warps an SM: 300 x 48 4.9 / 6.2 / 6.7 us, 1000 x 48
+  // 6.4 / 7.2 / 14.1, 3000 x 48 11.3 / 8.3 / 15.9, 10992 x 6 7.3 / 7.5 / 14.4, 13754 x 48 31.0 / 30.8 / 28.5; on
+  // E4M3 pages 8.0 / 10.5 / 10.5, 10.6 / 11.3 / 18.8, 19.5 / 14.4 / 24.6, 11.2 / 11.3 / 21.6, 43.9 / 44.1 / 51.3.)
+  constexpr int kSharePlanes = 12, kFewWarps = 8;
+  const int many_warps = a.pool.fp8 ? 24 : 96;
+  const long long few = std::min<long long>(planes, num_sms * kFewWarps / quads);
+  const long long many = std::min<long long>(planes / kSharePlanes, (long long)num_sms * many_warps / quads);
+  const int shares = (int)std::max({1ll, few, many});
   const int blocks = (int)((quads * shares + kWarps - 1) / kWarps);
   const cudaError_t e = a.n <= kSmallTokenBatch ? launch_rotary(small_args(a), r, blocks, shares, s)
                                                 : launch_rotary(a, r, blocks, shares, s);

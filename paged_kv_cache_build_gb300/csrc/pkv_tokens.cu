@@ -293,7 +293,7 @@ pkv_status append_rows(pkv_t h, int n, const int* sids, const int* row_off, int 
   if (units == 0) return PKV_OK;
   a.units = (int)units;
   cudaStream_t s = as_stream(cuda_stream);
-  PKV_CUDA(h, rotary ? launch_token_append_rotary(a, *rotary, s) : launch_token_append(a, s));
+  PKV_CUDA(h, rotary ? launch_token_append_rotary(a, *rotary, h->num_sms, s) : launch_token_append(a, s));
   if (layer == 0) {
     h->free_top -= (int)need;
     for (int i = 0; i < n; ++i)

@@ -247,7 +247,7 @@ struct TokenKeepArgsOf {
 using TokenKeepArgs = TokenKeepArgsOf<kMaxTokenBatch>;
 
 cudaError_t launch_token_append(const TokenRowsArgs& a, cudaStream_t s);
-cudaError_t launch_token_append_rotary(const TokenRowsArgs& a, const RotaryArgs& r, cudaStream_t s);
+cudaError_t launch_token_append_rotary(const TokenRowsArgs& a, const RotaryArgs& r, int num_sms, cudaStream_t s);
 cudaError_t launch_token_keep(const TokenKeepArgs& a, cudaStream_t s);
 cudaError_t launch_token_read(const TokenRowsArgs& a, cudaStream_t s);
 cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s);

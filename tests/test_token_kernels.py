@@ -161,3 +161,31 @@ def test_ragged_trees_on_e4m3_pages_go_together(lib):
 def test_a_few_long_trees_take_two_lanes(lib):
     """23 us, 24 with four."""
     assert launches(lib, [8000] * 4, [4, 16, 8, 32], 8, 4, False, True)[0] == ("tc", 1, 2)
+
+
+# (tokens, KV heads, query heads, warps a quad of tokens on bf16 and on E4M3 pages)
+SHARES = [(1, 16, 16, 48, 48), (64, 8, 32, 48, 48), (300, 8, 32, 15, 15), (1000, 8, 32, 4, 4), (1000, 2, 8, 4, 4),
+          (3000, 16, 16, 4, 4), (3000, 1, 4, 1, 1), (10992, 2, 2, 1, 1), (10992, 16, 16, 4, 1), (13754, 16, 16, 4, 1),
+          (40000, 8, 32, 1, 1), (300, 1, 0, 2, 2), (1000, 8, 0, 4, 4)]
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("tokens,heads,q_heads,bf16,e4m3", SHARES, ids=str)
+def test_warps_of_a_rotary_append(lib, tokens, heads, q_heads, bf16, e4m3, fp8):
+    """Shares of fewer than 12 planes, whose angles would take as long, only where an SM has few warps (1000
+    tokens of 48 planes: 6.4 us in four shares, 14.1 in 48)."""
+    from paged_kv_cache_build_gb300 import Rotary
+    ints = lambda x: (ctypes.c_int * len(x))(*x)  # noqa: E731
+    h, sid = ctypes.c_void_p(), ctypes.c_int()
+    create = lib.pkv_create_fp8 if fp8 else lib.pkv_create_ex
+    assert create(-(-tokens // 64), 64, heads, 64, 1, 1, ctypes.byref(h)) == OK
+    assert lib.pkv_stream_open_tokens(h, tokens, 0, 0, ctypes.byref(sid)) == OK
+    mem = ctypes.create_string_buffer(64)
+    at = (ctypes.addressof(mem) + 15) // 16 * 16
+    lib.recorded_clear()
+    assert lib.pkv_append_tokens_rotary(h, 1, ints([sid.value]), ints([0, tokens]), 0, at, at, 0, 0, at, q_heads, 0, at, at,
+                                        Rotary.sections([32]).cfg, None) == OK
+    assert lib.recorded_launches() == 1 and b"rotary" in lib.recorded_kernel(0)
+    quads = -(-(-(-tokens // 64) * 64) // 4)     # with the slots to be zeroed
+    assert lib.recorded_grid(0) == -(-quads * (e4m3 if fp8 else bf16) // 4)
+    assert lib.pkv_destroy(h) == OK
