@@ -233,12 +233,15 @@ pkv_status rotary_args(pkv_t h, const pkv_rotary* r, RotaryArgs* a) {
   return PKV_OK;
 }
 
-// An append, with or without rotation.
+pkv_status check_rows(pkv_t h, int n, const int* sids, const int* row_off) {
+  if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
+  return row_off ? PKV_OK : fail(h, PKV_ERR_INVALID, "null row_off");
+}
+
+// An append, with or without rotation (check_rows first).
 pkv_status append_rows(pkv_t h, int n, const int* sids, const int* row_off, int layer, const void* k,
                        const void* v, long long k_stride, long long v_stride, const RotaryArgs* rotary,
                        void* cuda_stream) {
-  if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
-  if (!row_off) return fail(h, PKV_ERR_INVALID, "null row_off");
   if (pkv_status r = check_layer(h, layer)) return r;
   const int row = h->H * kHeadDim;
   if (k_stride == 0) k_stride = row;
@@ -302,12 +305,10 @@ pkv_status append_rows(pkv_t h, int n, const int* sids, const int* row_off, int 
   return PKV_OK;
 }
 
-// Attention of the streams' last tokens: in a row, or (parents) as trees.
+// Attention of the streams' last tokens: in a row, or (parents) as trees (check_rows first).
 pkv_status attend_rows(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
                        const int* sids, int n, int layer, const int32_t* parents, void* out, int window,
                        int sinks, float sm_scale, void* cuda_stream) {
-  if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
-  if (!row_off) return fail(h, PKV_ERR_INVALID, "null row_off");
   if (pkv_status r = check_layer(h, layer)) return r;
   if (q_heads < 1 || q_heads % h->H != 0 || q_heads / h->H > kMaxGroup)
     return fail(h, PKV_ERR_INVALID, "q_heads %d must be 1..%d times the cache's %d heads", q_heads, kMaxGroup, h->H);
@@ -523,6 +524,7 @@ pkv_status pkv_stream_open_tokens(pkv_t h, int max_tokens, int window, int sinks
 pkv_status pkv_append_tokens(pkv_t h, int n, const int* sids, const int* row_off, int layer,
                              const void* k, const void* v, long long k_stride, long long v_stride,
                              void* cuda_stream) {
+  if (pkv_status r = check_rows(h, n, sids, row_off)) return r;
   return append_rows(h, n, sids, row_off, layer, k, v, k_stride, v_stride, nullptr, cuda_stream);
 }
 
@@ -530,8 +532,7 @@ pkv_status pkv_append_tokens_rotary(pkv_t h, int n, const int* sids, const int* 
                                     const void* k, const void* v, long long k_stride, long long v_stride,
                                     const void* q, int q_heads, long long q_stride, void* q_out,
                                     const void* positions, const pkv_rotary* rotary, void* cuda_stream) {
-  if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
-  if (!row_off) return fail(h, PKV_ERR_INVALID, "null row_off");
+  if (pkv_status r = check_rows(h, n, sids, row_off)) return r;
   RotaryArgs a;
   if (pkv_status r = rotary_args(h, rotary, &a)) return r;
   if (q_heads < 0 || q_heads > kMaxGroup * h->H)
@@ -682,6 +683,7 @@ pkv_status pkv_read_tokens(pkv_t h, int n, const int* sids, const int* pos0, con
 pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
                              const int* sids, int n, int layer, void* out, int window, int sinks,
                              float sm_scale, void* cuda_stream) {
+  if (pkv_status r = check_rows(h, n, sids, row_off)) return r;
   return attend_rows(h, q, q_heads, q_stride, row_off, sids, n, layer, nullptr, out, window, sinks, sm_scale,
                      cuda_stream);
 }
@@ -689,8 +691,7 @@ pkv_status pkv_attend_tokens(pkv_t h, const void* q, int q_heads, long long q_st
 pkv_status pkv_attend_tree(pkv_t h, const void* q, int q_heads, long long q_stride, const int* row_off,
                            const int* sids, int n, int layer, const void* parents, void* out, int window,
                            int sinks, float sm_scale, void* cuda_stream) {
-  if (pkv_status r = check_batch(h, n, sids, row_off)) return r;
-  if (!row_off) return fail(h, PKV_ERR_INVALID, "null row_off");
+  if (pkv_status r = check_rows(h, n, sids, row_off)) return r;
   if (row_off[n] > 0 && (!parents || (reinterpret_cast<uintptr_t>(parents) & 3u) != 0))
     return fail(h, PKV_ERR_INVALID, "parents must be a 4-byte aligned device pointer");
   for (int i = 0; i < n; ++i)
