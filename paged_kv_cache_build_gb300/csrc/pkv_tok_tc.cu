@@ -5,8 +5,8 @@
 //   out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),   s_j = log2(e) sm_scale q . k_j
 //
 // TREE: the rows are the nodes of drafted trees (pkv_attend_tree), with masks of their ancestors
-// in shared memory for the tiles that not every row sees whole (16 ragged streams of up to 4001
-// tokens, trees of up to 32 nodes, group 4: 25.6 us, the same rows as chains 25.3).
+// in shared memory for the tiles that not every row sees whole (16 ragged streams of up to 4250
+// tokens, 2 .. 32 nodes in one branch, group 4, in a graph: 24.6 us, without trees 22.6).
 //
 // Bounds: at head_dim 64 a 128 x 64 tile of scores takes 2 x 128 matrix-unit cycles (4096
 // multiply-adds a cycle) and 256 cycles of the SM's 32 exponentials a cycle, so neither may
