@@ -129,3 +129,30 @@ def test_a_tree_without_branches_to_a_rounding(n, group, fp8):
                                         int(hole[:700 + i + 1].sum()) - 1, 0, 0, SCALE)[0] for i in range(n)])
     assert (np.abs(less - ref) > 2 * tol).mean() > 0.5
     p.cache.close()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("past,new", [([9000, 9000, 100, 5000], [1, 60, 300, 16]), ([7000], [30]), ([20000, 3], [16, 1])], ids=str)
+def test_captured_batches_that_take_several_launches(past, new, fp8):
+    """Two kernels in turn over the same partial results, and joins, replayed among eager calls on the
+    capture's stream: the same bits each time."""
+    p = Pool(800, 64, 2, fp8)
+    sids = [p.open() for _ in past]
+    p.append(sids, past)
+    batch = p.append(sids, new)
+    q, want = p.check_attend(sids, new, 4, batch=batch)
+    stream, out = torch.cuda.Stream(), torch.empty_like(q)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        for _ in range(3):
+            p.cache.attend_tokens(batch, q, out=out)
+    for _ in range(4):
+        with torch.cuda.stream(stream):
+            out.zero_()
+            graph.replay()
+            again = p.cache.attend_tokens(batch, q)
+        stream.synchronize()
+        assert torch.equal(out, want) and torch.equal(again, want)
+    p.cache.sync()
+    p.cache.close()
