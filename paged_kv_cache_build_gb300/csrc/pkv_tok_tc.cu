@@ -721,8 +721,9 @@ double token_tc_tile_us(bool fp8, int rows, int lanes, int most) {
   if (fp8) return rows == 128 ? 0.72 : rows == 256 ? 0.79 : 1.6;
   return rows == 256 ? 1.29 : lanes == 2 ? 0.76 : 0.38;
 }
-// (Four lanes: no other CTA's products run beside a tree's walk. Trees of 30 nodes, group 4, two / four: 16
-// streams of 4031 tokens 37.0 / 33.0 us, of 1000 18.9 / 16.8, 4 of 8000 with up to 32 nodes 23.0 / 24.2.)
+
+// (Four lanes: no other CTA's products run beside a tree's walk. Trees of 30 nodes, group 4, two / four:
+// 16 streams of 4031 tokens 37.0 / 33.0 us, of 1000 18.9 / 16.8, 4 of 8000 with up to 32 nodes 23.0 / 24.2.)
 double token_tc_start_us(bool fp8, int lanes, bool tree) { return !fp8 && lanes == 4 ? (tree ? 5.5 : 3.0) : 0.0; }
 
 cudaError_t launch_token_tc(const TokenAttendArgs& a, cudaStream_t s) {

@@ -181,7 +181,8 @@ double plan_shape(pkv_t h, TokenAttendArgs* a, bool few, int shape, int lanes = 
   }
   int most = 0, splits = 1;
   for (int i = 0; i < a->n; ++i) most = std::max(most, a->item[i].n * a->group);
-  const CtaCost cost{h->num_sms * token_tc_ctas_per_sm(lanes), token_tc_tile_us(h->fp8, shape, lanes, most), 10, 4, 8, room, true};
+  const CtaCost cost{h->num_sms * token_tc_ctas_per_sm(lanes), token_tc_tile_us(h->fp8, shape, lanes, most),
+                     10, 4, 8, room, true};
   const double us = plan_splits(a, first, last, cost) + token_tc_start_us(h->fp8, lanes, a->parents != nullptr);
   for (int i = 0; i < a->n; ++i) splits = std::max(splits, a->item[i].splits);
   return splits > 1 ? us + splits * kTokenSplitUs : us;

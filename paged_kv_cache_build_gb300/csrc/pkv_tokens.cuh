@@ -252,16 +252,16 @@ cudaError_t launch_token_keep(const TokenKeepArgs& a, cudaStream_t s);
 cudaError_t launch_token_read(const TokenRowsArgs& a, cudaStream_t s);
 cudaError_t launch_token_drop(const TokenDropArgs& a, cudaStream_t s);
 
-// Attention in blocks of 8, 16 or 24 query rows (a.rows). A stream of more rows reads its keys
-// once a block, from L2 but for the first, so this kernel takes streams of at most
-// kTokenFewRowsAll rows per KV head, or of kTokenFewRows where this is estimated to end first (or
-// for f16 weights, see attend_rows). (16 streams of
-// 4001 tokens, 8 KV heads, 32 / 48 / 64 rows: 28 / 51 / 49 us on bf16 pages and 39 / 72 / 77 us on E4M3
-// pages, in launch_token_tc's blocks of 128 rows 31 / 31 / 31 and 50 / 51 / 51 us; streams of 500 .. 4001
-// tokens with 4 .. 48 / 4 .. 64 rows: 25 / 32 against 24 / 24 us, on E4M3 pages 37 / 45 against 32 / 33
-// us. One stream with 64 rows, here / there: 4000 tokens 11.1 / 12.9 us, 16000 16.9 / 16.9, 32000 26 / 24,
-// 131000 80 / 56, with 48 rows 10.9 / 12.8, 15.2 / 16.9, 22.1 / 23.5, 65 / 56; on E4M3 pages, 64 rows,
-// 14.2 / 16.5, 24.1 / 23.0, 39 / 34, 131 / 87. Four of 8000 with 48 / 64 rows 21 / 27 against 19 / 20 us.)
+// Attention in blocks of 8, 16 or 24 query rows (a.rows). A stream of more rows reads its keys once a
+// block, from L2 but for the first, so this kernel takes streams of at most kTokenFewRowsAll rows per KV
+// head, or of kTokenFewRows where this is estimated to end first (or for f16 weights, see attend_rows).
+// (16 streams of 4001 tokens, 8 KV heads, 32 / 48 / 64 rows: 28 / 51 / 49 us on bf16 pages and 39 / 72 /
+// 77 us on E4M3 pages, in launch_token_tc's blocks of 128 rows 31 / 31 / 31 and 50 / 51 / 51 us; streams
+// of 500 .. 4001 tokens with 4 .. 48 / 4 .. 64 rows: 25 / 32 against 24 / 24 us, on E4M3 pages 37 / 45
+// against 32 / 33 us. One stream with 64 rows, here / there: 4000 tokens 11.1 / 12.9 us, 16000 16.9 /
+// 16.9, 32000 26 / 24, 131000 80 / 56, with 48 rows 10.9 / 12.8, 15.2 / 16.9, 22.1 / 23.5, 65 / 56; on
+// E4M3 pages, 64 rows, 14.2 / 16.5, 24.1 / 23.0, 39 / 34, 131 / 87. Four of 8000 with 48 / 64 rows 21 /
+// 27 against 19 / 20 us.)
 constexpr int kTokenFewRows = 64;
 constexpr int kTokenFewRowsAll = 32;
 cudaError_t launch_token_few(const TokenAttendArgs& a, cudaStream_t s);
